@@ -452,6 +452,98 @@ int mla_block_hash(const void* kv_cache, int kv_dtype, int num_blocks, const int
 int mla_block_compare(const void* kv_cache, int kv_dtype, int num_blocks, const int32_t* block_a,
                       const int32_t* block_b, int n, int32_t* equal, uint32_t* dev_error, mla_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * mla_cache_append -- the rows of new tokens into the paged cache: the last
+ * step before attention can read them ("DeepSeek MLA — Prefix Cache 与 Chunked
+ * Prefill 深度解析", section 5.2, the packed row; the extend rows that
+ * mla_prefill_ctx and mla_decode find in the cache).  Row i of the n_r rows of
+ * request r becomes token t = seq_lens[r] - n_r + i of it (block
+ * block_table[r][t/64], slot t%64):
+ *   c = x[0..511] / sqrt(mean(x[0..511]^2) + norm_eps) * norm_weight
+ *       (norm_weight NULL: c = x[0..511], normalised already or not at all);
+ *   k = R(pos) x[512..575], interleaved pairs (2k, 2k+1) turned by
+ *       pos * theta^(-2k/64);
+ *   a bf16 row holds bf16(c) and bf16(k); an FP8 row E4M3(c / kv_scale),
+ *   saturated to +-448, and bf16(k).  fp32 arithmetic, each stored value
+ *   rounded once, to nearest even.
+ * The lengths and tables are read on the device, so the call can be captured
+ * into a CUDA graph that is replayed as they grow.
+ *  kv            device bf16 [rows][576], rows kv_row_stride elements apart (at
+ *                least 576, a multiple of 8: the last columns of a fused
+ *                projection's output will do), 16-byte aligned.
+ *  pos           device int32 [rows]: the position k is turned to (a token's
+ *                place in its document, where documents are cached at
+ *                canonical positions).
+ *  norm_weight   device bf16 [512], 16-byte aligned, or NULL.
+ *  cu_q          device int32 [num_reqs + 1]: ascending first rows of the
+ *                requests; NULL: every request has rows / num_reqs rows.  Rows
+ *                behind cu_q[num_reqs] are not read into the cache.
+ *  seq_lens      device int32 [num_reqs]: the requests' tokens with the new
+ *                rows.  A row whose token index is negative (a padded request
+ *                of length 0) is left out.
+ *  dev_error     device uint32, optional: bit 0 is set for a row whose block
+ *                id lies outside [0, num_blocks) or whose token lies behind
+ *                the block table (the row is not written).
+ *  kv_cache      written at those rows only; two rows of one call must not
+ *                share a cache slot (either may be found there).
+ * Errors: MLA_ERR_INVALID_ARG, MLA_ERR_CUDA.
+ * ---------------------------------------------------------------------- */
+int mla_cache_append(const void* kv, int64_t kv_row_stride, const int32_t* pos, const void* norm_weight,
+                     float norm_eps, const int32_t* cu_q, const int32_t* seq_lens, int num_reqs, int rows,
+                     const int32_t* block_table, int max_blocks_per_req, float rope_theta, void* kv_cache,
+                     int kv_dtype, float kv_scale, int num_blocks, uint32_t* dev_error, mla_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * mla_decode -- attention of one or a few new tokens per request over the
+ * paged cache, with every length on the device ("DeepSeek MLA — Prefix Cache 与
+ * Chunked Prefill 深度解析", section 3: the absorbed path for decode).  The
+ * values are those of mla_prefill_ctx with E_r = the request's rows of this
+ * call; the work is split over the keys on the device, so the call neither
+ * reads lengths on the host nor synchronises, and can be captured into a CUDA
+ * graph that is replayed while the sequences grow.
+ * Query i of the n_r rows of request r is token t = seq_lens[r] - n_r + i; it
+ * sees the keys 0 .. t that are not hidden by segments:
+ *  segments      device int64 [num_segments][3]: (start, length, rope offset)
+ *                of the relocated documents (see mla_segment), those of request
+ *                r at seg_ptr[r] .. seg_ptr[r + 1] - 1 in ascending order;
+ *                queries attend to a segment's keys with q_rope turned by
+ *                (q_pos - offset).  Keys behind the last segment's end are
+ *                attended with offset 0, keys between or before segments not
+ *                at all.  What overlaps an earlier segment or lies behind the
+ *                sequence is cut off.  NULL (with seg_ptr NULL): every key, with
+ *                offset 0.
+ *  seg_ptr       device int32 [num_reqs + 1].
+ *  q, q_pos      as mla_prefill_ctx, total_q rows.
+ *  seq_lens      device int32 [num_reqs]: the requests' tokens, the new ones
+ *                (already in the cache, see mla_cache_append) included.
+ *  cu_q          device int32 [num_reqs + 1], ascending first rows of the
+ *                requests; NULL: every request has total_q / num_reqs rows.
+ *                Rows behind cu_q[num_reqs] of out and lse are not written.
+ *  out           device [total_q, H, 128], fp32 or bf16 per out_dtype.  A row
+ *                that sees no key is 0.
+ *  lse           device fp32 [total_q, H], optional (NULL): natural log, -inf
+ *                for a row that sees no key.
+ *  workspace     device, 256-B aligned, at least mla_decode_workspace_size(...)
+ *                bytes; holds the device error word read by
+ *                mla_get_device_error().  Calls that may overlap on the GPU
+ *                must not share it.
+ *  num_heads     H in [1, 128].
+ * Rows of the cache that some query of the request sees have to be finite;
+ * others may hold anything.  A block id outside [0, num_blocks) reads as zero
+ * rows and sets the error word, as does a sequence longer than its block
+ * table, which is cut off there.
+ * Errors: MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED (H > 128),
+ * MLA_ERR_WORKSPACE, MLA_ERR_CUDA.
+ * ---------------------------------------------------------------------- */
+size_t mla_decode_workspace_size(int num_reqs, int total_q, int num_heads);
+
+int mla_decode(const void* q, const int32_t* q_pos, const void* kv_cache, int kv_dtype, float kv_scale,
+               int num_blocks, const int32_t* block_table, int max_blocks_per_req, const int32_t* seq_lens,
+               const int32_t* cu_q, int num_reqs, int total_q, int num_heads, const int64_t* segments,
+               const int32_t* seg_ptr, int num_segments, const void* kv_b_proj, float softmax_scale,
+               float rope_theta, void* out, int out_dtype, float* lse, void* workspace, size_t workspace_bytes,
+               mla_stream_t stream);
+
 /* Optional instrumentation.  With both arguments non-NULL (cudaEvent_t handles
  * created by the caller), every later mla_prefill_ctx call on this process
  * records `begin` on its stream just before its first fused prefill kernel

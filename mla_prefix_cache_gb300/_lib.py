@@ -94,6 +94,12 @@ SIGNATURES = {
                                   c_void_p, c_void_p]),
     "mla_block_hash": (c_int, [c_void_p, c_int, c_int, c_void_p, c_int, c_void_p, c_void_p, c_void_p]),
     "mla_block_compare": (c_int, [c_void_p, c_int, c_int, c_void_p, c_void_p, c_int, c_void_p, c_void_p, c_void_p]),
+    "mla_cache_append": (c_int, [c_void_p, c_int64, c_void_p, c_void_p, c_float, c_void_p, c_void_p, c_int, c_int,
+                                 c_void_p, c_int, c_float, c_void_p, c_int, c_float, c_int, c_void_p, c_void_p]),
+    "mla_decode_workspace_size": (c_size_t, [c_int, c_int, c_int]),
+    "mla_decode": (c_int, [c_void_p, c_void_p, c_void_p, c_int, c_float, c_int, c_void_p, c_int, c_void_p, c_void_p,
+                           c_int, c_int, c_int, c_void_p, c_void_p, c_int, c_void_p, c_float, c_float, c_void_p,
+                           c_int, c_void_p, c_void_p, c_size_t, c_void_p]),
     "mla_status_string": (ctypes.c_char_p, [c_int]),
     "mla_last_cuda_error": (ctypes.c_char_p, []),
     "mla_launch_count": (ctypes.c_uint64, []),

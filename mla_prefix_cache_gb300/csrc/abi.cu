@@ -15,6 +15,7 @@
 #include "absorb.h"
 #include "internal.h"
 #include "mla.h"
+#include "serving.h"
 
 namespace mla {
 
@@ -1796,6 +1797,106 @@ int mla_block_compare(const void* kv_cache, int kv_dtype, int num_blocks, const 
   return cuda_status(launch_block_compare(static_cast<const uint8_t*>(kv_cache), kv_dtype == MLA_KV_FP8_E4M3,
                                           num_blocks, block_a, block_b, n, equal, dev_error,
                                           reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// Shared validation of the serving entry points' batch description.
+static int batch_rows(const int32_t* cu_q, const int32_t* seq_lens, int num_reqs, int rows, BatchRows* b) {
+  if (num_reqs < 0 || rows < 0) return MLA_ERR_INVALID_ARG;
+  if (rows == 0) return MLA_OK;
+  if (num_reqs == 0 || seq_lens == nullptr) return MLA_ERR_INVALID_ARG;
+  if (cu_q == nullptr && rows % num_reqs != 0) return MLA_ERR_INVALID_ARG;
+  b->cu_q = cu_q;
+  b->seq_lens = seq_lens;
+  b->num_reqs = num_reqs;
+  b->rows = rows;
+  b->per_req = cu_q == nullptr ? rows / num_reqs : 0;
+  return MLA_OK;
+}
+
+static bool cache_args_ok(const void* kv_cache, int kv_dtype, float kv_scale, int num_blocks,
+                          const int32_t* block_table, int max_blocks) {
+  if (kv_dtype != MLA_KV_BF16 && kv_dtype != MLA_KV_FP8_E4M3) return false;
+  if (num_blocks <= 0 || max_blocks <= 0 || max_blocks > INT32_MAX / kBlock) return false;
+  if (kv_dtype == MLA_KV_FP8_E4M3 && !(std::isfinite(kv_scale) && kv_scale > 0.f)) return false;
+  return kv_cache != nullptr && block_table != nullptr && aligned(kv_cache, 16);
+}
+
+int mla_cache_append(const void* kv, int64_t kv_row_stride, const int32_t* pos, const void* norm_weight,
+                     float norm_eps, const int32_t* cu_q, const int32_t* seq_lens, int num_reqs, int rows,
+                     const int32_t* block_table, int max_blocks_per_req, float rope_theta, void* kv_cache,
+                     int kv_dtype, float kv_scale, int num_blocks, uint32_t* dev_error, mla_stream_t stream) {
+  AppendParams p;
+  const int st = batch_rows(cu_q, seq_lens, num_reqs, rows, &p.batch);
+  if (st != MLA_OK || rows == 0) return st;
+  if (!cache_args_ok(kv_cache, kv_dtype, kv_scale, num_blocks, block_table, max_blocks_per_req))
+    return MLA_ERR_INVALID_ARG;
+  if (!kv || !pos || !aligned(kv, 16) || kv_row_stride < kRowBf16 || kv_row_stride % 8 != 0) return MLA_ERR_INVALID_ARG;
+  if (norm_weight != nullptr && (!aligned(norm_weight, 16) || !(norm_eps >= 0.f) || !std::isfinite(norm_eps)))
+    return MLA_ERR_INVALID_ARG;
+  if (!(rope_theta > 1.f) || !std::isfinite(rope_theta)) return MLA_ERR_INVALID_ARG;
+  p.kv = static_cast<const uint16_t*>(kv);
+  p.row_stride = kv_row_stride;
+  p.pos = pos;
+  p.norm_weight = static_cast<const uint16_t*>(norm_weight);
+  p.norm_eps = norm_eps;
+  p.block_table = block_table;
+  p.max_blocks = max_blocks_per_req;
+  p.cache = static_cast<uint8_t*>(kv_cache);
+  p.num_blocks = num_blocks;
+  p.kv_scale = kv_scale;
+  p.err = dev_error;
+  rope_fracs((double)rope_theta, p.rope_frac);
+  return cuda_status(launch_cache_append(p, kv_dtype == MLA_KV_FP8_E4M3, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t mla_decode_workspace_size(int num_reqs, int total_q, int num_heads) {
+  if (num_reqs < 0 || total_q < 0 || num_heads < 1 || num_heads > kMaxHeads) return 0;
+  return 256;
+}
+
+int mla_decode(const void* q, const int32_t* q_pos, const void* kv_cache, int kv_dtype, float kv_scale,
+               int num_blocks, const int32_t* block_table, int max_blocks_per_req, const int32_t* seq_lens,
+               const int32_t* cu_q, int num_reqs, int total_q, int num_heads, const int64_t* segments,
+               const int32_t* seg_ptr, int num_segments, const void* kv_b_proj, float softmax_scale,
+               float rope_theta, void* out, int out_dtype, float* lse, void* workspace, size_t workspace_bytes,
+               mla_stream_t stream) {
+  DecodeParams p;
+  int st = batch_rows(cu_q, seq_lens, num_reqs, total_q, &p.batch);
+  if (st != MLA_OK) return st;
+  if (num_heads < 1) return MLA_ERR_INVALID_ARG;
+  if (num_heads > kMaxHeads) return MLA_ERR_UNSUPPORTED;
+  if (total_q == 0) return MLA_OK;
+  if (!cache_args_ok(kv_cache, kv_dtype, kv_scale, num_blocks, block_table, max_blocks_per_req))
+    return MLA_ERR_INVALID_ARG;
+  if (!q || !q_pos || !kv_b_proj || !out || !aligned(q, 16) || !aligned(kv_b_proj, 16) || !aligned(out, 16))
+    return MLA_ERR_INVALID_ARG;
+  if (out_dtype != MLA_OUT_FP32 && out_dtype != MLA_OUT_BF16) return MLA_ERR_INVALID_ARG;
+  if (num_segments < 0 || (segments == nullptr) != (seg_ptr == nullptr)) return MLA_ERR_INVALID_ARG;
+  if (!std::isfinite(softmax_scale) || !(rope_theta > 1.f) || !std::isfinite(rope_theta)) return MLA_ERR_INVALID_ARG;
+  if (workspace == nullptr || !aligned(workspace, 256) ||
+      workspace_bytes < mla_decode_workspace_size(num_reqs, total_q, num_heads))
+    return MLA_ERR_WORKSPACE;
+  p.q = static_cast<const uint16_t*>(q);
+  p.q_pos = q_pos;
+  p.block_table = block_table;
+  p.max_blocks = max_blocks_per_req;
+  p.cache = static_cast<const uint8_t*>(kv_cache);
+  p.num_blocks = num_blocks;
+  p.kv_scale = kv_scale;
+  p.segments = segments;
+  p.seg_ptr = seg_ptr;
+  p.num_segments = num_segments;
+  p.kv_b_proj = static_cast<const uint16_t*>(kv_b_proj);
+  p.num_heads = num_heads;
+  p.scale = softmax_scale;
+  p.out = out;
+  p.out_bf16 = out_dtype == MLA_OUT_BF16;
+  p.lse = lse;
+  p.err = static_cast<uint32_t*>(workspace);
+  rope_fracs((double)rope_theta, p.rope_frac);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if ((st = cuda_status(cudaMemsetAsync(p.err, 0, sizeof(uint32_t), s))) != MLA_OK) return st;
+  return cuda_status(launch_decode(p, kv_dtype == MLA_KV_FP8_E4M3, s));
 }
 
 }  // extern "C"
