@@ -527,13 +527,14 @@ int mla_cache_append(const void* kv, int64_t kv_row_stride, const int32_t* pos, 
  *                bytes; holds the device error word read by
  *                mla_get_device_error().  Calls that may overlap on the GPU
  *                must not share it.
+ *  softmax_scale positive.
  *  num_heads     H in [1, 128].
  * Rows of the cache that some query of the request sees have to be finite;
  * others may hold anything.  A block id outside [0, num_blocks) reads as zero
  * rows and sets the error word, as does a sequence longer than its block
  * table, which is cut off there.
- * Errors: MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED (H > 128),
- * MLA_ERR_WORKSPACE, MLA_ERR_CUDA.
+ * Errors: MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED (H > 128, a cache of more
+ * than 2^31 tokens, total_q * H above 2^31), MLA_ERR_WORKSPACE, MLA_ERR_CUDA.
  * ---------------------------------------------------------------------- */
 size_t mla_decode_workspace_size(int num_reqs, int total_q, int num_heads);
 

@@ -1849,9 +1849,28 @@ int mla_cache_append(const void* kv, int64_t kv_row_stride, const int32_t* pos, 
   return cuda_status(launch_cache_append(p, kv_dtype == MLA_KV_FP8_E4M3, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+// Workspace of mla_decode: byte offsets, 0 for sizes that it does not take.
+struct DecodeLayout {
+  size_t first, qlat, qscale, lat, lat_lse, part, part_lse, total;
+};
+static bool decode_layout(int num_reqs, int total_q, int num_heads, DecodeLayout* d) {
+  if (num_reqs < 0 || total_q < 0 || num_heads < 1 || num_heads > kMaxHeads) return false;
+  const size_t rows = (size_t)total_q * num_heads;
+  if (rows > (size_t)INT32_MAX) return false;   // TMA row coordinates
+  d->first = 256;
+  d->qlat = up256(d->first + ((size_t)num_reqs + 3) * 8);
+  d->qscale = up256(d->qlat + rows * kDc * 2);
+  d->lat = up256(d->qscale + rows * 4);
+  d->lat_lse = up256(d->lat + rows * kDc * 2);
+  d->part = up256(d->lat_lse + rows * 4);
+  d->part_lse = up256(d->part + (size_t)kDecodeSlots * kItemRows * kDc * 4);
+  d->total = up256(d->part_lse + (size_t)kDecodeSlots * kItemRows * 4);
+  return true;
+}
+
 size_t mla_decode_workspace_size(int num_reqs, int total_q, int num_heads) {
-  if (num_reqs < 0 || total_q < 0 || num_heads < 1 || num_heads > kMaxHeads) return 0;
-  return 256;
+  DecodeLayout d;
+  return decode_layout(num_reqs, total_q, num_heads, &d) ? d.total : 0;
 }
 
 int mla_decode(const void* q, const int32_t* q_pos, const void* kv_cache, int kv_dtype, float kv_scale,
@@ -1860,8 +1879,8 @@ int mla_decode(const void* q, const int32_t* q_pos, const void* kv_cache, int kv
                const int32_t* seg_ptr, int num_segments, const void* kv_b_proj, float softmax_scale,
                float rope_theta, void* out, int out_dtype, float* lse, void* workspace, size_t workspace_bytes,
                mla_stream_t stream) {
-  DecodeParams p;
-  int st = batch_rows(cu_q, seq_lens, num_reqs, total_q, &p.batch);
+  BatchRows rows;
+  int st = batch_rows(cu_q, seq_lens, num_reqs, total_q, &rows);
   if (st != MLA_OK) return st;
   if (num_heads < 1) return MLA_ERR_INVALID_ARG;
   if (num_heads > kMaxHeads) return MLA_ERR_UNSUPPORTED;
@@ -1872,31 +1891,108 @@ int mla_decode(const void* q, const int32_t* q_pos, const void* kv_cache, int kv
     return MLA_ERR_INVALID_ARG;
   if (out_dtype != MLA_OUT_FP32 && out_dtype != MLA_OUT_BF16) return MLA_ERR_INVALID_ARG;
   if (num_segments < 0 || (segments == nullptr) != (seg_ptr == nullptr)) return MLA_ERR_INVALID_ARG;
-  if (!std::isfinite(softmax_scale) || !(rope_theta > 1.f) || !std::isfinite(rope_theta)) return MLA_ERR_INVALID_ARG;
-  if (workspace == nullptr || !aligned(workspace, 256) ||
-      workspace_bytes < mla_decode_workspace_size(num_reqs, total_q, num_heads))
-    return MLA_ERR_WORKSPACE;
+  if (!(softmax_scale > 0.f) || !std::isfinite(softmax_scale) || !(rope_theta > 1.f) || !std::isfinite(rope_theta))
+    return MLA_ERR_INVALID_ARG;
+  if (num_blocks > INT32_MAX / kBlock) return MLA_ERR_UNSUPPORTED;   // TMA row coordinates
+  DecodeLayout d;
+  if (!decode_layout(num_reqs, total_q, num_heads, &d)) return MLA_ERR_UNSUPPORTED;
+  if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < d.total) return MLA_ERR_WORKSPACE;
+  const int H = num_heads;
+  const bool fp8 = kv_dtype == MLA_KV_FP8_E4M3;
+  const uint64_t n = (uint64_t)total_q * H;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  DecodeBatch batch;
+  batch.rows = rows;
+  batch.segments = segments;
+  batch.seg_ptr = seg_ptr;
+  batch.num_segments = num_segments;
+  batch.max_blocks = max_blocks_per_req;
+  batch.num_heads = H;
+  DecodeSpace space;
+  space.err = reinterpret_cast<uint32_t*>(ws);
+  space.first = reinterpret_cast<int64_t*>(ws + d.first);
+  space.qlat = ws + d.qlat;
+  space.qscale = reinterpret_cast<float*>(ws + d.qscale);
+  space.lat = reinterpret_cast<uint16_t*>(ws + d.lat);
+  space.lat_lse = reinterpret_cast<float*>(ws + d.lat_lse);
+  space.part = reinterpret_cast<float*>(ws + d.part);
+  space.part_lse = reinterpret_cast<float*>(ws + d.part_lse);
+
+  QAbsorbParams qp;
+  DecodeParams p;
+  DecodeOutParams op;
+  bool ok = true;
+  const CUtensorMapDataType bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, byte = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  {
+    // query absorption: q and the latent queries as (column, head, token), W_UK,h as rows of kv_b_proj
+    const uint64_t dq[3] = {(uint64_t)kDqk, (uint64_t)H, (uint64_t)total_q};
+    const uint64_t sq[2] = {(uint64_t)kDqk * 2, (uint64_t)H * kDqk * 2};
+    const uint32_t bq[3] = {64, 1, 128};
+    ok &= encode_map(&qp.tm_q, bf16, 3, q, dq, sq, bq, sw);
+    const uint64_t dw[2] = {(uint64_t)H * (kDnope + kDv), (uint64_t)kDc};
+    const uint64_t sww[1] = {(uint64_t)H * (kDnope + kDv) * 2};
+    const uint32_t bw[2] = {64, 256}, bo[2] = {64, 128};
+    ok &= encode_map(&qp.tm_w, bf16, 2, kv_b_proj, dw, sww, bw, sw);
+    ok &= encode_map(&op.tm_w, bf16, 2, kv_b_proj, dw, sww, bo, sw);
+    const uint64_t es = fp8 ? 1 : 2;
+    const uint64_t dl[3] = {(uint64_t)kDc, (uint64_t)H, (uint64_t)total_q};
+    const uint64_t sl[2] = {(uint64_t)kDc * es, (uint64_t)H * kDc * es};
+    const uint32_t bl[3] = {fp8 ? 128u : 64u, 1, 128};
+    ok &= encode_map(&qp.tm_out, fp8 ? byte : bf16, 3, space.qlat, dl, sl, bl, sw);
+    if (fp8) ok &= encode_map(&qp.tm_out2, byte, 3, space.qlat + n * kDc, dl, sl, bl, sw);
+  }
+  {
+    // the cache's rows in blocks of 128 B
+    const uint64_t blocks = fp8 ? 5 : 9;
+    const uint64_t dc[3] = {fp8 ? 128u : 64u, (uint64_t)num_blocks * kBlock, blocks};
+    const uint64_t sc[2] = {fp8 ? (uint64_t)kRowBytesFp8 : (uint64_t)kRowBytesBf16, 128};
+    const uint32_t bs[3] = {(uint32_t)dc[0], 64, 1};
+    const uint32_t bv[3] = {(uint32_t)dc[0], fp8 ? 64u : 32u, fp8 ? 4u : 8u};
+    ok &= encode_map(&p.tm_s, fp8 ? byte : bf16, 3, kv_cache, dc, sc, bs, sw);
+    ok &= encode_map(&p.tm_o, fp8 ? byte : bf16, 3, kv_cache, dc, sc, bv, sw);
+    const uint64_t dl[2] = {(uint64_t)kDc, n}, dp[2] = {(uint64_t)kDc, (uint64_t)kDecodeSlots * kItemRows};
+    const uint64_t sl[1] = {(uint64_t)kDc * 2}, sp[1] = {(uint64_t)kDc * 4};
+    const uint32_t bl[2] = {64, 128}, bp[2] = {32, 128};
+    ok &= encode_map(&p.tm_lat, bf16, 2, space.lat, dl, sl, bl, sw);
+    ok &= encode_map(&p.tm_part, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, space.part, dp, sp, bp, sw);
+  }
+  if (!ok) return MLA_ERR_CUDA;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+
+  qp.qscale = fp8 ? space.qscale : nullptr;
+  qp.err = space.err;
+  qp.clear = space.err;
+  qp.two = 1;
+  qp.scale = 1.f;
+  qp.row0 = 0;
+  qp.tokens = total_q;
+  qp.num_heads = H;
+  if ((st = cuda_status(launch_qabsorb(qp, s))) != MLA_OK) return st;
+
+  p.batch = batch;
+  p.ws = space;
   p.q = static_cast<const uint16_t*>(q);
   p.q_pos = q_pos;
   p.block_table = block_table;
-  p.max_blocks = max_blocks_per_req;
-  p.cache = static_cast<const uint8_t*>(kv_cache);
   p.num_blocks = num_blocks;
-  p.kv_scale = kv_scale;
-  p.segments = segments;
-  p.seg_ptr = seg_ptr;
-  p.num_segments = num_segments;
-  p.kv_b_proj = static_cast<const uint16_t*>(kv_b_proj);
-  p.num_heads = num_heads;
-  p.scale = softmax_scale;
-  p.out = out;
-  p.out_bf16 = out_dtype == MLA_OUT_BF16;
-  p.lse = lse;
-  p.err = static_cast<uint32_t*>(workspace);
+  p.kv_scale = fp8 ? kv_scale : 1.f;
+  p.scale_log2 = softmax_scale * 1.4426950408889634f;
   rope_fracs((double)rope_theta, p.rope_frac);
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if ((st = cuda_status(cudaMemsetAsync(p.err, 0, sizeof(uint32_t), s))) != MLA_OK) return st;
-  return cuda_status(launch_decode(p, kv_dtype == MLA_KV_FP8_E4M3, s));
+  cudaEvent_t ev_b = static_cast<cudaEvent_t>(g_ev_begin.load());
+  cudaEvent_t ev_e = static_cast<cudaEvent_t>(g_ev_end.load());
+  const bool timed = ev_b != nullptr && ev_e != nullptr;
+  if (timed && (st = cuda_status(cudaEventRecord(ev_b, s))) != MLA_OK) return st;
+  if ((st = cuda_status(launch_decode_attn(p, fp8, s))) != MLA_OK) return st;
+  if (timed && (st = cuda_status(cudaEventRecord(ev_e, s))) != MLA_OK) return st;
+
+  op.batch = batch;
+  op.ws = space;
+  op.out = out;
+  op.out_bf16 = out_dtype == MLA_OUT_BF16;
+  op.lse = lse;
+  op.out_scale = fp8 ? kv_scale : 1.f;
+  return cuda_status(launch_decode_out(op, s));
 }
 
 }  // extern "C"

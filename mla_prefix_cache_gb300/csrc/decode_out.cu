@@ -1,0 +1,283 @@
+// Last step of decode attention: the states that several clusters left of a
+// row's keys are joined, and every row goes through W_UV of its head,
+//   w_i = e^{lse_i - m} / sum_j e^{lse_j - m},  o = sum_i w_i o_i,  lse = m + ln sum_j e^{lse_j - m}
+//   out[t][h] = out_scale o W_UV,h
+// A CTA takes 128 tokens of one head.  Its warps join the fp32 states of their
+// rows (few rows: several warps a row, each some of the pieces), or take the
+// bf16 state that one cluster left, into one K-major swizzled operand of 512
+// columns; W_UV,h comes by TMA in four chunks of 128 rows, two buffers deep,
+// and one chain of M = 128, N = 128 MMAs makes the 128 output columns.  o is
+// rounded to bf16 for the product, once, after the join.
+#include "serving.cuh"
+
+namespace mla {
+namespace {
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr uint32_t kBlk = 16384;                   // [128 rows x 128 B] swizzled block
+constexpr uint32_t kA = 0;                         // 8 blocks of 64 columns
+constexpr uint32_t kB = 8 * kBlk;                  // 2 buffers of [128 c x 128 j] in two blocks
+constexpr uint32_t kRed = kB + 4 * kBlk;           // [8 warps][512] fp32: partial joins of few rows
+constexpr uint32_t kRows = kRed + kWarps * kDc * 4;
+constexpr uint32_t kBars = kRows + 128 * 24;       // B landed x 2, buffer's MMAs done x 2, TMEM address
+constexpr uint32_t kSmem = kBars + 48;
+static_assert(kSmem <= 232448, "more than 227 KB of shared memory per CTA");
+constexpr uint32_t kIdesc = idesc_bf16(128, 128, false, true);
+constexpr int kMaxPieces = kDecodeClusters;        // of one item
+
+struct RowOf {
+  int64_t x;       // unit of the item's first tile
+  int n;           // pieces: -1 no request's row, 0 no keys, 1 a whole item
+  int c0;          // cluster of the first piece
+  int ridx;        // row within the item
+  float lse;
+};
+static_assert(sizeof(RowOf) == 24, "row table");
+
+__device__ __forceinline__ bool wait(uint32_t* err, uint32_t bar, uint32_t parity) {
+  if (mbar_wait(bar, parity)) return true;
+  atomicOr(err, kErrTimeout);
+  return false;
+}
+
+// Request of row x by one thread (ascending cu_q).
+__device__ __forceinline__ int find_request(const BatchRows& b, int x) {
+  if (b.cu_q == nullptr) return x / b.per_req;
+  int lo = 0, hi = b.num_reqs - 1;   // the last request that starts at or before x
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (__ldg(b.cu_q + mid) <= x) lo = mid; else hi = mid - 1;
+  }
+  const int2 rr = request_rows(b, lo);
+  return x >= rr.x && x < rr.y ? lo : -1;
+}
+
+// 4 columns 4 lane + 128 k of row i as bf16 into the operand.
+__device__ __forceinline__ void put4(uint32_t a, int i, int lane, int k, float4 v) {
+  const int c = 4 * lane + 128 * k;
+  const uint32_t addr = a + (uint32_t)(c >> 6) * kBlk + sw128_off((uint32_t)i, (uint32_t)((c & 63) >> 3)) + (c & 4) * 2;
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(pack_bf16(v.x, v.y)), "r"(pack_bf16(v.z, v.w)) : "memory");
+}
+
+__global__ void __launch_bounds__(kThreads, 1) decode_out_kernel(const __grid_constant__ DecodeOutParams p) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sb = smem_u32(smem);
+  const uint32_t bars = sb + kBars;
+  RowOf* rows = reinterpret_cast<RowOf*>(smem + kRows);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kBars + 32);
+  float* red = reinterpret_cast<float*>(smem + kRed);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int H = p.batch.num_heads, h = blockIdx.z, r0 = blockIdx.x * 128;
+  const int R = min(128, p.batch.rows.rows - r0);
+
+  auto load_w = [&](int ch) {
+    const uint32_t b = ch & 1, dst = sb + kB + b * 2 * kBlk;
+    mbar_arrive_expect_tx(bars + 8 * b, 2 * kBlk);
+    tma_load_2d(dst, &p.tm_w, 128 * H + 128 * h, 128 * ch, bars + 8 * b);
+    tma_load_2d(dst + kBlk, &p.tm_w, 128 * H + 128 * h + 64, 128 * ch, bars + 8 * b);
+  };
+  if (tid == 0) {
+    prefetch_tensormap(&p.tm_w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mbar_init(bars + 8 * i, 1);
+    fence_mbar_init();
+    load_w(0);
+    load_w(1);
+  }
+  if (warp == 0) {
+    __syncwarp();
+    tmem_alloc(smem_u32(tmem_slot), 128);
+    tmem_relinquish();
+  }
+  const int B = p.batch.rows.num_reqs;
+  const int64_t total = p.ws.first[B + 1], n_clusters = p.ws.first[B + 2];
+  if (tid < R) {
+    RowOf o;
+    o.n = -1;
+    o.c0 = o.ridx = 0;
+    o.x = 0;
+    o.lse = -INFINITY;
+    const int r = find_request(p.batch.rows, r0 + tid);
+    if (r >= 0) {
+      const int2 rr = request_rows(p.batch.rows, r);
+      const int64_t f = p.ws.first[r];
+      const int items = ((rr.y - rr.x) * H + kItemRows - 1) / kItemRows;
+      const int64_t u = (p.ws.first[r + 1] - f) / items;
+      const int idx = (r0 + tid - rr.x) * H + h;
+      o.ridx = idx & (kItemRows - 1);
+      o.n = 0;
+      if (u > 0) {
+        o.x = f + (idx / kItemRows) * u + kItemUnits;
+        o.c0 = cluster_of(o.x, n_clusters, total);
+        o.n = cluster_of(o.x + u - kItemUnits - 1, n_clusters, total) - o.c0 + 1;
+      }
+    }
+    rows[tid] = o;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  // ---------------------------------------------------------------- the rows' states
+  const int G = R <= 1 ? 8 : R <= 2 ? 4 : R <= 4 ? 2 : 1;   // warps a row
+  for (int i = warp / G; i < R; i += kWarps / G) {
+    const RowOf o = rows[i];
+    const int64_t orow = (int64_t)(r0 + i) * H + h;
+    const int part = warp % G;
+    if (o.n == 1) {
+      if (part == 0) {
+        const uint4* src = reinterpret_cast<const uint4*>(p.ws.lat + orow * kDc);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int c = lane + 32 * k;   // 16-byte chunk of the row
+          const uint4 v = src[c];
+          sts128(sb + kA + (uint32_t)(c >> 3) * kBlk + sw128_off((uint32_t)i, (uint32_t)(c & 7)), v.x, v.y, v.z, v.w);
+        }
+        if (lane == 0) rows[i].lse = p.ws.lat_lse[orow];
+      }
+      continue;
+    }
+    float4 acc[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (o.n > 1) {
+      // lane l has the weights of pieces l, l + 32, l + 64
+      constexpr int kPerLane = (kMaxPieces + 31) / 32;
+      float w[kPerLane], m = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < kPerLane; ++k) {
+        const int i2 = lane + 32 * k;
+        w[k] = i2 < o.n ? p.ws.part_lse[piece_slot(o.c0 + i2, o.x, n_clusters, total) * kItemRows + o.ridx] : -INFINITY;
+        m = fmaxf(m, w[k]);
+      }
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+      float sum = 0.f;
+#pragma unroll
+      for (int k = 0; k < kPerLane; ++k) {
+        w[k] = m == -INFINITY ? 0.f : __expf(w[k] - m);
+        sum += w[k];
+      }
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      if (part == 0 && lane == 0) rows[i].lse = sum > 0.f ? m + __logf(sum) : -INFINITY;
+#pragma unroll
+      for (int k = 0; k < kPerLane; ++k) {
+        if (32 * k >= o.n) break;
+        const int last = min(32, o.n - 32 * k);
+        const int step = G;
+#pragma unroll 4
+        for (int l = part; l < last; l += step) {
+          const float wi = __shfl_sync(0xffffffffu, w[k], l) * inv;
+          const int slot = piece_slot(o.c0 + 32 * k + l, o.x, n_clusters, total);
+          const float4* src = reinterpret_cast<const float4*>(p.ws.part + ((int64_t)slot * kItemRows + o.ridx) * kDc) + lane;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float4 v = src[32 * q];
+            acc[q].x = fmaf(wi, v.x, acc[q].x);
+            acc[q].y = fmaf(wi, v.y, acc[q].y);
+            acc[q].z = fmaf(wi, v.z, acc[q].z);
+            acc[q].w = fmaf(wi, v.w, acc[q].w);
+          }
+        }
+      }
+    }
+    if (G == 1) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) put4(sb + kA, i, lane, k, acc[k]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) reinterpret_cast<float4*>(red + warp * kDc)[lane + 32 * k] = acc[k];
+    }
+  }
+  if (G > 1) {
+    __syncthreads();
+    if (warp < R && rows[warp].n != 1) {   // warp i sums row i's parts
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int g = 0; g < G; ++g) {
+          const float4 v = reinterpret_cast<const float4*>(red + (warp * G + g) * kDc)[lane + 32 * k];
+          s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+        }
+        put4(sb + kA, warp, lane, k, s);
+      }
+    }
+  }
+  fence_proxy_async_smem();
+  __syncthreads();
+
+  // ---------------------------------------------------------------- out = o W_UV,h
+  bool ok = true;
+  if (tid == 0) {
+    for (int ch = 0; ch < 4 && ok; ++ch) {
+      const uint32_t b = ch & 1;
+      ok = wait(p.ws.err, bars + 8 * b, (ch >> 1) & 1);
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk)
+        mma_bf16(tmem, sdesc_sw128(sb + kA + (2 * ch + (kk >> 2)) * kBlk + (kk & 3) * 32, 16, 1024),
+                 sdesc_sw128(sb + kB + b * 2 * kBlk + kk * 2048, kBlk, 1024), kIdesc, (ch | kk) ? 1u : 0u);
+      mma_commit(bars + 16 + 8 * b);
+      if (ch < 2) {
+        ok = wait(p.ws.err, bars + 16 + 8 * b, 0);
+        if (ok) load_w(ch + 2);
+      }
+    }
+  }
+  ok = __syncthreads_and(ok);
+  if (ok) ok = __all_sync(0xffffffffu, wait(p.ws.err, bars + 16, 1) && wait(p.ws.err, bars + 24, 1));
+  tc_fence_after();
+  if (ok) {
+    // warps w and w + 4 share TMEM lanes 32 (w mod 4) ..: columns 64 (w / 4) .. + 63
+    const int i = 32 * (warp & 3) + lane, cb = 64 * (warp >> 2);
+    uint32_t v[64];
+    tmem_ld64(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + cb, v);
+    if (i < R && rows[i].n >= 0) {
+      const int64_t orow = (int64_t)(r0 + i) * H + h, o = orow * kDv + cb;
+      const bool empty = rows[i].lse == -INFINITY;   // no key seen: 0
+#pragma unroll
+      for (int k = 0; k < 64; ++k) v[k] = empty ? 0u : __float_as_uint(__uint_as_float(v[k]) * p.out_scale);
+      if (p.out_bf16) {
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + o);
+        auto o2 = [&](int k) { return pack_bf16(__uint_as_float(v[k]), __uint_as_float(v[k + 1])); };
+#pragma unroll
+        for (int k = 0; k < 8; ++k) dst[k] = make_uint4(o2(8 * k), o2(8 * k + 2), o2(8 * k + 4), o2(8 * k + 6));
+      } else {
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<float*>(p.out) + o);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) dst[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+      }
+      if (p.lse != nullptr && warp < 4) p.lse[orow] = rows[i].lse;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 128);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_decode_out(const DecodeOutParams& p, cudaStream_t s) {
+  static int configured = -1;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (configured != dev) {
+    e = cudaFuncSetAttribute(decode_out_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    if (e != cudaSuccess) return e;
+    configured = dev;
+  }
+  const dim3 grid((p.batch.rows.rows + 127) / 128, 1, p.batch.num_heads);
+  decode_out_kernel<<<grid, kThreads, kSmem, s>>>(p);
+  count_launch();
+  return cudaGetLastError();
+}
+
+}  // namespace mla

@@ -1,8 +1,9 @@
 // The two per-head projections of the absorbed (latent-space) path ("DeepSeek
 // MLA — Prefix Cache 与 Chunked Prefill 深度解析", section 3: W_UK folded into
 // the query, W_UV applied after the attention), on the tensor cores:
-//   qabsorb_kernel<false>  qlat[t][h][:]  = bf16(scale q_nope[t][h] W_UK,h^T)   [512]
-//   qabsorb_kernel<true>   qlat8[t][h][:] = e4m3(qlat / s), s = amax / 448 of the row
+//   qabsorb_kernel<kBf16>  qlat[t][h][:]  = bf16(scale q_nope[t][h] W_UK,h^T)   [512]
+//   qabsorb_kernel<kE4m3>  qlat8[t][h][:] = e4m3(qlat / s), s = amax / 448 of the row
+//   qabsorb_kernel<kTwoE4m3>  the same, and e4m3(qlat / s - qlat8)
 //   absorb_proj_kernel     out[t][h][:]   = scale o[t H + h] W_UV,h             [128]
 // Both are one tcgen05 MMA chain per CTA (M = 128 rows of one head), operands
 // staged in shared memory with 128-byte swizzle, the accumulator in TMEM.
@@ -31,8 +32,11 @@ __device__ __forceinline__ bool hwait(uint32_t* err, uint32_t bar, uint32_t pari
 // Shared memory: A = q_nope [128 x 128] as two [128 x 64] blocks, then B = the
 // CTA's rows of W_UK,h as [256 c x 64 d] blocks (d block, c half); after the
 // MMAs the same memory stages the output rows for the TMA stores.
-template <bool kF8>
+enum QaForm { kBf16, kE4m3, kTwoE4m3 };
+
+template <int kForm>
 struct QA {
+  static constexpr bool kF8 = kForm != kBf16;
   static constexpr int kCols = kF8 ? 512 : 256;           // latent columns of a CTA
   static constexpr int kHalves = kCols / 256;
   static constexpr uint32_t kA = 0;
@@ -43,9 +47,10 @@ struct QA {
 };
 constexpr uint32_t kIdescQA = idesc_bf16(128, 256, false, false);
 
-template <bool kF8>
+template <int kForm>
 __global__ void __launch_bounds__(128, 1) qabsorb_kernel(const __grid_constant__ QAbsorbParams p) {
-  using L = QA<kF8>;
+  using L = QA<kForm>;
+  constexpr bool kF8 = L::kF8;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* sgen = smem_raw + (sbase - smem_u32(smem_raw));
@@ -57,6 +62,7 @@ __global__ void __launch_bounds__(128, 1) qabsorb_kernel(const __grid_constant__
   const int t0 = p.row0 + blockIdx.x * 128;   // first token of the tile (TMA coordinates)
 
   if (threadIdx.x == 0) {
+    if (p.clear != nullptr && (blockIdx.x | blockIdx.y | blockIdx.z) == 0) *p.clear = 0u;
     mbar_init(bar_full, 1);
     mbar_init(bar_done, 1);
     fence_mbar_init();
@@ -126,7 +132,8 @@ __global__ void __launch_bounds__(128, 1) qabsorb_kernel(const __grid_constant__
 #pragma unroll
         for (int i = 0; i < 32; ++i) m = fmaxf(m, fabsf(__uint_as_float(v[i])));
       }
-      const float sc = m > 0.f ? m / 448.f : 1.f;
+      // two terms: the scale is kept where q_rope can still be divided by it
+      const float sc = kForm == kTwoE4m3 ? fmaxf(m / 448.f, 1e-18f) : (m > 0.f ? m / 448.f : 1.f);
       const float inv = 1.f / sc;
       // 32 columns a load: 32 B of E4M3 = two 16-byte chunks of a [128 x 128 B] block
 #pragma unroll 1
@@ -136,14 +143,24 @@ __global__ void __launch_bounds__(128, 1) qabsorb_kernel(const __grid_constant__
         const uint32_t blk = sbase + (j >> 2) * kAtomRows128;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          uint32_t w[4];
+          uint32_t w[4], w2[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int k = 16 * c + 4 * i;
-            w[i] = (uint32_t)pack_e4m3x2(__uint_as_float(v[k]) * inv, __uint_as_float(v[k + 1]) * inv) |
-                   ((uint32_t)pack_e4m3x2(__uint_as_float(v[k + 2]) * inv, __uint_as_float(v[k + 3]) * inv) << 16);
+            float x[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = __uint_as_float(v[k + e]) * inv;
+            const uint32_t lo = pack_e4m3x2(x[0], x[1]), hi = pack_e4m3x2(x[2], x[3]);
+            w[i] = lo | (hi << 16);
+            if constexpr (kForm == kTwoE4m3) {
+              const float2 fl = e4m3x2_floats(lo), fh = e4m3x2_floats(hi);   // exact, and so are the differences
+              w2[i] = (uint32_t)pack_e4m3x2(x[0] - fl.x, x[1] - fl.y) |
+                      ((uint32_t)pack_e4m3x2(x[2] - fh.x, x[3] - fh.y) << 16);
+            }
           }
           sts128(blk + sw128_off(r, (j & 3) * 2 + c), w[0], w[1], w[2], w[3]);
+          if constexpr (kForm == kTwoE4m3)
+            sts128(blk + 4 * kAtomRows128 + sw128_off(r, (j & 3) * 2 + c), w2[0], w2[1], w2[2], w2[3]);
         }
       }
       const int t = t0 + r;
@@ -157,6 +174,10 @@ __global__ void __launch_bounds__(128, 1) qabsorb_kernel(const __grid_constant__
     // rows past the launch's last token are clipped by the map
 #pragma unroll
     for (int b = 0; b < 4; ++b) tma_store_3d(&p.tm_out, sbase + b * kAtomRows128, c0 + (kF8 ? 128 : 64) * b, h, t0);
+    if constexpr (kForm == kTwoE4m3) {
+#pragma unroll
+      for (int b = 0; b < 4; ++b) tma_store_3d(&p.tm_out2, sbase + (4 + b) * kAtomRows128, 128 * b, h, t0);
+    }
     bulk_commit();
     bulk_wait0();
   }
@@ -312,8 +333,9 @@ cudaError_t configure_headproj() {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess || configured_device == dev) return e;
-  e = set_smem(qabsorb_kernel<false>, QA<false>::kSmem);
-  if (e == cudaSuccess) e = set_smem(qabsorb_kernel<true>, QA<true>::kSmem);
+  e = set_smem(qabsorb_kernel<kBf16>, QA<kBf16>::kSmem);
+  if (e == cudaSuccess) e = set_smem(qabsorb_kernel<kE4m3>, QA<kE4m3>::kSmem);
+  if (e == cudaSuccess) e = set_smem(qabsorb_kernel<kTwoE4m3>, QA<kTwoE4m3>::kSmem);
   if (e == cudaSuccess) e = set_smem(absorb_proj_kernel, kPSmem);
   if (e == cudaSuccess) configured_device = dev;
   return e;
@@ -327,8 +349,9 @@ cudaError_t launch_qabsorb(const QAbsorbParams& p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const bool f8 = p.qscale != nullptr;
   const dim3 grid((p.tokens + 127) / 128, f8 ? 1 : kDc / 256, p.num_heads);
-  if (f8) qabsorb_kernel<true><<<grid, 128, QA<true>::kSmem, s>>>(p);
-  else qabsorb_kernel<false><<<grid, 128, QA<false>::kSmem, s>>>(p);
+  if (f8 && p.two) qabsorb_kernel<kTwoE4m3><<<grid, 128, QA<kTwoE4m3>::kSmem, s>>>(p);
+  else if (f8) qabsorb_kernel<kE4m3><<<grid, 128, QA<kE4m3>::kSmem, s>>>(p);
+  else qabsorb_kernel<kBf16><<<grid, 128, QA<kBf16>::kSmem, s>>>(p);
   count_launch();
   return cudaGetLastError();
 }

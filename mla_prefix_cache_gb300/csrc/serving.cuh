@@ -33,19 +33,6 @@ __device__ __forceinline__ int request_of_row(const BatchRows& b, int row, int l
   return row >= rr.x && row < rr.y ? lo : -1;
 }
 
-// Two E4M3 codes (low 16 bits) to floats, exactly.
-__device__ __forceinline__ float2 e4m3x2_floats(uint32_t pair) {
-  float2 f;
-  asm("{\n\t.reg .b16 in, l, h;\n\t.reg .b32 hx;\n\t"
-      "cvt.u16.u32 in, %2;\n\t"
-      "cvt.rn.f16x2.e4m3x2 hx, in;\n\t"
-      "mov.b32 {l, h}, hx;\n\t"
-      "cvt.f32.f16 %0, l;\n\t"
-      "cvt.f32.f16 %1, h;\n\t}"
-      : "=f"(f.x), "=f"(f.y) : "r"(pair));
-  return f;
-}
-
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
@@ -56,14 +43,14 @@ struct KeyRange {
 };
 // Ranges of a request: its segments in order, then the keys behind the last
 // segment's end (offset 0).
-__device__ __forceinline__ int2 request_segments(const DecodeParams& p, int r) {
-  if (p.segments == nullptr) return make_int2(0, 0);
-  const int lo = min(max(__ldg(p.seg_ptr + r), 0), p.num_segments);
-  return make_int2(lo, min(max(__ldg(p.seg_ptr + r + 1), lo), p.num_segments));
+__device__ __forceinline__ int2 request_segments(const DecodeBatch& b, int r) {
+  if (b.segments == nullptr) return make_int2(0, 0);
+  const int lo = min(max(__ldg(b.seg_ptr + r), 0), b.num_segments);
+  return make_int2(lo, min(max(__ldg(b.seg_ptr + r + 1), lo), b.num_segments));
 }
 // Range i of [sg.x, sg.y] (i == sg.y: the tail, from `end` on), clamped to
 // [end, len): a segment never reaches back over the ones before it.
-__device__ __forceinline__ KeyRange request_range(const DecodeParams& p, int2 sg, int i, int end, int len) {
+__device__ __forceinline__ KeyRange request_range(const DecodeBatch& b, int2 sg, int i, int end, int len) {
   KeyRange k;
   if (i >= sg.y) {
     k.lo = min(end, len);
@@ -71,13 +58,55 @@ __device__ __forceinline__ KeyRange request_range(const DecodeParams& p, int2 sg
     k.offset = 0;
     return k;
   }
-  const int64_t s = __ldg(p.segments + 3 * (int64_t)i), n = __ldg(p.segments + 3 * (int64_t)i + 1);
-  k.offset = __ldg(p.segments + 3 * (int64_t)i + 2);
+  const int64_t s = __ldg(b.segments + 3 * (int64_t)i), n = __ldg(b.segments + 3 * (int64_t)i + 1);
+  k.offset = __ldg(b.segments + 3 * (int64_t)i + 2);
   const int64_t lo = s < end ? (int64_t)end : s;
-  const int64_t e = n <= 0 ? lo : (n > (int64_t)len - s ? (int64_t)len : s + n);   // no overflow for any s, n
+  const int64_t e = n <= 0 ? lo : (n > (int64_t)len - s ? (int64_t)len : s + n);   // no overflow for any n
   k.lo = (int)(lo < len ? lo : len);
   k.hi = (int)(e < k.lo ? k.lo : e);
   return k;
+}
+// 128-key tiles of a range: they start at the cache block that holds its first key.
+__device__ __forceinline__ int range_tiles(const KeyRange& k) {
+  return k.hi > k.lo ? (k.hi - (k.lo & ~(kBlock - 1)) + 127) >> 7 : 0;
+}
+
+// A request's share of the decode work.  Its rows (token * H + head) form items
+// of 128 rows; an item has `tiles` key tiles and counts `units` = tiles +
+// kItemUnits in the schedule (none if it has no keys).
+constexpr int kItemUnits = 2;   // an item's start and end cost about as much as this many tiles
+struct RequestWork {
+  int q_begin, q_count, len, tiles, items;
+  int2 sg;
+  __device__ __forceinline__ int units() const { return tiles > 0 ? tiles + kItemUnits : 0; }
+};
+__device__ __forceinline__ RequestWork request_work(const DecodeBatch& b, int r) {
+  RequestWork w;
+  const int2 rr = request_rows(b.rows, r);
+  w.q_begin = rr.x;
+  w.q_count = rr.y - rr.x;
+  w.len = min(max(__ldg(b.rows.seq_lens + r), 0), b.max_blocks * kBlock);
+  w.sg = request_segments(b, r);
+  w.items = (w.q_count * b.num_heads + kItemRows - 1) / kItemRows;
+  w.tiles = 0;
+  int end = 0;
+  for (int g = w.sg.x; g <= w.sg.y; ++g) {
+    const KeyRange k = request_range(b, w.sg, g, end, w.len);
+    end = k.hi;
+    w.tiles += range_tiles(k);
+  }
+  return w;
+}
+
+// The units [0, total) of the batch are cut evenly: cluster c of n has
+// [unit_begin(c), unit_begin(c + 1)); cluster_of(x) is the one that has unit x.
+__device__ __forceinline__ int64_t unit_begin(int64_t c, int64_t n, int64_t total) { return c * total / n; }
+__device__ __forceinline__ int cluster_of(int64_t x, int64_t n, int64_t total) { return (int)(((x + 1) * n - 1) / total); }
+// The slot of the state that cluster c has of an item whose first tile is unit
+// x: each cluster shares one item with the clusters before it at most, and one
+// with those after it.
+__device__ __forceinline__ int piece_slot(int c, int64_t x, int64_t n, int64_t total) {
+  return 2 * c + (unit_begin(c, n, total) <= x ? 1 : 0);
 }
 
 }  // namespace mla

@@ -34,27 +34,63 @@ struct AppendParams {
 };
 cudaError_t launch_cache_append(const AppendParams& p, bool fp8, cudaStream_t s);
 
+// The decode attention's clusters (two CTAs each): the persistent grid of a
+// GB300's 152 SMs.  Each has two slots for the states of pieces that it shares
+// with its neighbours.
+constexpr int kDecodeClusters = 76;
+constexpr int kDecodeSlots = 2 * kDecodeClusters;
+constexpr int kItemRows = 128;   // (token, head) rows of a work item
+
+// What both kernels know of the batch's work.
+struct DecodeBatch {
+  BatchRows rows;
+  const int64_t* segments;   // optional [..][3]: start, length, rope offset
+  const int32_t* seg_ptr;    // [num_reqs + 1]
+  int num_segments;
+  int max_blocks;
+  int num_heads;
+};
+
+// Latent attention (decode.cu).  Workspace arrays:
+struct DecodeSpace {
+  uint32_t* err;
+  int64_t* first;        // [num_reqs + 1]: the requests' first work units, then two more: units in all, clusters used
+  uint8_t* qlat;         // bf16 [rows * H][512], or E4M3 [2][rows * H][512]
+  float* qscale;         // [rows * H]: the E4M3 rows' scales
+  uint16_t* lat;         // bf16 [rows * H][512]: states of rows whose keys one cluster had
+  float* lat_lse;        // [rows * H]
+  float* part;           // [kDecodeSlots][128][512]: states of shared rows
+  float* part_lse;       // [kDecodeSlots][128]
+};
+
 struct DecodeParams {
+  CUtensorMap tm_s;      // the cache's rows in blocks of 128 B, box 128 B x 64 rows x 1
+  CUtensorMap tm_o;      // the same, box 128 B x 32 rows x 8 (bf16) or 128 B x 64 rows x 4 (FP8)
+  CUtensorMap tm_lat;    // lat as [rows * H][512], box 64 x 128
+  CUtensorMap tm_part;   // part as [kDecodeSlots * 128][512], box 32 x 128
+  DecodeBatch batch;
+  DecodeSpace ws;
   const uint16_t* q;             // [rows][H][192], q_rope not rotated
   const int32_t* q_pos;          // [rows]
-  BatchRows batch;
   const int32_t* block_table;    // [num_reqs][max_blocks]
-  int max_blocks;
-  const uint8_t* cache;
   int num_blocks;
-  float kv_scale;
-  const int64_t* segments;       // optional [..][3]: start, length, rope offset
-  const int32_t* seg_ptr;        // [num_reqs + 1]
-  int num_segments;
-  const uint16_t* kv_b_proj;     // [512][H * 256]
-  int num_heads;
-  float scale;
-  void* out;                     // [rows][H][128]
-  int out_bf16;
-  float* lse;                    // optional [rows][H]
-  uint32_t* err;
+  float kv_scale;                // 1 for bf16 rows
+  float scale_log2;
   uint64_t rope_frac[kDr / 2];
 };
-cudaError_t launch_decode(const DecodeParams& p, bool fp8, cudaStream_t s);
+cudaError_t launch_decode_attn(const DecodeParams& p, bool fp8, cudaStream_t s);
+
+// Joining of the pieces' states and the output projection (decode_out.cu):
+// out[t][h] = out_scale sum_pieces w o W_UV,h, lse[t][h].
+struct DecodeOutParams {
+  CUtensorMap tm_w;      // kv_b_proj as [512][H * 256], box 64 x 128
+  DecodeBatch batch;
+  DecodeSpace ws;
+  void* out;             // [rows][H][128]
+  int out_bf16;
+  float* lse;            // optional [rows][H]
+  float out_scale;
+};
+cudaError_t launch_decode_out(const DecodeOutParams& p, cudaStream_t s);
 
 }  // namespace mla

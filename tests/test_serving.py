@@ -214,7 +214,7 @@ def test_decode_validates_without_gpu(lib):
                               od, None, ws, wb, None)
     bad = [dict(q=None), dict(q=ctypes.c_void_p(4104)), dict(pos=None), dict(cache=None), dict(kvt=5), dict(nb=0),
            dict(bt=None), dict(mb=0), dict(sl=None), dict(cu=None), dict(B=0), dict(B=-2), dict(T=-1), dict(H=0),
-           dict(sg=d), dict(sp=d), dict(ns=-1), dict(w=None), dict(w=ctypes.c_void_p(4098)), dict(sm=float("nan")),
+           dict(sg=d), dict(sp=d), dict(ns=-1), dict(w=None), dict(w=ctypes.c_void_p(4098)), dict(sm=float("nan")), dict(sm=0.0), dict(sm=-0.1),
            dict(theta=0.5), dict(out=None), dict(out=ctypes.c_void_p(4104)), dict(od=2), dict(kvt=1, scale=-1.0)]
     for b in bad:
         assert call(**b) == _lib.MLA_ERR_INVALID_ARG, b
