@@ -533,8 +533,10 @@ int mla_cache_append(const void* kv, int64_t kv_row_stride, const int32_t* pos, 
  * others may hold anything.  A block id outside [0, num_blocks) reads as zero
  * rows and sets the error word, as does a sequence longer than its block
  * table, which is cut off there.
- * Errors: MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED (H > 128, a cache of more
- * than 2^31 tokens, total_q * H above 2^31), MLA_ERR_WORKSPACE, MLA_ERR_CUDA.
+ * Errors: MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED (H > 128, a cache of 2^31
+ * tokens or more, total_q * H of 2^30 or more, a batch whose block table and
+ * segments could hold 2^31 or more pairs of 128 rows and 128 keys),
+ * MLA_ERR_WORKSPACE, MLA_ERR_CUDA.
  * ---------------------------------------------------------------------- */
 size_t mla_decode_workspace_size(int num_reqs, int total_q, int num_heads);
 

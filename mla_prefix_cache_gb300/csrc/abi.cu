@@ -1856,9 +1856,9 @@ struct DecodeLayout {
 static bool decode_layout(int num_reqs, int total_q, int num_heads, DecodeLayout* d) {
   if (num_reqs < 0 || total_q < 0 || num_heads < 1 || num_heads > kMaxHeads) return false;
   const size_t rows = (size_t)total_q * num_heads;
-  if (rows > (size_t)INT32_MAX) return false;   // TMA row coordinates
+  if (rows > (size_t)INT32_MAX / 2) return false;   // TMA row coordinates
   d->first = 256;
-  d->qlat = up256(d->first + ((size_t)num_reqs + 3) * 8);
+  d->qlat = up256(d->first + ((size_t)num_reqs + 2) * 4);
   d->qscale = up256(d->qlat + rows * kDc * 2);
   d->lat = up256(d->qscale + rows * 4);
   d->lat_lse = up256(d->lat + rows * kDc * 2);
@@ -1896,6 +1896,9 @@ int mla_decode(const void* q, const int32_t* q_pos, const void* kv_cache, int kv
   if (num_blocks > INT32_MAX / kBlock) return MLA_ERR_UNSUPPORTED;   // TMA row coordinates
   DecodeLayout d;
   if (!decode_layout(num_reqs, total_q, num_heads, &d)) return MLA_ERR_UNSUPPORTED;
+  // the most work units that any lengths can give (items x tiles of the longest sequence) stay within 31 bits
+  const double items = (double)total_q * num_heads / kItemRows + num_reqs;
+  if (items * ((double)max_blocks_per_req / 2 + num_segments + 4) >= 2147483648.0) return MLA_ERR_UNSUPPORTED;
   if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < d.total) return MLA_ERR_WORKSPACE;
   const int H = num_heads;
   const bool fp8 = kv_dtype == MLA_KV_FP8_E4M3;
@@ -1910,7 +1913,7 @@ int mla_decode(const void* q, const int32_t* q_pos, const void* kv_cache, int kv
   batch.num_heads = H;
   DecodeSpace space;
   space.err = reinterpret_cast<uint32_t*>(ws);
-  space.first = reinterpret_cast<int64_t*>(ws + d.first);
+  space.first = reinterpret_cast<int32_t*>(ws + d.first);
   space.qlat = ws + d.qlat;
   space.qscale = reinterpret_cast<float*>(ws + d.qscale);
   space.lat = reinterpret_cast<uint16_t*>(ws + d.lat);
@@ -1948,12 +1951,15 @@ int mla_decode(const void* q, const int32_t* q_pos, const void* kv_cache, int kv
     const uint64_t dc[3] = {fp8 ? 128u : 64u, (uint64_t)num_blocks * kBlock, blocks};
     const uint64_t sc[2] = {fp8 ? (uint64_t)kRowBytesFp8 : (uint64_t)kRowBytesBf16, 128};
     const uint32_t bs[3] = {(uint32_t)dc[0], 64, 1};
-    const uint32_t bv[3] = {(uint32_t)dc[0], fp8 ? 64u : 32u, fp8 ? 4u : 8u};
+    const uint32_t bv[3] = {(uint32_t)dc[0], fp8 ? 64u : 32u, fp8 ? 2u : 4u};
     ok &= encode_map(&p.tm_s, fp8 ? byte : bf16, 3, kv_cache, dc, sc, bs, sw);
     ok &= encode_map(&p.tm_o, fp8 ? byte : bf16, 3, kv_cache, dc, sc, bv, sw);
     const uint64_t dl[2] = {(uint64_t)kDc, n}, dp[2] = {(uint64_t)kDc, (uint64_t)kDecodeSlots * kItemRows};
     const uint64_t sl[1] = {(uint64_t)kDc * 2}, sp[1] = {(uint64_t)kDc * 4};
     const uint32_t bl[2] = {64, 128}, bp[2] = {32, 128};
+    const uint64_t dq[2] = {(uint64_t)kDc, fp8 ? 2 * n : n}, sq[1] = {fp8 ? (uint64_t)kDc : (uint64_t)kDc * 2};
+    const uint32_t bq[2] = {(uint32_t)dc[0], 128};
+    ok &= encode_map(&p.tm_q, fp8 ? byte : bf16, 2, space.qlat, dq, sq, bq, sw);
     ok &= encode_map(&p.tm_lat, bf16, 2, space.lat, dl, sl, bl, sw);
     ok &= encode_map(&p.tm_part, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, space.part, dp, sp, bp, sw);
   }

@@ -41,44 +41,47 @@
 namespace mla {
 namespace {
 
-constexpr int kThreads = 256;   // warp 0: loads (scores: first half of a tile); 1: MMA; 2: TMEM; 3: loads of the
-                                // second half (scores), P landed (values); 4-7: softmax or rescale and epilogue
+// Scores: warps 0, 3 load; 1: MMA; 2: TMEM, then the copies of P; 4-11: softmax,
+// two threads a row; 12-15: Q.  Values: warps 0, 2 load; 1: MMA; 3: P landed;
+// 4-11: rescale and epilogue, half the columns each.
+constexpr int kThreads = 512;
 constexpr uint32_t kBlk = 16384;                 // [128 rows x 128 B] swizzled block
 // scores CTA: rotated q_rope, two P staging buffers, the ring
 constexpr uint32_t kQR = 0;
 constexpr uint32_t kPS = kBlk;
 constexpr uint32_t kPBytes = 2 * kBlk;           // P of a tile: [128 x 128] bf16, or two 8-bit terms
 constexpr uint32_t kSRing = kPS + 2 * kPBytes;
-constexpr int kSStages = 3;
-constexpr uint32_t kSStage = 3 * kBlk;           // three 128-byte blocks of 128 rows
+constexpr int kSStages = 9;                      // of one 128-byte block of 128 rows
 // values CTA: two P tiles, the ring, two boxes for the epilogue
 constexpr uint32_t kOP = 0;
 constexpr uint32_t kORing = 2 * kPBytes;
-constexpr int kOStages = 4;
-constexpr uint32_t kOStage = 32768;              // 32 bf16 rows or 64 FP8 rows, without k_rope
+constexpr int kOStages = 8;
+constexpr uint32_t kOStage = 16384;              // 256 latent columns of 32 bf16 rows or 64 FP8 rows
 constexpr uint32_t kOBox = kORing + kOStages * kOStage;
 // both: per P buffer the rows' factors, sums and four rescale flags (staged and copied like P), then barriers
-constexpr uint32_t kFac = kSRing + kSStages * kSStage;
+constexpr uint32_t kFac = kSRing + kSStages * kBlk;
 static_assert(kFac == kOBox + 2 * kBlk, "the factors sit at one offset in both CTAs");
 constexpr uint32_t kFacSum = 512, kFacFlags = 1024, kFacBytes = 1040;
 constexpr uint32_t kBars = kFac + 2 * kFacBytes;
 enum : uint32_t {
   // scores
-  kSF = 0,      // 3: stage landed (two loading threads)
-  kSE = 3,      // 3: the stage's MMAs are done
-  kSSF = 6,     // 2: S buffer written
-  kSSR = 8,     // 2: the 4 softmax warps have read the S buffer
-  kQRd = 10,    // Q of the range in place (4 warps)
-  kPFR = 11,    // 2: the PV of the P tile is done (from the values CTA)
-  kSTF = 13,    // 2: a staging buffer's last copy landed (from the values CTA)
+  kSF = 0,      // 9: stage landed
+  kSE = 9,      // 9: the stage has been read (its MMAs are done, or Q is in TMEM)
+  kSSF = 18,    // 2: S buffer written
+  kSSR = 20,    // 2: the 8 softmax warps have read the S buffer
+  kQRd = 22,    // Q of the run in place (4 warps)
+  kQE = 23,     // the MMAs that read it are done
+  kPST = 24,    // 2: P staged (8 warps)
+  kPFR = 26,    // 2: the PV of the P tile is done (from the values CTA)
+  kSTF = 28,    // 2: a staging buffer's last copy landed (from the values CTA)
   // values
-  kCF = 15,     // 4: stage landed
-  kCE = 19,     // 4: the stage's MMAs are done
-  kPF = 23,     // 2: P tile, factors and flags landed
-  kPVD = 25,    // 2: PV of the tile done
-  kCN = 27,     // the control warp handed a tile, or a piece's end, to the correction warps
-  kCD = 28,     // the 4 correction warps rescaled their rows (piece's end: have read the sums)
-  kEP = 29,     // the 4 correction warps have read the piece's O
+  kCF = 0,      // 8: stage landed
+  kCE = 8,      // 8: the stage's MMAs are done
+  kPF = 16,     // 2: P tile, factors and flags landed
+  kPVD = 18,    // 2: PV of the tile done
+  kCN = 20,     // the control warp handed a tile, or a piece's end, to the correction warps
+  kCD = 21,     // the 8 correction warps rescaled their rows (piece's end: have read the sums)
+  kEP = 22,     // the 8 correction warps have read the piece's O
   kNBars = 30
 };
 constexpr uint32_t kShared = kBars + 8 * kNBars;   // Start, then the hand-over word
@@ -94,67 +97,76 @@ constexpr uint32_t kIdPV8 = idesc_8bit(128, 256, 1, 0, true);     // E5M2 P
 constexpr uint32_t kIdPV8r = idesc_8bit(128, 256, 0, 0, true);    // E4M3 rest of P
 constexpr float kRescale = 8.f;   // log2 units: P stays <= 256
 
+// The larger of two bf16 values (16 bits each), as float bits.
+__device__ __forceinline__ uint32_t max_bf16(uint32_t a, uint32_t b) {
+  return __float_as_uint(fmaxf(__uint_as_float(a << 16), __uint_as_float(b << 16)));
+}
+// A float's bf16 not below it, as 16 bits.
+__device__ __forceinline__ uint32_t bf16_up(float x) {
+  const uint32_t u = __float_as_uint(x);
+  return ((int32_t)u >= 0 ? u + 0xFFFFu : u) >> 16;
+}
+
 // Where a cluster's run of units begins: in request r, whose first unit is `first`.
 struct Start {
-  int64_t begin, end, first, total;
-  int r, n;      // n: clusters in use
+  int begin, end, first, r;
+  RequestWork w;   // of request r
   uint32_t tmem;
 };
 
 // The units of all requests, and this cluster's run.  Every thread of the CTA;
 // thread t takes requests [t k, (t + 1) k).  CTA 0 of the grid leaves the
 // requests' first units for decode_out_kernel and reports cut sequences.
-__device__ void schedule(const DecodeParams& p, Start* st, int64_t* scratch, int cluster) {
+__device__ void schedule(const DecodeParams& p, Start* st, int* scratch, int cluster) {
   const int B = p.batch.rows.num_reqs, k = (B + kThreads - 1) / kThreads;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int r0 = min(B, tid * k), r1 = min(B, r0 + k);
-  int64_t sum = 0;
+  RequestWork w;
+  int sum = 0;
   for (int r = r0; r < r1; ++r) {
-    const RequestWork w = request_work(p.batch, r);
-    sum += (int64_t)w.units() * w.items;
+    w = request_work(p.batch, r);
+    sum += w.units() * w.items;
     if (blockIdx.x == 0 && __ldg(p.batch.rows.seq_lens + r) > p.batch.max_blocks * kBlock) atomicOr(p.ws.err, kErrBadBlock);
   }
-  int64_t pre = sum;
+  int pre = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t v = __shfl_up_sync(0xffffffffu, pre, o);
+    const int v = __shfl_up_sync(0xffffffffu, pre, o);
     if (lane >= o) pre += v;
   }
   if (lane == 31) scratch[warp] = pre;
+  if (tid == 0) st->r = B;
   __syncthreads();
-  int64_t total = 0;
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) pre += scratch[w];
-    total += scratch[w];
+  int total = 0;
+#pragma unroll 4
+  for (int i = 0; i < kThreads / 32; ++i) {
+    if (i < warp) pre += scratch[i];
+    total += scratch[i];
   }
   pre -= sum;   // units of the requests before r0
-  const int64_t n = total < (int64_t)(gridDim.x / 2) ? total : (int64_t)(gridDim.x / 2);
-  const int64_t begin = cluster < n ? unit_begin(cluster, n, total) : total;
+  const int n = min(total, (int)gridDim.x / 2);
+  const int begin = cluster < n ? unit_begin(cluster, n, total) : total;
   if (tid == 0) {
     st->begin = begin;
     st->end = cluster < n ? unit_begin(cluster + 1, n, total) : total;
-    st->total = total;
-    st->n = (int)n;
-    st->r = B;
     if (blockIdx.x == 0) {
       p.ws.first[B] = total;
-      p.ws.first[B + 1] = total;
-      p.ws.first[B + 2] = n;
+      p.ws.first[B + 1] = n;
     }
   }
-  __syncthreads();
   const bool mine = begin >= pre && begin < pre + sum;
   if (mine || blockIdx.x == 0) {
-    int64_t at = pre;
+    int at = pre;
     bool found = false;
     for (int r = r0; r < r1; ++r) {
-      const RequestWork w = request_work(p.batch, r);
+      if (k > 1) w = request_work(p.batch, r);
       if (blockIdx.x == 0) p.ws.first[r] = at;
-      const int64_t next = at + (int64_t)w.units() * w.items;
+      const int next = at + w.units() * w.items;
       if (mine && !found && begin < next) {
         found = true;
         st->r = r;
         st->first = at;
+        st->w = w;
       }
       at = next;
     }
@@ -162,82 +174,101 @@ __device__ void schedule(const DecodeParams& p, Start* st, int64_t* scratch, int
   __syncthreads();
 }
 
-// A piece: tiles [lo, hi) of one item.
-struct Piece {
-  RequestWork w;
-  int r, row0, lo, hi, slot;   // slot -1: the whole item
-};
-// The pieces of a cluster's run in order, walked alike by every role.
-struct Pieces {
-  RequestWork w;
-  int64_t at, end;   // next unit, one past the run's last
-  int64_t first;     // first unit of request r
-  int r, cluster;
-  bool loaded;
-  __device__ Pieces(const Start& s, int cluster_) : at(s.begin), end(s.end), first(s.first), r(s.r), cluster(cluster_), loaded(false) {}
-  __device__ bool next(const DecodeParams& p, Piece& o) {
-    while (at < end && r < p.batch.rows.num_reqs) {
-      if (!loaded) {
-        w = request_work(p.batch, r);
-        loaded = true;
-      }
-      const int u = w.units();
-      const int64_t past = first + (int64_t)u * w.items;
-      if (at >= past) {   // also a request without units
-        first = past;
-        ++r;
-        loaded = false;
-        continue;
-      }
-      const int item = (int)((at - first) / u);
-      const int64_t base = first + (int64_t)item * u;
-      const int64_t stop = min(base + u, end);
-      o.lo = (int)max((int64_t)0, at - base - kItemUnits);
-      o.hi = (int)max((int64_t)0, stop - base - kItemUnits);
-      at = stop;
-      if (o.hi <= o.lo) continue;   // only units of the item's start
-      o.w = w;
-      o.r = r;
-      o.row0 = item * kItemRows;
-      o.slot = (o.lo == 0 && o.hi == w.tiles) ? -1 : 2 * cluster + (o.lo == 0 ? 1 : 0);
-      return true;
-    }
-    return false;
-  }
-};
-
-// The part of a piece with one RoPE offset: tiles j = 0 .. n - 1 from key t0 on, keys [k_lo, k_hi).
-struct Run {
+// A cluster's run of units, walked alike by every role, as ranges of key tiles
+// with one RoPE offset: tiles j = 0 .. n - 1 of 128 keys from key t0 on, of
+// which [k_lo, k_hi) count.  The ranges of a piece (a run of one item's tiles)
+// follow one another, the first marked `head`, the last `tail`.
+struct Walk {
+  // range
   int t0, n, k_lo, k_hi;
   int64_t offset;
-};
-struct Runs {
-  int g, end, acc;
-  __device__ explicit Runs(const Piece& o) : g(o.w.sg.x), end(0), acc(0) {}
-  __device__ bool next(const DecodeParams& p, const Piece& o, Run& u) {
-    while (g <= o.w.sg.y && acc < o.hi) {
-      const KeyRange k = request_range(p.batch, o.w.sg, g, end, o.w.len);
-      const int from = acc;
-      end = k.hi;
-      acc += range_tiles(k);
-      ++g;
-      const int lo = max(from, o.lo), hi = min(acc, o.hi);
-      if (lo >= hi) continue;
-      u.t0 = (k.lo & ~(kBlock - 1)) + 128 * (lo - from);
-      u.n = hi - lo;
-      u.k_lo = k.lo;
-      u.k_hi = k.hi;
-      u.offset = k.offset;
-      return true;
-    }
-    return false;
+  bool head, tail;
+  // its piece
+  int r, row0, slot;      // request, first row of the item, slot of its state (-1: a whole item)
+  int q_begin, rows, len; // first query row of the request, its (token, head) rows, its tokens
+  // where the walk is
+  RequestWork w;
+  int at, end, first, cluster;
+  int lo, hi, g, last_key, acc;   // the piece's tiles; next range, end of the keys so far, tiles so far
+  __device__ __forceinline__ void start(const Start& s, int cluster_) {
+    w = s.w;
+    at = s.begin;
+    end = s.end;
+    first = s.first;
+    r = s.r;
+    cluster = cluster_;
+    lo = hi = acc = 0;
   }
 };
 
-__device__ __forceinline__ bool await(const DecodeParams& p, uint32_t bar, uint32_t parity) {
+// One copy of this code serves every role: inlined into each, the kernel's code
+// was 170 KB and its roles waited for instructions (1.5 times the time).
+__device__ __noinline__ bool next_range(const DecodeParams& p, Walk& k) {
+  k.head = false;
+  while (k.acc >= k.hi) {   // the next piece
+    while (true) {
+      if (k.at >= k.end || k.r >= p.batch.rows.num_reqs) return false;
+      const int u = k.w.units();
+      const int past = k.first + u * k.w.items;
+      if (k.at >= past) {   // also a request without units
+        k.first = past;
+        if (++k.r < p.batch.rows.num_reqs) k.w = request_work(p.batch, k.r);
+        continue;
+      }
+      const int item = (k.at - k.first) / u;
+      const int base = k.first + item * u;
+      const int stop = min(base + u, k.end);
+      k.lo = max(0, k.at - base - kItemUnits);
+      k.hi = max(0, stop - base - kItemUnits);
+      k.at = stop;
+      if (k.hi <= k.lo) continue;   // only units of the item's start
+      k.row0 = item * kItemRows;
+      k.slot = (k.lo == 0 && k.hi == k.w.tiles) ? -1 : 2 * k.cluster + (k.lo == 0 ? 1 : 0);
+      break;
+    }
+    k.q_begin = k.w.q_begin;
+    k.rows = k.w.q_count * p.batch.num_heads;
+    k.len = k.w.len;
+    k.g = k.w.sg.x;
+    k.last_key = 0;
+    k.acc = 0;
+    k.head = true;
+    // ranges before the piece's first tile
+    while (k.g <= k.w.sg.y) {
+      const KeyRange kr = request_range(p.batch, k.w.sg, k.g, k.last_key, k.len);
+      const int t = range_tiles(kr);
+      if (k.acc + t > k.lo) break;
+      k.acc += t;
+      k.last_key = kr.hi;
+      ++k.g;
+    }
+  }
+  while (true) {   // the next range with tiles: the piece's tiles say there is one
+    const KeyRange kr = request_range(p.batch, k.w.sg, k.g, k.last_key, k.len);
+    const int t = range_tiles(kr), from = k.acc;
+    k.last_key = kr.hi;
+    k.acc += t;
+    ++k.g;
+    const int lo = max(from, k.lo), hi = min(k.acc, k.hi);
+    if (lo >= hi) continue;
+    k.t0 = (kr.lo & ~(kBlock - 1)) + 128 * (lo - from);
+    k.n = hi - lo;
+    k.k_lo = kr.lo;
+    k.k_hi = kr.hi;
+    k.offset = kr.offset;
+    k.tail = k.acc >= k.hi;
+    return true;
+  }
+}
+
+// Waits for a barrier's phase; false, and the error word, when it gives up.
+__device__ __noinline__ bool await_long(uint32_t* err, uint32_t bar, uint32_t parity) {
   if (mbar_wait(bar, parity)) return true;
-  atomicOr(p.ws.err, kErrTimeout);
+  atomicOr(err, kErrTimeout);
   return false;
+}
+__device__ __forceinline__ bool await(const DecodeParams& p, uint32_t bar, uint32_t parity) {
+  return mbar_try_wait(bar, parity) || await_long(p.ws.err, bar, parity);
 }
 __device__ __forceinline__ bool await_warp(const DecodeParams& p, uint32_t bar, uint32_t parity) {
   return __all_sync(0xffffffffu, await(p, bar, parity));
@@ -257,6 +288,18 @@ __device__ __forceinline__ int cache_row(const DecodeParams& p, int r, int kt, i
   return id * kBlock + (kt & (kBlock - 1));
 }
 
+// Zeroes all but rows [lo, hi) of a values stage, for the MMAs that this warp issues next.
+template <int kRows>
+__device__ __noinline__ void zero_rows(uint32_t stage, int lo, int hi, int lane) {
+  for (int row = 0; row < kRows; ++row) {
+    if (row >= lo && row < hi) continue;
+    for (int c = lane; c < (int)(kOStage / kRows / 16); c += 32)
+      sts128(stage + (c >> 3) * (kRows * 128) + row * 128 + (c & 7) * 16, 0u, 0u, 0u, 0u);
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
 template <bool kFp8>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     decode_attn_kernel(const __grid_constant__ DecodeParams p) {
@@ -268,21 +311,25 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   const int H = p.batch.num_heads;
   auto bar = [&](uint32_t i) { return sb + kBars + 8u * i; };
   Start* start = reinterpret_cast<Start*>(smem + kShared);
-  constexpr int kTileStages = kFp8 ? 2 : 3;   // scores: 128-byte blocks 3 m .. of [c | k_rope] a stage (9 or 5 in all)
-  constexpr int kBlocks = kFp8 ? 5 : 9, kLatBlocks = kFp8 ? 4 : 8;
-  constexpr int kORows = kFp8 ? 64 : 32, kOPerTile = 128 / kORows;
+  constexpr int kBlocks = kFp8 ? 5 : 9, kLatBlocks = kFp8 ? 4 : 8;   // 128-byte blocks of a row [c | k_rope], of c
+  constexpr int kQBoxes = 8;                                         // and of an item's Q
+  constexpr int kORows = kFp8 ? 64 : 32, kOPerTile = 128 / kORows;   // key rows of a values stage
 
   if (tid == 0) {
     prefetch_tensormap(scores ? &p.tm_s : &p.tm_o);
     for (uint32_t i = 0; i < kNBars; ++i) {
       uint32_t cnt = 1;
-      if (i < kSE) cnt = 2;
-      else if (i == kSSR || i == kSSR + 1 || i == kQRd || i == kCD || i == kEP) cnt = 4;
+      if (scores) {
+        if (i == kSSR || i == kSSR + 1 || i == kPST || i == kPST + 1) cnt = 8;
+        else if (i == kQRd) cnt = 4;
+      } else if (i == kCD || i == kEP) {
+        cnt = 8;
+      }
       mbar_init(bar(i), cnt);
     }
     fence_mbar_init();
   }
-  schedule(p, start, reinterpret_cast<int64_t*>(smem), cluster);
+  schedule(p, start, reinterpret_cast<int*>(smem), cluster);
   cluster_sync_all();   // both CTAs' barriers exist before either is signalled
   if (warp == 2) {
     tmem_alloc(smem_u32(&start->tmem), 512);
@@ -292,37 +339,46 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&start->tmem);
-  Pieces pieces(*start, cluster);
-  Piece pc;
-  Run run;
+  Walk k;
+  k.start(*start, cluster);
 
   if (scores) {
     if ((warp == 0 || warp == 3) && lane == 0) {
-      // ---------------------------------------------------------- loads: 64 keys of each tile, all its blocks
-      const int half = warp == 3 ? 1 : 0;
+      // ---------------------------------------------------------- loads: an item's Q, then the blocks of its tiles,
+      // every other stage a thread
+      const int mine = warp == 3 ? 1 : 0;
       bool ok = true;
       int u = 0;
-      while (ok && pieces.next(p, pc)) {
-        Runs runs(pc);
-        while (ok && runs.next(p, pc, run)) {
-          for (int j = 0; j < run.n && ok; ++j) {
-            const int row = cache_row(p, pc.r, run.t0 + 128 * j + 64 * half, run.k_hi);
-            for (int m = 0; m < kTileStages; ++m, ++u) {
-              const int s = u % kSStages;
-              if (u >= kSStages && !await(p, bar(kSE + s), ((u / kSStages) - 1) & 1)) {
-                ok = false;
-                break;
-              }
-              const int nb = min(3, kBlocks - 3 * m);
-              mbar_arrive_expect_tx(bar(kSF + s), (uint32_t)nb * (kBlk / 2));
-              for (int b = 0; b < nb; ++b)
-                tma_load_3d(sb + kSRing + s * kSStage + b * kBlk + half * (kBlk / 2), &p.tm_s, 0, row, 3 * m + b,
-                            bar(kSF + s));
-            }
+      // stage u's slot is free: arms its barrier
+      auto open = [&]() {
+        const int s = u % kSStages;
+        if (u >= kSStages && !await(p, bar(kSE + s), ((u / kSStages) - 1) & 1)) return false;
+        mbar_arrive_expect_tx(bar(kSF + s), kBlk);
+        return true;
+      };
+      while (ok && next_range(p, k)) {
+        const int qrow = k.q_begin * H + k.row0;
+        for (int i = 0; k.head && i < kQBoxes; ++i, ++u) {
+          if ((u & 1) != mine) continue;
+          if (!(ok = open())) break;
+          const int s = u % kSStages;
+          if (kFp8) tma_load_2d(sb + kSRing + s * kBlk, &p.tm_q, 128 * (i & 3), qrow + (i >> 2) * p.batch.rows.rows * H, bar(kSF + s));
+          else tma_load_2d(sb + kSRing + s * kBlk, &p.tm_q, 64 * i, qrow, bar(kSF + s));
+        }
+        for (int j = 0; j < k.n && ok; ++j) {
+          const int kt = k.t0 + 128 * j;
+          const int row0 = cache_row(p, k.r, kt, k.k_hi), row1 = cache_row(p, k.r, kt + 64, k.k_hi);
+#pragma unroll 1
+          for (int b = 0; b < kBlocks; ++b, ++u) {
+            if ((u & 1) != mine) continue;
+            if (!(ok = open())) break;
+            const int s = u % kSStages;
+            tma_load_3d(sb + kSRing + s * kBlk, &p.tm_s, 0, row0, b, bar(kSF + s));
+            tma_load_3d(sb + kSRing + s * kBlk + kBlk / 2, &p.tm_s, 0, row1, b, bar(kSF + s));
           }
         }
       }
-      // the last commits land before this CTA exits
+      // the last reads are signalled before this CTA exits
       for (int v = max(0, u - kSStages); v < u && ok; ++v) ok = await(p, bar(kSE + v % kSStages), (v / kSStages) & 1);
     } else if (warp == 1) {
       // ---------------------------------------------------------- S = Q [c | k_rope]^T
@@ -331,237 +387,277 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       const uint64_t sd0 = sdesc_sw128(sb + kSRing, 16, 1024);
       int g = 0, s = 0, e = 0;
       uint32_t ph = 0;
-      while (ok && pieces.next(p, pc)) {
-        Runs runs(pc);
-        while (ok && runs.next(p, pc, run)) {
-          if (!await_warp(p, bar(kQRd), e++ & 1)) { ok = false; break; }
-          for (int j = 0; j < run.n && ok; ++j, ++g) {
-            const int b = g & 1;
-            if (g >= 2 && !await_warp(p, bar(kSSR + b), ((g >> 1) - 1) & 1)) { ok = false; break; }
-            const uint32_t d = tmem + 256 + 128 * b;
-#pragma unroll
-            for (int m = 0; m < kTileStages; ++m) {
-              if (!await_warp(p, bar(kSF + s), ph)) { ok = false; break; }
-              tc_fence_after();
-              const uint64_t sd = sdesc_add(sd0, s * kSStage);
-#pragma unroll
-              for (int kb = 0; kb < 3; ++kb) {
-                const int blk = 3 * m + kb;
-                if (blk >= kBlocks) break;
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                  const uint64_t bd = sdesc_add(sd, kb * kBlk + kk * 32);
-                  const uint32_t acc = (blk | kk) ? 1u : 0u;
-                  if (blk >= kLatBlocks) {
-                    mma_ss_elect(d, sdesc_add(qd, kk * 32), bd, kIdS, 1u);
-                  } else if (kFp8) {
-                    mma_ts_8bit_elect(d, tmem + 32 * blk + 8 * kk, bd, kIdS8, acc);
-                    mma_ts_8bit_elect(d, tmem + 128 + 32 * blk + 8 * kk, bd, kIdS8, 1u);
-                  } else {
-                    mma_ts_elect(d, tmem + 32 * blk + 8 * kk, bd, kIdS, acc);
-                  }
-                }
-              }
-              mma_commit_elect(bar(kSE + s));
-              if (++s == kSStages) { s = 0; ph ^= 1u; }
-            }
-            if (ok) mma_commit_elect(bar(kSSF + b));
-          }
+      while (ok && next_range(p, k)) {
+        if (k.head) {
+          s += kQBoxes;   // the Q stages
+          if (s >= kSStages) { s -= kSStages; ph ^= 1u; }
         }
+        const int n = k.n;
+        if (!await_warp(p, bar(kQRd), e++ & 1)) { ok = false; break; }
+        for (int j = 0; j < n && ok; ++j, ++g) {
+          const int b = g & 1;
+          if (g >= 2 && !await_warp(p, bar(kSSR + b), ((g >> 1) - 1) & 1)) { ok = false; break; }
+          const uint32_t d = tmem + 256 + 128 * b;
+          // unrolled: with the block in a register, every MMA took 130 cycles to issue
+#pragma unroll
+          for (int blk = 0; blk < kBlocks; ++blk) {
+            if (!await_warp(p, bar(kSF + s), ph)) { ok = false; break; }
+            tc_fence_after();
+            const uint64_t sd = sdesc_add(sd0, s * kBlk);
+            const uint32_t qa = tmem + 32 * blk;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+              const uint64_t bd = sdesc_add(sd, kk * 32);
+              const uint32_t acc = (blk | kk) ? 1u : 0u;
+              if (blk >= kLatBlocks) {
+                mma_ss_elect(d, sdesc_add(qd, kk * 32), bd, kIdS, 1u);
+              } else if (kFp8) {
+                mma_ts_8bit_elect(d, qa + 8 * kk, bd, kIdS8, acc);
+                mma_ts_8bit_elect(d, qa + 128 + 8 * kk, bd, kIdS8, 1u);
+              } else {
+                mma_ts_elect(d, qa + 8 * kk, bd, kIdS, acc);
+              }
+            }
+            mma_commit_elect(bar(kSE + s));
+            if (++s == kSStages) { s = 0; ph ^= 1u; }
+          }
+          if (ok) mma_commit_elect(bar(kSSF + b));
+        }
+        if (ok) mma_commit_elect(bar(kQE));
       }
-    } else if (warp >= 4) {
-      // ---------------------------------------------------------- Q into TMEM and shared memory; softmax
-      const int r = tid - 128;
-      const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    } else if (warp == 2 && lane == 0) {
+      // ---------------------------------------------------------- staged P and its factors into the values CTA
       const uint32_t o_p = mapa_shared(sb + kOP, 1u), o_fac = mapa_shared(sb + kFac, 1u), o_pf = mapa_shared(bar(kPF), 1u);
       bool ok = true;
       int g = 0;
-      while (ok && pieces.next(p, pc)) {
-        const int prow = pc.row0 + r;
-        const bool live = prow < pc.w.q_count * H;
-        const int tl = live ? prow / H : 0;
-        const int64_t grow = (int64_t)pc.w.q_begin + tl;
-        const int64_t orow = (int64_t)pc.w.q_begin * H + prow;
-        const float qs = kFp8 ? (live ? p.ws.qscale[orow] : 1.f) * p.kv_scale : 1.f;
-        // qlat: every earlier score MMA is done (this warp has seen the last S buffer of the piece before)
-        {
-          const uint8_t* src = p.ws.qlat + orow * (kFp8 ? kDc : 2 * kDc);
-          const int64_t second = kFp8 ? (int64_t)p.batch.rows.rows * H * kDc : kDc;   // TMEM columns 128 .. 255
-#pragma unroll 1
-          for (int i = 0; i < 4; ++i) {
-            const uint4* v4 = reinterpret_cast<const uint4*>(src + (i >> 1) * second + (i & 1) * 256);
-            uint4 v[16];
-#pragma unroll
-            for (int c = 0; c < 16; ++c) v[c] = live ? v4[c] : make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-              uint32_t w[32];
-#pragma unroll
-              for (int c = 0; c < 8; ++c) {
-                w[4 * c] = v[8 * hh + c].x; w[4 * c + 1] = v[8 * hh + c].y;
-                w[4 * c + 2] = v[8 * hh + c].z; w[4 * c + 3] = v[8 * hh + c].w;
-              }
-              tmem_st32(tmem + lane_off + 64 * i + 32 * hh, w);
-            }
-          }
-          tmem_wait_st();
-        }
-        const int qk = live ? pc.w.len - pc.w.q_count + tl : -1;   // the last key token the row sees
-        const float sl2 = p.scale_log2 * qs;
-        float m_used = -INFINITY, l = 0.f;
-        Runs runs(pc);
-        while (ok && runs.next(p, pc, run)) {
-          {
-            // q_rope turned by pos - offset, as a K-major swizzled block; FP8 scores count in units of qs,
-            // so it is divided by that
-            const uint4* qr = reinterpret_cast<const uint4*>(p.q + orow * kDqk + kDnope);
-            const int64_t delta = live ? (int64_t)__ldg(p.q_pos + grow) - run.offset : 0;
-            const float rq = 1.f / qs;
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              const uint4 qv = live ? __ldg(qr + c) : make_uint4(0, 0, 0, 0);
-              const uint32_t w4[4] = {qv.x, qv.y, qv.z, qv.w};
-              uint32_t o4[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                float sn, cs;
-                rope_sincos_sfu(delta, p.rope_frac[4 * c + i], &sn, &cs);
-                const float x0 = bf16_lo(w4[i]), x1 = bf16_hi(w4[i]);
-                o4[i] = pack_bf16((x0 * cs - x1 * sn) * rq, (x0 * sn + x1 * cs) * rq);
-              }
-              sts128(sb + kQR + sw128_off((uint32_t)r, (uint32_t)c), o4[0], o4[1], o4[2], o4[3]);
-            }
-            fence_proxy_async_smem();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kQRd));
-          }
-          for (int j = 0; j < run.n; ++j, ++g) {
-            const int b = g & 1;
-            uint32_t v0[64], v1[64];
-            float mx = -INFINITY;
-            bool wok = await_warp(p, bar(kSSF + b), (g >> 1) & 1);
-            tc_fence_after();
-            if (wok) {
-              const float m0 = tmem_ld64_max(tmem + lane_off + 256 + 128 * b, v0);
-              const float m1 = tmem_ld64_max(tmem + lane_off + 256 + 128 * b + 64, v1);
-              mx = fmaxf(m0, m1);
-            }
-            tc_fence_before();
-            __syncwarp();
-            // relaxed: the reads are ordered for the next MMAs by the tcgen05 fences around it
-            if (lane == 0 && wok) mbar_arrive_relaxed(bar(kSSR + b));
-            const int kt0 = run.t0 + 128 * j;
-            if (!(kt0 >= run.k_lo && kt0 + 127 < run.k_hi && kt0 + 127 <= qk)) {
-              const int hi = min(run.k_hi - 1, qk) - kt0, lo = run.k_lo - kt0;   // visible columns lo .. hi
-              float m8[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) m8[i] = -INFINITY;
-#pragma unroll
-              for (int c = 0; c < 64; ++c) {
-                const float xa = (c >= lo && c <= hi) ? __uint_as_float(v0[c]) : -INFINITY;
-                const float xb = (c + 64 >= lo && c + 64 <= hi) ? __uint_as_float(v1[c]) : -INFINITY;
-                v0[c] = __float_as_uint(xa);
-                v1[c] = __float_as_uint(xb);
-                m8[c & 7] = fmax3(m8[c & 7], xa, xb);
-              }
-              mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])), fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
-            }
-            const float m_tile = mx * sl2;
-            float alpha = 1.f;
-            if (m_tile > m_used + kRescale) {
-              alpha = ex2(m_used - m_tile);   // 0 when m_used = -inf
-              m_used = m_tile;
-            }
-            const float mref = (m_used == -INFINITY) ? 0.f : m_used;
-            const uint64_t sc2 = f2pack(sl2, sl2), nm2 = f2pack(-mref, -mref);
-            // P in registers while the previous tile's copy is still in flight: bf16 pairs, or per four keys a
-            // word of E5M2 and a word of E4M3 codes
-            uint64_t s4[4] = {0ull, 0ull, 0ull, 0ull};
-            uint32_t pk[64];
-            if (wok) {
-#pragma unroll
-              for (int c = 0; c < 64; ++c) {
-                const uint32_t x0u = c < 32 ? v0[2 * c] : v1[2 * c - 64], x1u = c < 32 ? v0[2 * c + 1] : v1[2 * c - 63];
-                float x0, x1;
-                f2unpack(ffma2(f2pack(__uint_as_float(x0u), __uint_as_float(x1u)), sc2, nm2), x0, x1);
-                const float a = ex2(x0), bb = ex2(x1);
-                s4[c & 3] = fadd2(s4[c & 3], f2pack(a, bb));
-                if constexpr (kFp8) {
-                  // a value to 2 mantissa bits (half up), exact in E5M2 above 2^-14, and the rest
-                  const float ah = __uint_as_float((__float_as_uint(a) + 0x00100000u) & 0xFFE00000u);
-                  const float bh = __uint_as_float((__float_as_uint(bb) + 0x00100000u) & 0xFFE00000u);
-                  const uint32_t h2 = pack_e5m2x2(ah, bh), r2 = pack_e4m3x2(a - ah, bb - bh);
-                  if (c & 1) {
-                    pk[c >> 1] |= h2 << 16;
-                    pk[32 + (c >> 1)] |= r2 << 16;
-                  } else {
-                    pk[c >> 1] = h2;
-                    pk[32 + (c >> 1)] = r2;
-                  }
-                } else {
-                  pk[c] = pack_bf16(a, bb);
-                }
-              }
-            }
-            // the staging buffer is free once the copy it held two tiles ago landed; the four warps go on, or
-            // leave, together
-            if (wok && g >= 2) wok = await_warp(p, bar(kSTF + b), ((g - 2) >> 1) & 1);
-            if (named_bar_or(1, 128, !wok)) { ok = false; break; }
-            const uint32_t stg = sb + kPS + b * kPBytes;
-#pragma unroll
-            for (int hk = 0; hk < 2; ++hk)
-#pragma unroll
-              for (int c = 0; c < 8; ++c)
-                sts128(stg + hk * kBlk + sw128_off((uint32_t)r, (uint32_t)c), pk[32 * hk + 4 * c],
-                       pk[32 * hk + 4 * c + 1], pk[32 * hk + 4 * c + 2], pk[32 * hk + 4 * c + 3]);
-            float s8[4];
-            f2unpack(fadd2(s4[0], s4[1]), s8[0], s8[1]);
-            f2unpack(fadd2(s4[2], s4[3]), s8[2], s8[3]);
-            l = l * alpha + ((s8[0] + s8[2]) + (s8[1] + s8[3]));
-            uint8_t* fac = smem + kFac + b * kFacBytes;
-            reinterpret_cast<float*>(fac)[r] = alpha;
-            reinterpret_cast<float*>(fac + kFacSum)[r] = l;
-            const uint32_t any_rescale = __any_sync(0xffffffffu, alpha != 1.f) ? 1u : 0u;
-            if (lane == 0) reinterpret_cast<uint32_t*>(fac + kFacFlags)[warp & 3] = any_rescale;
-            fence_proxy_async_smem();   // the staged tile is read by the bulk copies (async proxy)
-            named_bar_sync(1, 128);
-            if (r == 0) {
-              // P tile b of the values CTA is free once the PV of tile g - 2 is done
-              if (g >= 2 && !await(p, bar(kPFR + b), ((g - 2) >> 1) & 1)) continue;   // the others time out next tile
-              bulk_copy_to_peer(o_p + b * kPBytes, stg, kPBytes, o_pf + 8u * b);
-              bulk_copy_to_peer(o_fac + b * kFacBytes, sb + kFac + b * kFacBytes, kFacBytes, o_pf + 8u * b);
-            }
-          }
-        }
-        if (live) {
-          const float lse = (ok && l > 0.f) ? (m_used + __log2f(l)) * 0.6931471805599453f : -INFINITY;
-          if (pc.slot < 0) p.ws.lat_lse[orow] = lse;
-          else p.ws.part_lse[pc.slot * kItemRows + r] = lse;
+      while (ok && next_range(p, k)) {
+        for (int j = 0; j < k.n && ok; ++j, ++g) {
+          const int b = g & 1;
+          // P tile b of the values CTA is free once the PV of tile g - 2 is done
+          ok = await(p, bar(kPST + b), (g >> 1) & 1) && (g < 2 || await(p, bar(kPFR + b), ((g - 2) >> 1) & 1));
+          if (!ok) break;
+          bulk_copy_to_peer(o_p + b * kPBytes, sb + kPS + b * kPBytes, kPBytes, o_pf + 8u * b);
+          bulk_copy_to_peer(o_fac + b * kFacBytes, sb + kFac + b * kFacBytes, kFacBytes, o_pf + 8u * b);
         }
       }
       // the last two PV commits land before this CTA exits
-      for (int v = max(0, g - 2); v < g && ok; ++v) ok = await_warp(p, bar(kPFR + (v & 1)), (v >> 1) & 1);
-    }
-  } else {
-    if (warp == 0 && lane == 0) {
-      // ---------------------------------------------------------- loads: latent columns of 32 (64) keys a stage
+      for (int v = max(0, g - 2); v < g && ok; ++v) ok = await(p, bar(kPFR + (v & 1)), (v >> 1) & 1);
+    } else if (warp >= 12) {
+      // ---------------------------------------------------------- Q: qlat from its stages into TMEM, rotated q_rope
+      // into shared memory
+      const int r = tid - 384;
+      const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
       bool ok = true;
-      int u = 0;
-      while (ok && pieces.next(p, pc)) {
-        Runs runs(pc);
-        while (ok && runs.next(p, pc, run)) {
-          const int stages = kOPerTile * run.n;
-          for (int i = 0; i < stages; ++i, ++u) {
-            const int s = u % kOStages;
-            const int row = cache_row(p, pc.r, run.t0 + kORows * i, run.k_hi);
-            if (u >= kOStages && !await(p, bar(kCE + s), ((u / kOStages) - 1) & 1)) { ok = false; break; }
-            mbar_arrive_expect_tx(bar(kCF + s), kOStage);
-            tma_load_3d(sb + kORing + s * kOStage, &p.tm_o, 0, row, 0, bar(kCF + s));
+      int e = 0, u = 0;
+      while (next_range(p, k)) {
+        const int prow = k.row0 + r;
+        const bool live = prow < k.rows;
+        const int64_t grow = (int64_t)k.q_begin + (live ? prow / H : 0);
+        const int64_t orow = (int64_t)k.q_begin * H + prow;
+        const float rq = kFp8 && live ? 1.f / (p.ws.qscale[orow] * p.kv_scale) : 1.f;
+        const uint4* qr = reinterpret_cast<const uint4*>(p.q + orow * kDqk + kDnope);
+        const int64_t delta = live ? (int64_t)__ldg(p.q_pos + grow) - k.offset : 0;
+        uint4 x[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) x[c] = live ? __ldg(qr + c) : make_uint4(0, 0, 0, 0);
+        // the MMAs that read the Q before this are done
+        if (ok && e > 0) ok = await_warp(p, bar(kQE), (e - 1) & 1);
+        ++e;
+        tc_fence_after();
+        if (k.head) {
+#pragma unroll 1
+          for (int i = 0; i < kQBoxes; ++i, ++u) {
+            const int s = u % kSStages;
+            if (ok) ok = await_warp(p, bar(kSF + s), (u / kSStages) & 1);
+            uint32_t w[32];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              uint32_t w4[4];
+              lds128(sb + kSRing + s * kBlk + sw128_off((uint32_t)r, (uint32_t)c), w4);
+              w[4 * c] = w4[0]; w[4 * c + 1] = w4[1]; w[4 * c + 2] = w4[2]; w[4 * c + 3] = w4[3];
+            }
+            tmem_st32(tmem + lane_off + 32 * i, w);
+            named_bar_sync(6, 128);   // all rows of the stage are read
+            if (r == 0 && ok) mbar_arrive(bar(kSE + s));
           }
         }
+        // q_rope as a K-major swizzled block, turned in place by pos - offset (a row is one thread's); FP8
+        // scores count in units of the row's scale, so it is divided by that
+#pragma unroll
+        for (int c = 0; c < 8; ++c) sts128(sb + kQR + sw128_off((uint32_t)r, (uint32_t)c), x[c].x, x[c].y, x[c].z, x[c].w);
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c) {
+          const uint32_t at = sb + kQR + sw128_off((uint32_t)r, (uint32_t)c);
+          uint32_t w4[4];
+          lds128(at, w4);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float sn, cs;
+            rope_sincos_sfu(delta, p.rope_frac[4 * c + i], &sn, &cs);
+            const float x0 = bf16_lo(w4[i]), x1 = bf16_hi(w4[i]);
+            w4[i] = pack_bf16((x0 * cs - x1 * sn) * rq, (x0 * sn + x1 * cs) * rq);
+          }
+          sts128(at, w4[0], w4[1], w4[2], w4[3]);
+        }
+        tmem_wait_st();
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0 && ok) mbar_arrive(bar(kQRd));
+        u += kBlocks * k.n;   // the stages of its tiles
       }
-      for (int v = max(0, u - kOStages); v < u && ok; ++v) ok = await(p, bar(kCE + v % kOStages), (v / kOStages) & 1);
+      if (ok && e > 0) await_warp(p, bar(kQE), (e - 1) & 1);   // the last commit lands before this CTA exits
+    } else if (warp >= 4) {
+      // ---------------------------------------------------------- softmax: columns 64 half .. of a row a thread
+      const int half = (warp - 4) >> 2, r = 32 * (warp & 3) + lane;
+      const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+      const uint32_t pair = 1 + (warp & 3);   // barrier of the two warps that share 32 rows
+      // a warp whose wait gave up goes on without waits and signals: its barriers with the other warp of its rows
+      // are met
+      bool ok = true;
+      int g = 0;
+      float m_used = -INFINITY, l = 0.f, lsum = 0.f;
+      while (next_range(p, k)) {
+        const int prow = k.row0 + r;
+        const bool live = prow < k.rows;
+        const int64_t orow = (int64_t)k.q_begin * H + prow;
+        const float sl2 = p.scale_log2 * (kFp8 && live ? p.ws.qscale[orow] * p.kv_scale : 1.f);
+        const int qk = live ? k.len - (k.rows - 1 - prow) / H - 1 : -1;   // the last key token the row sees
+        const int n = k.n, t0 = k.t0, k_lo = k.k_lo, k_hi = k.k_hi, slot = k.slot;
+        const bool tail = k.tail;
+        if (k.head) {
+          m_used = -INFINITY;
+          l = lsum = 0.f;
+        }
+#pragma unroll 1
+        for (int j = 0; j < n; ++j, ++g) {
+          const int b = g & 1;
+          uint32_t v[64];
+          float mx;
+          // the staging buffer is free once the copy it held two tiles ago landed
+          if (ok && g >= 2) ok = await_warp(p, bar(kSTF + b), ((g - 2) >> 1) & 1);
+          if (ok) ok = await_warp(p, bar(kSSF + b), (g >> 1) & 1);
+          tc_fence_after();
+          mx = tmem_ld64_max(tmem + lane_off + 256 + 128 * b + 64 * half, v);
+          tc_fence_before();
+          __syncwarp();
+          // relaxed: the reads are ordered for the next MMAs by the tcgen05 fences around it
+          if (lane == 0 && ok) mbar_arrive_relaxed(bar(kSSR + b));
+          const int kt0 = t0 + 128 * j + 64 * half;
+          if (!(kt0 >= k_lo && kt0 + 63 < k_hi && kt0 + 63 <= qk)) {
+            const int hi = min(k_hi - 1, qk) - kt0, lo = k_lo - kt0;   // visible columns lo .. hi
+            float m4[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m4[i] = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < 64; c += 2) {
+              const float xa = (c >= lo && c <= hi) ? __uint_as_float(v[c]) : -INFINITY;
+              const float xb = (c + 1 >= lo && c + 1 <= hi) ? __uint_as_float(v[c + 1]) : -INFINITY;
+              v[c] = __float_as_uint(xa);
+              v[c + 1] = __float_as_uint(xb);
+              m4[(c >> 1) & 3] = fmax3(m4[(c >> 1) & 3], xa, xb);
+            }
+            mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+          }
+          // the row's maximum over both halves, rounded up to bf16 by both threads alike (any common reference
+          // near the maximum will do).  The two warps exchange in their 128 bytes of the sums' place beside this
+          // P tile; two tiles on, both are past the next tile's barrier, so these reads are done.
+          uint8_t* fac = smem + kFac + b * kFacBytes;
+          volatile uint16_t* mx16 = reinterpret_cast<volatile uint16_t*>(fac + kFacSum + 128 * (warp & 3));
+          volatile float* l32 = reinterpret_cast<volatile float*>(fac + kFacSum + 128 * (warp & 3));
+          mx16[32 * half + lane] = (uint16_t)bf16_up(mx);
+          named_bar_sync(pair, 64);
+          const float m_tile = __uint_as_float(max_bf16(mx16[lane], mx16[32 + lane])) * sl2;
+          float alpha = 1.f;
+          if (m_tile > m_used + kRescale) {
+            alpha = ex2(m_used - m_tile);   // 0 when m_used = -inf
+            m_used = m_tile;
+          }
+          const float mref = (m_used == -INFINITY) ? 0.f : m_used;
+          const uint64_t sc2 = f2pack(sl2, sl2), nm2 = f2pack(-mref, -mref);
+          // P in registers while the previous tile's copy is still in flight: bf16 pairs, or per four keys a
+          // word of E5M2 and a word of E4M3 codes
+          uint64_t s2[2] = {0ull, 0ull};
+          uint32_t pk[32];
+          {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              float x0, x1;
+              f2unpack(ffma2(f2pack(__uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1])), sc2, nm2), x0, x1);
+              const float a = ex2(x0), bb = ex2(x1);
+              s2[c & 1] = fadd2(s2[c & 1], f2pack(a, bb));
+              if constexpr (kFp8) {
+                // a value to 2 mantissa bits (half up), exact in E5M2 above 2^-14, and the rest
+                const float ah = __uint_as_float((__float_as_uint(a) + 0x00100000u) & 0xFFE00000u);
+                const float bh = __uint_as_float((__float_as_uint(bb) + 0x00100000u) & 0xFFE00000u);
+                const uint32_t h2 = pack_e5m2x2(ah, bh), r2 = pack_e4m3x2(a - ah, bb - bh);
+                if (c & 1) {
+                  pk[c >> 1] |= h2 << 16;
+                  pk[16 + (c >> 1)] |= r2 << 16;
+                } else {
+                  pk[c >> 1] = h2;
+                  pk[16 + (c >> 1)] = r2;
+                }
+              } else {
+                pk[c] = pack_bf16(a, bb);
+              }
+            }
+          }
+          float s4[4];
+          f2unpack(s2[0], s4[0], s4[1]);
+          f2unpack(s2[1], s4[2], s4[3]);
+          l = l * alpha + ((s4[0] + s4[2]) + (s4[1] + s4[3]));
+          if (tail && j == n - 1) {   // the piece's last tile: the row's sum over both halves
+            named_bar_sync(pair, 64);   // the maxima have been read
+            if (half) l32[lane] = l;
+            named_bar_sync(pair, 64);
+            if (half == 0) {
+              lsum = l + l32[lane];
+              l32[lane] = lsum;
+            }
+          }
+          const uint32_t stg = sb + kPS + b * kPBytes;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            // bf16: 64 keys are the half's own block; 8-bit: 4 chunks of each term's block
+            const uint32_t at = kFp8 ? stg + (c >> 2) * kBlk + sw128_off((uint32_t)r, (uint32_t)(4 * half + (c & 3)))
+                                     : stg + half * kBlk + sw128_off((uint32_t)r, (uint32_t)c);
+            sts128(at, pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+          }
+          if (half == 0) {
+            reinterpret_cast<float*>(fac)[r] = alpha;
+            const uint32_t any_rescale = __any_sync(0xffffffffu, alpha != 1.f) ? 1u : 0u;
+            if (lane == 0) reinterpret_cast<uint32_t*>(fac + kFacFlags)[warp & 3] = any_rescale;
+          }
+          fence_proxy_async_smem();   // the staged tile is read by the bulk copies (async proxy)
+          __syncwarp();
+          if (lane == 0 && ok) mbar_arrive(bar(kPST + b));
+        }
+        if (tail && live && half == 0) {
+          const float lse = (ok && lsum > 0.f) ? (m_used + __log2f(lsum)) * 0.6931471805599453f : -INFINITY;
+          if (slot < 0) p.ws.lat_lse[orow] = lse;
+          else p.ws.part_lse[slot * kItemRows + r] = lse;
+        }
+      }
+    }
+  } else {
+    if ((warp == 0 || warp == 2) && lane == 0) {
+      // ---------------------------------------------------------- loads: 256 latent columns of 32 (64) keys a stage,
+      // each half of the columns by its thread
+      const int nh = warp >> 1;
+      bool ok = true;
+      int u = nh;
+      while (ok && next_range(p, k)) {
+        const int stages = kOPerTile * k.n;
+        for (int i = 0; i < stages; ++i, u += 2) {
+          const int s = u & (kOStages - 1);
+          const int row = cache_row(p, k.r, k.t0 + kORows * i, k.k_hi);
+          if (u >= kOStages && !await(p, bar(kCE + s), ((u / kOStages) - 1) & 1)) { ok = false; break; }
+          mbar_arrive_expect_tx(bar(kCF + s), kOStage);
+          tma_load_3d(sb + kORing + s * kOStage, &p.tm_o, 0, row, (kLatBlocks / 2) * nh, bar(kCF + s));
+        }
+      }
+      for (int v = max(nh, u - kOStages); v < u && ok; v += 2) ok = await(p, bar(kCE + (v & (kOStages - 1))), (v / kOStages) & 1);
     } else if (warp == 1) {
       // ---------------------------------------------------------- P landed, rows rescaled, O += P c
       volatile int* hand = reinterpret_cast<volatile int*>(smem + kHand);
@@ -571,85 +667,76 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       int g = 0, u = 0, events = 0, done = 0;   // tiles, stages, hand-overs, finished pieces
       if (lane == 0)
         for (int b = 0; b < 2; ++b) mbar_arrive_expect_tx(bar(kPF + b), kTxP);
-      while (ok && pieces.next(p, pc)) {
-        Runs runs(pc);
-        int left = pc.hi - pc.lo;
-        bool head = true;
-        while (ok && runs.next(p, pc, run)) {
-          for (int j = 0; j < run.n && ok; ++j, ++g, --left) {
-            const int b = g & 1;
-            if (!await_warp(p, bar(kPF + b), (g >> 1) & 1)) { ok = false; break; }
-            if (!head) {
-              uint32_t f[4];
-              lds128(sb + kFac + b * kFacBytes + kFacFlags, f);
-              if (f[0] | f[1] | f[2] | f[3]) {
-                // O must hold the PV of every earlier tile before its rows are rescaled
-                if (!await_warp(p, bar(kPVD + ((g - 1) & 1)), ((g - 1) >> 1) & 1)) { ok = false; break; }
-                if (lane == 0) {
-                  *hand = b;
-                  mbar_arrive(bar(kCN));
-                }
-                if (!await_warp(p, bar(kCD), events++ & 1)) { ok = false; break; }
-              }
-            } else if (done > 0) {
-              // the piece before has been read out of O
-              if (!await_warp(p, bar(kEP), (done - 1) & 1)) { ok = false; break; }
-            }
-            if (left == 1) {
-              // the row sums sit beside this P tile: read before the next tiles may replace them
+      bool head = true;
+      while (ok && next_range(p, k)) {
+        if (k.head) head = true;
+#pragma unroll 1
+        for (int j = 0; j < k.n && ok; ++j, ++g) {
+          const int b = g & 1;
+          if (!await_warp(p, bar(kPF + b), (g >> 1) & 1)) { ok = false; break; }
+          if (!head) {
+            uint32_t f[4];
+            lds128(sb + kFac + b * kFacBytes + kFacFlags, f);
+            if (f[0] | f[1] | f[2] | f[3]) {
+              // O must hold the PV of every earlier tile before its rows are rescaled
+              if (!await_warp(p, bar(kPVD + ((g - 1) & 1)), ((g - 1) >> 1) & 1)) { ok = false; break; }
               if (lane == 0) {
-                *hand = 2 + b;
+                *hand = b;
                 mbar_arrive(bar(kCN));
               }
               if (!await_warp(p, bar(kCD), events++ & 1)) { ok = false; break; }
             }
-            fence_proxy_async_smem();   // P was written by the other CTA's copy, the MMA reads it as an operand
-            if (lane == 0) mbar_arrive_expect_tx_relaxed(bar(kPF + b), kTxP);
-            __syncwarp();
-            tc_fence_after();
+          } else if (done > 0) {
+            // the piece before has been read out of O
+            if (!await_warp(p, bar(kEP), (done - 1) & 1)) { ok = false; break; }
+          }
+          if (k.tail && j == k.n - 1) {
+            // the row sums sit beside this P tile: read before the next tiles may replace them
+            if (lane == 0) {
+              *hand = 2 + b;
+              mbar_arrive(bar(kCN));
+            }
+            if (!await_warp(p, bar(kCD), events++ & 1)) { ok = false; break; }
+          }
+          fence_proxy_async_smem();   // P was written by the other CTA's copy, the MMA reads it as an operand
+          if (lane == 0) mbar_arrive_expect_tx_relaxed(bar(kPF + b), kTxP);
+          __syncwarp();
+          tc_fence_after();
+#pragma unroll 1
+          for (int i = 0; i < kOPerTile; ++i) {
+            if (!ok) break;
 #pragma unroll
-            for (int i = 0; i < kOPerTile; ++i, ++u) {
+            for (int nh = 0; nh < 2; ++nh, ++u) {
               const int s = u & (kOStages - 1);
               if (!await_warp(p, bar(kCF + s), (u / kOStages) & 1)) { ok = false; break; }
               // rows outside the run meet P = 0, but may hold anything: they are zeroed
-              const int kt = run.t0 + 128 * j + kORows * i;
-              const int lo = max(0, run.k_lo - kt), hi = min(kORows, run.k_hi - kt);
-              if ((lo > 0 || hi < kORows) && hi > 0) {
-                for (int row = 0; row < kORows; ++row) {
-                  if (row >= lo && row < hi) continue;
-                  for (int c = lane; c < (int)(kOStage / kORows / 16); c += 32)
-                    sts128(sb + kORing + s * kOStage + (c >> 3) * (kORows * 128) + row * 128 + (c & 7) * 16, 0u, 0u, 0u, 0u);
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-              }
+              const int kt = k.t0 + 128 * j + kORows * i;
+              const int lo = max(0, k.k_lo - kt), hi = min(kORows, k.k_hi - kt);
+              if ((lo > 0 || hi < kORows) && hi > 0) zero_rows<kORows>(sb + kORing + s * kOStage, lo, hi, lane);
               tc_fence_after();
               const uint64_t cd = sdesc_add(cd0, s * kOStage);
 #pragma unroll
               for (int kk = 0; kk < 2; ++kk) {
                 const int k = 2 * i + kk;   // the tile's k-step: 16 keys (bf16) or 32 (FP8)
                 const uint32_t acc = (head && k == 0) ? 0u : 1u;
-#pragma unroll
-                for (int nh = 0; nh < 2; ++nh) {
-                  const uint64_t bd = sdesc_add(cd, nh * (kOStage / 2) + kk * (kORows * 64));
-                  if (kFp8) {
-                    mma_ss_8bit_elect(tmem + 256 * nh, sdesc_add(pd0, b * kPBytes + k * 32), bd, kIdPV8, acc);
-                    mma_ss_8bit_elect(tmem + 256 * nh, sdesc_add(pd0, b * kPBytes + kBlk + k * 32), bd, kIdPV8r, 1u);
-                  } else {
-                    mma_ss_elect(tmem + 256 * nh, sdesc_add(pd0, b * kPBytes + (k >> 2) * kBlk + (k & 3) * 32), bd,
-                                 kIdPV, acc);
-                  }
+                const uint64_t bd = sdesc_add(cd, kk * (kORows * 64));
+                if (kFp8) {
+                  mma_ss_8bit_elect(tmem + 256 * nh, sdesc_add(pd0, b * kPBytes + k * 32), bd, kIdPV8, acc);
+                  mma_ss_8bit_elect(tmem + 256 * nh, sdesc_add(pd0, b * kPBytes + kBlk + k * 32), bd, kIdPV8r, 1u);
+                } else {
+                  mma_ss_elect(tmem + 256 * nh, sdesc_add(pd0, b * kPBytes + (k >> 2) * kBlk + (k & 3) * 32), bd,
+                               kIdPV, acc);
                 }
               }
               mma_commit_elect(bar(kCE + s));
             }
-            if (!ok) break;
-            head = false;
-            mma_commit_elect(bar(kPVD + b));
-            mma_commit_mc_elect(bar(kPFR + b), 0x1);
           }
+          if (!ok) break;
+          head = false;
+          mma_commit_elect(bar(kPVD + b));
+          mma_commit_mc_elect(bar(kPFR + b), 0x1);
         }
-        ++done;
+        if (k.tail) ++done;
       }
       if (!ok && lane == 0) {
         *hand = -1;
@@ -662,20 +749,22 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       const uint32_t stf = mapa_shared(bar(kSTF), 0u);
       int g = 0;
       bool ok = true;
-      while (ok && pieces.next(p, pc))
-        for (int j = pc.lo; j < pc.hi && ok; ++j, ++g) {
+      while (ok && next_range(p, k))
+        for (int j = 0; j < k.n && ok; ++j, ++g) {
           ok = await(p, bar(kPF + (g & 1)), (g >> 1) & 1);
           if (ok) mbar_arrive_cluster_relaxed(stf + 8u * (g & 1));   // relaxed: a landed copy has read its source
         }
-    } else if (warp >= 4) {
-      // ---------------------------------------------------------- rescale O rows; epilogue
-      const int r = tid - 128;
-      const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    } else if (warp >= 4 && warp < 12) {
+      // ---------------------------------------------------------- rescale O rows; epilogue: columns 256 half ..
+      const int half = (warp - 4) >> 2, r = 32 * (warp & 3) + lane;
+      const uint32_t o_cols = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 256 * half;
+      const uint32_t box = sb + kOBox + half * kBlk;
       const volatile int* hand = reinterpret_cast<const volatile int*>(smem + kHand);
       bool ok = true;
       int g = 0, ev = 0;
-      while (pieces.next(p, pc)) {
-        g += pc.hi - pc.lo;
+      while (next_range(p, k)) {
+        g += k.n;
+        if (!k.tail) continue;   // a piece's states leave at its end
         float lsum = 0.f;
         while (ok) {
           if (!await_warp(p, bar(kCN), ev++ & 1)) { ok = false; break; }
@@ -691,12 +780,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           const float a = reinterpret_cast<const float*>(smem + kFac + h * kFacBytes)[r];
           if (__any_sync(0xffffffffu, a != 1.f)) {
 #pragma unroll 1
-            for (int cc = 0; cc < 16; ++cc) {
+            for (int cc = 0; cc < 8; ++cc) {
               uint32_t o[32];
-              tmem_ld32(tmem + lane_off + 32 * cc, o);
+              tmem_ld32(o_cols + 32 * cc, o);
 #pragma unroll
               for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
-              tmem_st32(tmem + lane_off + 32 * cc, o);
+              tmem_st32(o_cols + 32 * cc, o);
             }
             tmem_wait_st();
           }
@@ -705,72 +794,63 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           if (lane == 0) mbar_arrive(bar(kCD));
         }
         if (ok) ok = await_warp(p, bar(kPVD + ((g - 1) & 1)), ((g - 1) >> 1) & 1);
-        if (named_bar_or(2, 128, !ok)) {   // the four warps leave together
+        if (named_bar_or(2, 256, !ok)) {   // the eight warps leave together
           ok = false;
           break;
         }
         tc_fence_after();
         const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
-        const int prow = pc.row0 + r;
-        const int rows = pc.w.q_count * H - pc.row0;      // live rows of the item
-        const int64_t orow0 = (int64_t)pc.w.q_begin * H + pc.row0;
-        const bool whole = pc.slot < 0;
+        const int rows = k.rows - k.row0;      // live rows of the item
+        const int64_t orow0 = (int64_t)k.q_begin * H + k.row0;
+        const bool whole = k.slot < 0;
         const bool full = rows >= kItemRows;
-        // 128 live rows leave by TMA stores of staged 128-byte columns, fewer by their threads
+        // 128 live rows leave by TMA stores of staged 128-byte columns (64 bf16 or 32 fp32), fewer by their threads
 #pragma unroll 1
-        for (int cc = 0; cc < 16; ++cc) {
+        for (int cc = 0; cc < 8; ++cc) {
           uint32_t o[32];
-          tmem_ld32(tmem + lane_off + 32 * cc, o);
+          tmem_ld32(o_cols + 32 * cc, o);
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
-          if (cc == 15) {
+          if (cc == 7) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kEP));   // O has been read: the next piece may begin
           }
+          const int col = 256 * half + 32 * cc;
           if (whole) {
-            uint32_t w[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) w[i] = pack_bf16(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
-            if (full) {
-              const uint32_t box = sb + kOBox + (uint32_t)((cc >> 1) & 1) * kBlk;
-              if ((cc & 1) == 0) {   // a box of 64 columns: its last store has read it
-                if (r == 0) bulk_wait_read<1>();
-                named_bar_sync(2, 128);
-              }
-#pragma unroll
-              for (int c = 0; c < 4; ++c)
-                sts128(box + sw128_off((uint32_t)r, (uint32_t)(4 * (cc & 1) + c)), w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
-              if (cc & 1) {
-                fence_proxy_async_smem();
-                named_bar_sync(2, 128);
-                if (r == 0) {
-                  tma_store_2d(&p.tm_lat, box, 64 * (cc >> 1), (int)orow0);
-                  bulk_commit();
-                }
-              }
-            } else if (prow < pc.w.q_count * H) {
-              uint4* dst = reinterpret_cast<uint4*>(p.ws.lat + (orow0 + r) * kDc + 32 * cc);
-#pragma unroll
-              for (int c = 0; c < 4; ++c) dst[c] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+            for (int i = 0; i < 16; ++i) o[i] = pack_bf16(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
+          }
+          if (full) {
+            const bool first = !whole || (cc & 1) == 0, last = !whole || (cc & 1) != 0;
+            if (first) {   // the box's last store has read it
+              if (r == 0) bulk_wait_read0();
+              named_bar_sync(3 + half, 128);
             }
-          } else if (full) {
-            const uint32_t box = sb + kOBox + (uint32_t)(cc & 1) * kBlk;
-            if (r == 0) bulk_wait_read<1>();
-            named_bar_sync(2, 128);
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-              sts128(box + sw128_off((uint32_t)r, (uint32_t)c), o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
-            fence_proxy_async_smem();
-            named_bar_sync(2, 128);
-            if (r == 0) {
-              tma_store_2d(&p.tm_part, box, 32 * cc, pc.slot * kItemRows);
-              bulk_commit();
+            for (int c = 0; c < 4; ++c)
+              sts128(box + sw128_off((uint32_t)r, (uint32_t)(c + (whole ? 4 * (cc & 1) : 0))), o[4 * c], o[4 * c + 1],
+                     o[4 * c + 2], o[4 * c + 3]);
+            if (!whole) {
+#pragma unroll
+              for (int c = 4; c < 8; ++c)
+                sts128(box + sw128_off((uint32_t)r, (uint32_t)c), o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+            }
+            if (last) {
+              fence_proxy_async_smem();
+              named_bar_sync(3 + half, 128);
+              if (r == 0) {
+                if (whole) tma_store_2d(&p.tm_lat, box, col - 32, (int)orow0);
+                else tma_store_2d(&p.tm_part, box, col, k.slot * kItemRows);
+                bulk_commit();
+              }
             }
           } else if (r < rows) {
-            uint4* dst = reinterpret_cast<uint4*>(p.ws.part + ((int64_t)pc.slot * kItemRows + r) * kDc + 32 * cc);
+            uint4* dst = whole ? reinterpret_cast<uint4*>(p.ws.lat + (orow0 + r) * kDc + col)
+                               : reinterpret_cast<uint4*>(p.ws.part + ((int64_t)k.slot * kItemRows + r) * kDc + col);
 #pragma unroll
-            for (int c = 0; c < 8; ++c) dst[c] = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+            for (int c = 0; c < 8; ++c)
+              if (c < 4 || !whole) dst[c] = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
           }
         }
       }

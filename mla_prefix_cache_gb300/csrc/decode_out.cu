@@ -26,13 +26,13 @@ constexpr uint32_t kIdesc = idesc_bf16(128, 128, false, true);
 constexpr int kMaxPieces = kDecodeClusters;        // of one item
 
 struct RowOf {
-  int64_t x;       // unit of the item's first tile
+  int x;           // unit of the item's first tile
   int n;           // pieces: -1 no request's row, 0 no keys, 1 a whole item
   int c0;          // cluster of the first piece
   int ridx;        // row within the item
   float lse;
 };
-static_assert(sizeof(RowOf) == 24, "row table");
+static_assert(sizeof(RowOf) == 20, "row table");
 
 __device__ __forceinline__ bool wait(uint32_t* err, uint32_t bar, uint32_t parity) {
   if (mbar_wait(bar, parity)) return true;
@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_out_kernel(const __grid_co
     tmem_relinquish();
   }
   const int B = p.batch.rows.num_reqs;
-  const int64_t total = p.ws.first[B + 1], n_clusters = p.ws.first[B + 2];
+  const int total = p.ws.first[B], n_clusters = p.ws.first[B + 1];
   if (tid < R) {
     RowOf o;
     o.n = -1;
@@ -100,9 +100,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_out_kernel(const __grid_co
     const int r = find_request(p.batch.rows, r0 + tid);
     if (r >= 0) {
       const int2 rr = request_rows(p.batch.rows, r);
-      const int64_t f = p.ws.first[r];
+      const int f = p.ws.first[r];
       const int items = ((rr.y - rr.x) * H + kItemRows - 1) / kItemRows;
-      const int64_t u = (p.ws.first[r + 1] - f) / items;
+      const int u = (p.ws.first[r + 1] - f) / items;
       const int idx = (r0 + tid - rr.x) * H + h;
       o.ridx = idx & (kItemRows - 1);
       o.n = 0;

@@ -90,6 +90,7 @@ __device__ __forceinline__ RequestWork request_work(const DecodeBatch& b, int r)
   w.items = (w.q_count * b.num_heads + kItemRows - 1) / kItemRows;
   w.tiles = 0;
   int end = 0;
+#pragma unroll 2
   for (int g = w.sg.x; g <= w.sg.y; ++g) {
     const KeyRange k = request_range(b, w.sg, g, end, w.len);
     end = k.hi;
@@ -100,12 +101,13 @@ __device__ __forceinline__ RequestWork request_work(const DecodeBatch& b, int r)
 
 // The units [0, total) of the batch are cut evenly: cluster c of n has
 // [unit_begin(c), unit_begin(c + 1)); cluster_of(x) is the one that has unit x.
-__device__ __forceinline__ int64_t unit_begin(int64_t c, int64_t n, int64_t total) { return c * total / n; }
-__device__ __forceinline__ int cluster_of(int64_t x, int64_t n, int64_t total) { return (int)(((x + 1) * n - 1) / total); }
+// (The host keeps total below 2^31.)
+__device__ __forceinline__ int unit_begin(int c, int n, int total) { return (int)((uint64_t)c * (uint32_t)total / (uint32_t)n); }
+__device__ __forceinline__ int cluster_of(int x, int n, int total) { return (int)(((uint64_t)(x + 1) * (uint32_t)n - 1) / (uint32_t)total); }
 // The slot of the state that cluster c has of an item whose first tile is unit
 // x: each cluster shares one item with the clusters before it at most, and one
 // with those after it.
-__device__ __forceinline__ int piece_slot(int c, int64_t x, int64_t n, int64_t total) {
+__device__ __forceinline__ int piece_slot(int c, int x, int n, int total) {
   return 2 * c + (unit_begin(c, n, total) <= x ? 1 : 0);
 }
 

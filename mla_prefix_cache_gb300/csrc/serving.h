@@ -54,7 +54,7 @@ struct DecodeBatch {
 // Latent attention (decode.cu).  Workspace arrays:
 struct DecodeSpace {
   uint32_t* err;
-  int64_t* first;        // [num_reqs + 1]: the requests' first work units, then two more: units in all, clusters used
+  int32_t* first;        // [num_reqs + 2]: the requests' first work units, all units, clusters in use
   uint8_t* qlat;         // bf16 [rows * H][512], or E4M3 [2][rows * H][512]
   float* qscale;         // [rows * H]: the E4M3 rows' scales
   uint16_t* lat;         // bf16 [rows * H][512]: states of rows whose keys one cluster had
@@ -64,8 +64,9 @@ struct DecodeSpace {
 };
 
 struct DecodeParams {
+  CUtensorMap tm_q;      // qlat as [rows * H][512] bf16, or [2 * rows * H][512] bytes, box 128 B x 128
   CUtensorMap tm_s;      // the cache's rows in blocks of 128 B, box 128 B x 64 rows x 1
-  CUtensorMap tm_o;      // the same, box 128 B x 32 rows x 8 (bf16) or 128 B x 64 rows x 4 (FP8)
+  CUtensorMap tm_o;      // the same, box 128 B x 32 rows x 4 (bf16) or 128 B x 64 rows x 2 (FP8)
   CUtensorMap tm_lat;    // lat as [rows * H][512], box 64 x 128
   CUtensorMap tm_part;   // part as [kDecodeSlots * 128][512], box 32 x 128
   DecodeBatch batch;
