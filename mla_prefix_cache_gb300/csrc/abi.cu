@@ -1993,6 +1993,9 @@ int mla_decode(const void* q, const int32_t* q_pos, const void* kv_cache, int kv
   if (timed && (st = cuda_status(cudaEventRecord(ev_e, s))) != MLA_OK) return st;
 
   op.batch = batch;
+  // as many tokens a CTA as still give every SM one
+  op.tile = 128;
+  while (op.tile > 16 && (int64_t)((total_q + op.tile / 2 - 1) / (op.tile / 2)) * H <= 2 * kDecodeClusters) op.tile /= 2;
   op.ws = space;
   op.out = out;
   op.out_bf16 = out_dtype == MLA_OUT_BF16;

@@ -116,17 +116,20 @@ struct Start {
 
 // The units of all requests, and this cluster's run.  Every thread of the CTA;
 // thread t takes requests [t k, (t + 1) k).  CTA 0 of the grid leaves the
-// requests' first units for decode_out_kernel and reports cut sequences.
-__device__ void schedule(const DecodeParams& p, Start* st, int* scratch, int cluster) {
+// requests' first units for decode_out_kernel; true if this thread met a
+// sequence longer than its table.  It may run before the kernel that clears the
+// error word has.
+__device__ bool schedule(const DecodeParams& p, Start* st, int* scratch, int cluster) {
   const int B = p.batch.rows.num_reqs, k = (B + kThreads - 1) / kThreads;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int r0 = min(B, tid * k), r1 = min(B, r0 + k);
   RequestWork w;
   int sum = 0;
+  bool cut = false;   // a sequence longer than its table
   for (int r = r0; r < r1; ++r) {
     w = request_work(p.batch, r);
     sum += w.units() * w.items;
-    if (blockIdx.x == 0 && __ldg(p.batch.rows.seq_lens + r) > p.batch.max_blocks * kBlock) atomicOr(p.ws.err, kErrBadBlock);
+    cut |= __ldg(p.batch.rows.seq_lens + r) > p.batch.max_blocks * kBlock;
   }
   int pre = sum;
 #pragma unroll
@@ -172,6 +175,7 @@ __device__ void schedule(const DecodeParams& p, Start* st, int* scratch, int clu
     }
   }
   __syncthreads();
+  return cut;
 }
 
 // A cluster's run of units, walked alike by every role, as ranges of key tiles
@@ -329,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     }
     fence_mbar_init();
   }
-  schedule(p, start, reinterpret_cast<int*>(smem), cluster);
+  const bool cut = schedule(p, start, reinterpret_cast<int*>(smem), cluster);
   cluster_sync_all();   // both CTAs' barriers exist before either is signalled
   if (warp == 2) {
     tmem_alloc(smem_u32(&start->tmem), 512);
@@ -341,6 +345,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&start->tmem);
   Walk k;
   k.start(*start, cluster);
+  grid_wait();      // the queries' kernel is done (it also clears the error word)
+  grid_trigger();   // decode_out_kernel may take SMs as they fall free
+  if (cut && blockIdx.x == 0) atomicOr(p.ws.err, kErrBadBlock);
 
   if (scores) {
     if ((warp == 0 || warp == 3) && lane == 0) {
@@ -896,10 +903,8 @@ cudaError_t launch_decode_attn(const DecodeParams& p, bool fp8, cudaStream_t s) 
     clusters = resident < 1 ? 1 : resident < kDecodeClusters ? resident : kDecodeClusters;
     configured = dev;
   }
-  if (fp8) decode_attn_kernel<true><<<2 * clusters, kThreads, kSmem, s>>>(p);
-  else decode_attn_kernel<false><<<2 * clusters, kThreads, kSmem, s>>>(p);
-  count_launch();
-  return cudaGetLastError();
+  return launch_dependent(fp8 ? decode_attn_kernel<true> : decode_attn_kernel<false>, dim3(2 * clusters), kThreads, kSmem,
+                          p, s);
 }
 
 }  // namespace mla

@@ -2,28 +2,32 @@
 // row's keys are joined, and every row goes through W_UV of its head,
 //   w_i = e^{lse_i - m} / sum_j e^{lse_j - m},  o = sum_i w_i o_i,  lse = m + ln sum_j e^{lse_j - m}
 //   out[t][h] = out_scale o W_UV,h
-// A CTA takes 128 tokens of one head.  Its warps join the fp32 states of their
-// rows (few rows: several warps a row, each some of the pieces), or take the
-// bf16 state that one cluster left, into one K-major swizzled operand of 512
-// columns; W_UV,h comes by TMA in four chunks of 128 rows, two buffers deep,
-// and one chain of M = 128, N = 128 MMAs makes the 128 output columns.  o is
-// rounded to bf16 for the product, once, after the join.
+// A CTA takes some tokens of one head: up to 128, fewer where the grid would
+// not fill the GPU.  Its 32 warps join the fp32 states of their rows (few rows:
+// several warps a row, each some of the pieces), or take the bf16 state that
+// one cluster left, into one K-major swizzled operand of 512 columns; W_UV,h
+// comes by TMA in four chunks of 128 rows, two buffers deep, and one chain of
+// M = 128, N = 128 MMAs makes the 128 output columns.  o is rounded to bf16 for
+// the product, once, after the join.  Latency-bound: a row is two dependent
+// loads from L2 (weights, states), so the rows are spread over many warps (8
+// warps took 30 us for 64 tokens of 128 heads).
 #include "serving.cuh"
 
 namespace mla {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kThreads = 1024, kWarps = kThreads / 32;
 constexpr uint32_t kBlk = 16384;                   // [128 rows x 128 B] swizzled block
 constexpr uint32_t kA = 0;                         // 8 blocks of 64 columns
 constexpr uint32_t kB = 8 * kBlk;                  // 2 buffers of [128 c x 128 j] in two blocks
-constexpr uint32_t kRed = kB + 4 * kBlk;           // [8 warps][512] fp32: partial joins of few rows
-constexpr uint32_t kRows = kRed + kWarps * kDc * 4;
-constexpr uint32_t kBars = kRows + 128 * 24;       // B landed x 2, buffer's MMAs done x 2, TMEM address
+constexpr uint32_t kRows = kB + 4 * kBlk;
+constexpr uint32_t kBegin = kRows + 128 * 20;      // first unit of each cluster
+constexpr uint32_t kBars = (kBegin + 4 * (kDecodeClusters + 1) + 15) & ~15u;   // B landed x 2, MMAs done x 2, TMEM address
 constexpr uint32_t kSmem = kBars + 48;
 static_assert(kSmem <= 232448, "more than 227 KB of shared memory per CTA");
 constexpr uint32_t kIdesc = idesc_bf16(128, 128, false, true);
 constexpr int kMaxPieces = kDecodeClusters;        // of one item
+constexpr int kMaxShare = 8;                       // warps that share a row
 
 struct RowOf {
   int x;           // unit of the item's first tile
@@ -33,6 +37,11 @@ struct RowOf {
   float lse;
 };
 static_assert(sizeof(RowOf) == 20, "row table");
+
+// Partial sums of warps that share rows (at most 4 rows then): 2 KB each in the
+// operand's rows from 8 on, which nothing else uses.
+__device__ __forceinline__ uint32_t share_at(int warp) { return kA + (uint32_t)(warp / 7) * kBlk + 1024 + (uint32_t)(warp % 7) * 2048; }
+static_assert((kWarps + 6) / 7 <= 8, "the warps' partial sums fit beside the rows");
 
 __device__ __forceinline__ bool wait(uint32_t* err, uint32_t bar, uint32_t parity) {
   if (mbar_wait(bar, parity)) return true;
@@ -64,11 +73,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_out_kernel(const __grid_co
   const uint32_t sb = smem_u32(smem);
   const uint32_t bars = sb + kBars;
   RowOf* rows = reinterpret_cast<RowOf*>(smem + kRows);
+  int* begin = reinterpret_cast<int*>(smem + kBegin);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kBars + 32);
-  float* red = reinterpret_cast<float*>(smem + kRed);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int H = p.batch.num_heads, h = blockIdx.z, r0 = blockIdx.x * 128;
-  const int R = min(128, p.batch.rows.rows - r0);
+  const int H = p.batch.num_heads, h = blockIdx.z, r0 = blockIdx.x * p.tile;
+  const int R = min(p.tile, p.batch.rows.rows - r0);
 
   auto load_w = [&](int ch) {
     const uint32_t b = ch & 1, dst = sb + kB + b * 2 * kBlk;
@@ -84,22 +93,25 @@ __global__ void __launch_bounds__(kThreads, 1) decode_out_kernel(const __grid_co
     load_w(0);
     load_w(1);
   }
-  if (warp == 0) {
-    __syncwarp();
+  if (warp == 1) {
     tmem_alloc(smem_u32(tmem_slot), 128);
     tmem_relinquish();
   }
   const int B = p.batch.rows.num_reqs;
+  int r = -1;
+  int2 rr = make_int2(0, 0);
+  if (tid < R) {
+    r = find_request(p.batch.rows, r0 + tid);
+    if (r >= 0) rr = request_rows(p.batch.rows, r);
+  }
+  grid_wait();   // the attention kernel's states are there
   const int total = p.ws.first[B], n_clusters = p.ws.first[B + 1];
   if (tid < R) {
     RowOf o;
     o.n = -1;
-    o.c0 = o.ridx = 0;
-    o.x = 0;
+    o.c0 = o.ridx = o.x = 0;
     o.lse = -INFINITY;
-    const int r = find_request(p.batch.rows, r0 + tid);
     if (r >= 0) {
-      const int2 rr = request_rows(p.batch.rows, r);
       const int f = p.ws.first[r];
       const int items = ((rr.y - rr.x) * H + kItemRows - 1) / kItemRows;
       const int u = (p.ws.first[r + 1] - f) / items;
@@ -110,9 +122,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_out_kernel(const __grid_co
         o.x = f + (idx / kItemRows) * u + kItemUnits;
         o.c0 = cluster_of(o.x, n_clusters, total);
         o.n = cluster_of(o.x + u - kItemUnits - 1, n_clusters, total) - o.c0 + 1;
+        if (o.n == 1) o.lse = p.ws.lat_lse[(int64_t)(r0 + tid) * H + h];
       }
     }
     rows[tid] = o;
+  } else if (tid >= 512 && tid - 512 < n_clusters) {
+    begin[tid - 512] = unit_begin(tid - 512, n_clusters, total);
   }
   tc_fence_before();
   __syncthreads();
@@ -120,21 +135,19 @@ __global__ void __launch_bounds__(kThreads, 1) decode_out_kernel(const __grid_co
   const uint32_t tmem = *tmem_slot;
 
   // ---------------------------------------------------------------- the rows' states
-  const int G = R <= 1 ? 8 : R <= 2 ? 4 : R <= 4 ? 2 : 1;   // warps a row
+  const int G = R <= 4 ? kMaxShare : 1;   // warps a row
+  const int part = warp % G;
   for (int i = warp / G; i < R; i += kWarps / G) {
     const RowOf o = rows[i];
-    const int64_t orow = (int64_t)(r0 + i) * H + h;
-    const int part = warp % G;
     if (o.n == 1) {
       if (part == 0) {
-        const uint4* src = reinterpret_cast<const uint4*>(p.ws.lat + orow * kDc);
+        const uint4* src = reinterpret_cast<const uint4*>(p.ws.lat + ((int64_t)(r0 + i) * H + h) * kDc);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const int c = lane + 32 * k;   // 16-byte chunk of the row
           const uint4 v = src[c];
           sts128(sb + kA + (uint32_t)(c >> 3) * kBlk + sw128_off((uint32_t)i, (uint32_t)(c & 7)), v.x, v.y, v.z, v.w);
         }
-        if (lane == 0) rows[i].lse = p.ws.lat_lse[orow];
       }
       continue;
     }
@@ -142,13 +155,16 @@ __global__ void __launch_bounds__(kThreads, 1) decode_out_kernel(const __grid_co
 #pragma unroll
     for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (o.n > 1) {
-      // lane l has the weights of pieces l, l + 32, l + 64
+      // lane l has the weights and slots of pieces l, l + 32, l + 64
       constexpr int kPerLane = (kMaxPieces + 31) / 32;
       float w[kPerLane], m = -INFINITY;
+      int at[kPerLane];   // row of the states
 #pragma unroll
       for (int k = 0; k < kPerLane; ++k) {
-        const int i2 = lane + 32 * k;
-        w[k] = i2 < o.n ? p.ws.part_lse[piece_slot(o.c0 + i2, o.x, n_clusters, total) * kItemRows + o.ridx] : -INFINITY;
+        const int c = o.c0 + lane + 32 * k;
+        const bool have = lane + 32 * k < o.n;
+        at[k] = have ? (2 * c + (begin[c] <= o.x ? 1 : 0)) * kItemRows + o.ridx : 0;
+        w[k] = have ? p.ws.part_lse[at[k]] : -INFINITY;
         m = fmaxf(m, w[k]);
       }
 #pragma unroll
@@ -167,19 +183,20 @@ __global__ void __launch_bounds__(kThreads, 1) decode_out_kernel(const __grid_co
       for (int k = 0; k < kPerLane; ++k) {
         if (32 * k >= o.n) break;
         const int last = min(32, o.n - 32 * k);
-        const int step = G;
-#pragma unroll 4
-        for (int l = part; l < last; l += step) {
+#pragma unroll 2
+        for (int l = part; l < last; l += G) {
           const float wi = __shfl_sync(0xffffffffu, w[k], l) * inv;
-          const int slot = piece_slot(o.c0 + 32 * k + l, o.x, n_clusters, total);
-          const float4* src = reinterpret_cast<const float4*>(p.ws.part + ((int64_t)slot * kItemRows + o.ridx) * kDc) + lane;
+          const int row = __shfl_sync(0xffffffffu, at[k], l);
+          const float4* src = reinterpret_cast<const float4*>(p.ws.part + (int64_t)row * kDc) + lane;
+          float4 v[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) v[q] = src[32 * q];
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const float4 v = src[32 * q];
-            acc[q].x = fmaf(wi, v.x, acc[q].x);
-            acc[q].y = fmaf(wi, v.y, acc[q].y);
-            acc[q].z = fmaf(wi, v.z, acc[q].z);
-            acc[q].w = fmaf(wi, v.w, acc[q].w);
+            acc[q].x = fmaf(wi, v[q].x, acc[q].x);
+            acc[q].y = fmaf(wi, v[q].y, acc[q].y);
+            acc[q].z = fmaf(wi, v[q].z, acc[q].z);
+            acc[q].w = fmaf(wi, v[q].w, acc[q].w);
           }
         }
       }
@@ -189,20 +206,20 @@ __global__ void __launch_bounds__(kThreads, 1) decode_out_kernel(const __grid_co
       for (int k = 0; k < 4; ++k) put4(sb + kA, i, lane, k, acc[k]);
     } else {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) reinterpret_cast<float4*>(red + warp * kDc)[lane + 32 * k] = acc[k];
+      for (int k = 0; k < 4; ++k) reinterpret_cast<float4*>(smem + share_at(warp))[lane + 32 * k] = acc[k];
     }
   }
   if (G > 1) {
     __syncthreads();
-    if (warp < R && rows[warp].n != 1) {   // warp i sums row i's parts
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
+    if (warp < 4 * R) {   // columns 128 k .. of row i
+      const int i = warp >> 2, k = warp & 3;
+      if (rows[i].n != 1) {
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int g = 0; g < G; ++g) {
-          const float4 v = reinterpret_cast<const float4*>(red + (warp * G + g) * kDc)[lane + 32 * k];
+          const float4 v = reinterpret_cast<const float4*>(smem + share_at(i * G + g))[lane + 32 * k];
           s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
         }
-        put4(sb + kA, warp, lane, k, s);
+        put4(sb + kA, i, lane, k, s);
       }
     }
   }
@@ -232,31 +249,33 @@ __global__ void __launch_bounds__(kThreads, 1) decode_out_kernel(const __grid_co
   if (ok) ok = __all_sync(0xffffffffu, wait(p.ws.err, bars + 16, 1) && wait(p.ws.err, bars + 24, 1));
   tc_fence_after();
   if (ok) {
-    // warps w and w + 4 share TMEM lanes 32 (w mod 4) ..: columns 64 (w / 4) .. + 63
-    const int i = 32 * (warp & 3) + lane, cb = 64 * (warp >> 2);
-    uint32_t v[64];
-    tmem_ld64(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + cb, v);
-    if (i < R && rows[i].n >= 0) {
-      const int64_t orow = (int64_t)(r0 + i) * H + h, o = orow * kDv + cb;
-      const bool empty = rows[i].lse == -INFINITY;   // no key seen: 0
+    // sixteen warps: TMEM lanes 32 (w mod 4) .., columns 32 (w / 4) ..
+    const int i = 32 * (warp & 3) + lane, cb = 32 * (warp >> 2);
+    if (warp < 16 && 32 * (warp & 3) < R) {
+      uint32_t v[32];
+      tmem_ld32(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + cb, v);
+      if (i < R && rows[i].n >= 0) {
+        const int64_t orow = (int64_t)(r0 + i) * H + h, o = orow * kDv + cb;
+        const bool empty = rows[i].lse == -INFINITY;   // no key seen: 0
 #pragma unroll
-      for (int k = 0; k < 64; ++k) v[k] = empty ? 0u : __float_as_uint(__uint_as_float(v[k]) * p.out_scale);
-      if (p.out_bf16) {
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + o);
-        auto o2 = [&](int k) { return pack_bf16(__uint_as_float(v[k]), __uint_as_float(v[k + 1])); };
+        for (int k = 0; k < 32; ++k) v[k] = empty ? 0u : __float_as_uint(__uint_as_float(v[k]) * p.out_scale);
+        if (p.out_bf16) {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + o);
+          auto o2 = [&](int k) { return pack_bf16(__uint_as_float(v[k]), __uint_as_float(v[k + 1])); };
 #pragma unroll
-        for (int k = 0; k < 8; ++k) dst[k] = make_uint4(o2(8 * k), o2(8 * k + 2), o2(8 * k + 4), o2(8 * k + 6));
-      } else {
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<float*>(p.out) + o);
+          for (int k = 0; k < 4; ++k) dst[k] = make_uint4(o2(8 * k), o2(8 * k + 2), o2(8 * k + 4), o2(8 * k + 6));
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<float*>(p.out) + o);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) dst[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+          for (int k = 0; k < 8; ++k) dst[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+        }
+        if (p.lse != nullptr && warp < 4) p.lse[orow] = rows[i].lse;
       }
-      if (p.lse != nullptr && warp < 4) p.lse[orow] = rows[i].lse;
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 0) {
+  if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 128);
   }
@@ -274,10 +293,8 @@ cudaError_t launch_decode_out(const DecodeOutParams& p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     configured = dev;
   }
-  const dim3 grid((p.batch.rows.rows + 127) / 128, 1, p.batch.num_heads);
-  decode_out_kernel<<<grid, kThreads, kSmem, s>>>(p);
-  count_launch();
-  return cudaGetLastError();
+  return launch_dependent(decode_out_kernel, dim3((p.batch.rows.rows + p.tile - 1) / p.tile, 1, p.batch.num_heads), kThreads,
+                          kSmem, p, s);
 }
 
 }  // namespace mla

@@ -62,7 +62,10 @@ __global__ void __launch_bounds__(128, 1) qabsorb_kernel(const __grid_constant__
   const int t0 = p.row0 + blockIdx.x * 128;   // first token of the tile (TMA coordinates)
 
   if (threadIdx.x == 0) {
-    if (p.clear != nullptr && (blockIdx.x | blockIdx.y | blockIdx.z) == 0) *p.clear = 0u;
+    if (p.clear != nullptr) {
+      asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the attention kernel may start its own set-up
+      if ((blockIdx.x | blockIdx.y | blockIdx.z) == 0) *p.clear = 0u;
+    }
     mbar_init(bar_full, 1);
     mbar_init(bar_done, 1);
     fence_mbar_init();

@@ -7,6 +7,29 @@
 
 namespace mla {
 
+// Programmatic dependent launch: a kernel launched by launch_dependent may
+// start while the kernel before it in the stream still runs; grid_wait() in it
+// returns when that one's memory is visible, grid_trigger() in the earlier one
+// lets it start.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <class Params>
+cudaError_t launch_dependent(void (*kernel)(Params), dim3 grid, int threads, size_t smem, const Params& p, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  count_launch();
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
 // First row of request r and one past its last, clamped to the batch's rows.
 __device__ __forceinline__ int2 request_rows(const BatchRows& b, int r) {
   if (b.cu_q == nullptr) return make_int2(r * b.per_req, (r + 1) * b.per_req);

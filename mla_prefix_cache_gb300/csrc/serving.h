@@ -87,6 +87,7 @@ struct DecodeOutParams {
   CUtensorMap tm_w;      // kv_b_proj as [512][H * 256], box 64 x 128
   DecodeBatch batch;
   DecodeSpace ws;
+  int tile;              // tokens of a CTA (at most 128)
   void* out;             // [rows][H][128]
   int out_bf16;
   float* lse;            // optional [rows][H]
