@@ -52,15 +52,14 @@ constexpr uint32_t kPS = kBlk;
 constexpr uint32_t kPBytes = 2 * kBlk;           // P of a tile: [128 x 128] bf16, or two 8-bit terms
 constexpr uint32_t kSRing = kPS + 2 * kPBytes;
 constexpr int kSStages = 9;                      // of one 128-byte block of 128 rows
-// values CTA: two P tiles, the ring, two boxes for the epilogue
+// values CTA: two P tiles, the ring (whose stages also take the states that leave)
 constexpr uint32_t kOP = 0;
 constexpr uint32_t kORing = 2 * kPBytes;
-constexpr int kOStages = 8;
+constexpr int kOStages = 10;                     // even ones for columns 0 .. 255, odd ones for 256 .. 511
 constexpr uint32_t kOStage = 16384;              // 256 latent columns of 32 bf16 rows or 64 FP8 rows
-constexpr uint32_t kOBox = kORing + kOStages * kOStage;
 // both: per P buffer the rows' factors, sums and four rescale flags (staged and copied like P), then barriers
 constexpr uint32_t kFac = kSRing + kSStages * kBlk;
-static_assert(kFac == kOBox + 2 * kBlk, "the factors sit at one offset in both CTAs");
+static_assert(kFac == kORing + kOStages * kOStage, "the factors sit at one offset in both CTAs");
 constexpr uint32_t kFacSum = 512, kFacFlags = 1024, kFacBytes = 1040;
 constexpr uint32_t kBars = kFac + 2 * kFacBytes;
 enum : uint32_t {
@@ -75,13 +74,13 @@ enum : uint32_t {
   kPFR = 26,    // 2: the PV of the P tile is done (from the values CTA)
   kSTF = 28,    // 2: a staging buffer's last copy landed (from the values CTA)
   // values
-  kCF = 0,      // 8: stage landed
-  kCE = 8,      // 8: the stage's MMAs are done
-  kPF = 16,     // 2: P tile, factors and flags landed
-  kPVD = 18,    // 2: PV of the tile done
-  kCN = 20,     // the control warp handed a tile, or a piece's end, to the correction warps
-  kCD = 21,     // the 8 correction warps rescaled their rows (piece's end: have read the sums)
-  kEP = 22,     // the 8 correction warps have read the piece's O
+  kCF = 0,      // 10: stage landed (or free for a box of states)
+  kCE = 10,     // 10: the stage's MMAs are done (or its box has been read)
+  kPF = 20,     // 2: P tile, factors and flags landed
+  kPVD = 22,    // 2: PV of the tile done
+  kCN = 24,     // the control warp handed a tile, or a piece's end, to the correction warps
+  kCD = 25,     // the 8 correction warps rescaled their rows (piece's end: have read the sums)
+  kEP = 26,     // the 8 correction warps have read the piece's O
   kNBars = 30
 };
 constexpr uint32_t kShared = kBars + 8 * kNBars;   // Start, then the hand-over word
@@ -194,6 +193,9 @@ struct Walk {
   RequestWork w;
   int at, end, first, cluster;
   int lo, hi, g, last_key, acc;   // the piece's tiles; next range, end of the keys so far, tiles so far
+  // stages of each half of the columns that take the piece's states (128 rows of 64 bf16 or 32 fp32), if all of its
+  // rows are live; fewer are written by their threads
+  __device__ __forceinline__ int boxes() const { return rows - row0 < kItemRows ? 0 : slot < 0 ? 4 : 8; }
   __device__ __forceinline__ void start(const Start& s, int cluster_) {
     w = s.w;
     at = s.begin;
@@ -321,6 +323,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 
   if (tid == 0) {
     prefetch_tensormap(scores ? &p.tm_s : &p.tm_o);
+    prefetch_tensormap(scores ? &p.tm_q : &p.tm_part);
+    if (!scores) prefetch_tensormap(&p.tm_lat);
     for (uint32_t i = 0; i < kNBars; ++i) {
       uint32_t cnt = 1;
       if (scores) {
@@ -471,28 +475,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         if (ok && e > 0) ok = await_warp(p, bar(kQE), (e - 1) & 1);
         ++e;
         tc_fence_after();
-        if (k.head) {
-#pragma unroll 1
-          for (int i = 0; i < kQBoxes; ++i, ++u) {
-            const int s = u % kSStages;
-            if (ok) ok = await_warp(p, bar(kSF + s), (u / kSStages) & 1);
-            uint32_t w[32];
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              uint32_t w4[4];
-              lds128(sb + kSRing + s * kBlk + sw128_off((uint32_t)r, (uint32_t)c), w4);
-              w[4 * c] = w4[0]; w[4 * c + 1] = w4[1]; w[4 * c + 2] = w4[2]; w[4 * c + 3] = w4[3];
-            }
-            tmem_st32(tmem + lane_off + 32 * i, w);
-            named_bar_sync(6, 128);   // all rows of the stage are read
-            if (r == 0 && ok) mbar_arrive(bar(kSE + s));
-          }
-        }
         // q_rope as a K-major swizzled block, turned in place by pos - offset (a row is one thread's); FP8
         // scores count in units of the row's scale, so it is divided by that
 #pragma unroll
         for (int c = 0; c < 8; ++c) sts128(sb + kQR + sw128_off((uint32_t)r, (uint32_t)c), x[c].x, x[c].y, x[c].z, x[c].w);
-#pragma unroll 1
+#pragma unroll 2
         for (int c = 0; c < 8; ++c) {
           const uint32_t at = sb + kQR + sw128_off((uint32_t)r, (uint32_t)c);
           uint32_t w4[4];
@@ -505,6 +492,30 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             w4[i] = pack_bf16((x0 * cs - x1 * sn) * rq, (x0 * sn + x1 * cs) * rq);
           }
           sts128(at, w4[0], w4[1], w4[2], w4[3]);
+        }
+        if (k.head) {
+#pragma unroll 1
+          for (int i = 0; i < kQBoxes; i += 2, u += 2) {
+            const int sa = u % kSStages, sc = (u + 1) % kSStages;
+            if (ok) ok = await_warp(p, bar(kSF + sa), (u / kSStages) & 1);
+            if (ok) ok = await_warp(p, bar(kSF + sc), ((u + 1) / kSStages) & 1);
+            uint32_t w[2][32];
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {
+                uint32_t w4[4];
+                lds128(sb + kSRing + (hh ? sc : sa) * kBlk + sw128_off((uint32_t)r, (uint32_t)c), w4);
+                w[hh][4 * c] = w4[0]; w[hh][4 * c + 1] = w4[1]; w[hh][4 * c + 2] = w4[2]; w[hh][4 * c + 3] = w4[3];
+              }
+            tmem_st32(tmem + lane_off + 32 * i, w[0]);
+            tmem_st32(tmem + lane_off + 32 * i + 32, w[1]);
+            named_bar_sync(6, 128);   // all rows of the stages are read
+            if (r == 0 && ok) {
+              mbar_arrive(bar(kSE + sa));
+              mbar_arrive(bar(kSE + sc));
+            }
+          }
         }
         tmem_wait_st();
         fence_proxy_async_smem();
@@ -655,23 +666,33 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       bool ok = true;
       int u = nh;
       while (ok && next_range(p, k)) {
-        const int stages = kOPerTile * k.n;
-        for (int i = 0; i < stages; ++i, u += 2) {
-          const int s = u & (kOStages - 1);
-          const int row = cache_row(p, k.r, k.t0 + kORows * i, k.k_hi);
+        const int stages = kOPerTile * k.n, boxes = k.tail ? k.boxes() : 0;
+        for (int i = 0; i < stages + boxes; ++i, u += 2) {
+          const int s = u % kOStages;
+          const int row = i < stages ? cache_row(p, k.r, k.t0 + kORows * i, k.k_hi) : 0;
           if (u >= kOStages && !await(p, bar(kCE + s), ((u / kOStages) - 1) & 1)) { ok = false; break; }
-          mbar_arrive_expect_tx(bar(kCF + s), kOStage);
-          tma_load_3d(sb + kORing + s * kOStage, &p.tm_o, 0, row, (kLatBlocks / 2) * nh, bar(kCF + s));
+          if (i < stages) {
+            mbar_arrive_expect_tx(bar(kCF + s), kOStage);
+            tma_load_3d(sb + kORing + s * kOStage, &p.tm_o, 0, row, (kLatBlocks / 2) * nh, bar(kCF + s));
+          } else {
+            mbar_arrive(bar(kCF + s));   // the stage is the correction warps'
+          }
         }
       }
-      for (int v = max(nh, u - kOStages); v < u && ok; v += 2) ok = await(p, bar(kCE + (v & (kOStages - 1))), (v / kOStages) & 1);
+      for (int v = u - kOStages < nh ? nh : u - kOStages; v < u && ok; v += 2) ok = await(p, bar(kCE + v % kOStages), (v / kOStages) & 1);
     } else if (warp == 1) {
       // ---------------------------------------------------------- P landed, rows rescaled, O += P c
       volatile int* hand = reinterpret_cast<volatile int*>(smem + kHand);
       const uint64_t pd0 = sdesc_sw128(sb + kOP, 16, 1024);                        // P, K-major
       const uint64_t cd0 = sdesc_sw128(sb + kORing, kORows * 128, 1024);           // latent stages, MN-major
       bool ok = true;
-      int g = 0, u = 0, events = 0, done = 0;   // tiles, stages, hand-overs, finished pieces
+      int g = 0, events = 0, done = 0;   // tiles, hand-overs, finished pieces
+      int s = 0;                         // next stage, and the parity of its fill
+      uint32_t ph = 0;
+      auto advance = [&](int n) {
+        s += n;
+        while (s >= kOStages) { s -= kOStages; ph ^= 1u; }
+      };
       if (lane == 0)
         for (int b = 0; b < 2; ++b) mbar_arrive_expect_tx(bar(kPF + b), kTxP);
       bool head = true;
@@ -713,9 +734,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           for (int i = 0; i < kOPerTile; ++i) {
             if (!ok) break;
 #pragma unroll
-            for (int nh = 0; nh < 2; ++nh, ++u) {
-              const int s = u & (kOStages - 1);
-              if (!await_warp(p, bar(kCF + s), (u / kOStages) & 1)) { ok = false; break; }
+            for (int nh = 0; nh < 2; ++nh) {
+              if (!await_warp(p, bar(kCF + s), ph)) { ok = false; break; }
               // rows outside the run meet P = 0, but may hold anything: they are zeroed
               const int kt = k.t0 + 128 * j + kORows * i;
               const int lo = max(0, k.k_lo - kt), hi = min(kORows, k.k_hi - kt);
@@ -736,6 +756,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 }
               }
               mma_commit_elect(bar(kCE + s));
+              advance(1);
             }
           }
           if (!ok) break;
@@ -743,7 +764,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           mma_commit_elect(bar(kPVD + b));
           mma_commit_mc_elect(bar(kPFR + b), 0x1);
         }
-        if (k.tail) ++done;
+        if (k.tail) {
+          ++done;
+          advance(2 * k.boxes());
+        }
       }
       if (!ok && lane == 0) {
         *hand = -1;
@@ -765,12 +789,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       // ---------------------------------------------------------- rescale O rows; epilogue: columns 256 half ..
       const int half = (warp - 4) >> 2, r = 32 * (warp & 3) + lane;
       const uint32_t o_cols = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 256 * half;
-      const uint32_t box = sb + kOBox + half * kBlk;
       const volatile int* hand = reinterpret_cast<const volatile int*>(smem + kHand);
       bool ok = true;
-      int g = 0, ev = 0;
+      int g = 0, ev = 0, u = half;   // tiles, hand-overs, this half's next stage
       while (next_range(p, k)) {
         g += k.n;
+        u += 2 * kOPerTile * k.n;
         if (!k.tail) continue;   // a piece's states leave at its end
         float lsum = 0.f;
         while (ok) {
@@ -810,55 +834,68 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         const int rows = k.rows - k.row0;      // live rows of the item
         const int64_t orow0 = (int64_t)k.q_begin * H + k.row0;
         const bool whole = k.slot < 0;
-        const bool full = rows >= kItemRows;
-        // 128 live rows leave by TMA stores of staged 128-byte columns (64 bf16 or 32 fp32), fewer by their threads
+        const bool full = k.boxes() > 0;
+        int prev = -1, prev2 = -1;   // the stages whose boxes are being stored
 #pragma unroll 1
-        for (int cc = 0; cc < 8; ++cc) {
-          uint32_t o[32];
-          tmem_ld32(o_cols + 32 * cc, o);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
-          if (cc == 7) {
+        for (int cc = 0; cc < 4; ++cc) {   // 64 columns: one box of bf16, two of fp32
+          uint32_t o[64];
+          tmem_ld64(o_cols + 64 * cc, o);
+          if (cc == 3) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kEP));   // O has been read: the next piece may begin
           }
-          const int col = 256 * half + 32 * cc;
+#pragma unroll
+          for (int i = 0; i < 64; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
+          const int col = 256 * half + 64 * cc;
           if (whole) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = pack_bf16(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
+            for (int i = 0; i < 32; ++i) o[i] = pack_bf16(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
           }
           if (full) {
-            const bool first = !whole || (cc & 1) == 0, last = !whole || (cc & 1) != 0;
-            if (first) {   // the box's last store has read it
-              if (r == 0) bulk_wait_read0();
-              named_bar_sync(3 + half, 128);
-            }
+            const int st = u % kOStages, st2 = (u + 2) % kOStages;
+            const uint32_t box = sb + kORing + st * kOStage, box2 = sb + kORing + st2 * kOStage;
+            if (ok) ok = await_warp(p, bar(kCF + st), (u / kOStages) & 1);
+            if (ok && !whole) ok = await_warp(p, bar(kCF + st2), ((u + 2) / kOStages) & 1);
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-              sts128(box + sw128_off((uint32_t)r, (uint32_t)(c + (whole ? 4 * (cc & 1) : 0))), o[4 * c], o[4 * c + 1],
-                     o[4 * c + 2], o[4 * c + 3]);
+            for (int c = 0; c < 8; ++c)
+              sts128(box + sw128_off((uint32_t)r, (uint32_t)c), o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
             if (!whole) {
 #pragma unroll
-              for (int c = 4; c < 8; ++c)
-                sts128(box + sw128_off((uint32_t)r, (uint32_t)c), o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+              for (int c = 0; c < 8; ++c)
+                sts128(box2 + sw128_off((uint32_t)r, (uint32_t)c), o[32 + 4 * c], o[33 + 4 * c], o[34 + 4 * c], o[35 + 4 * c]);
             }
-            if (last) {
-              fence_proxy_async_smem();
-              named_bar_sync(3 + half, 128);
-              if (r == 0) {
-                if (whole) tma_store_2d(&p.tm_lat, box, col - 32, (int)orow0);
-                else tma_store_2d(&p.tm_part, box, col, k.slot * kItemRows);
-                bulk_commit();
+            fence_proxy_async_smem();
+            named_bar_sync(3 + half, 128);
+            if (r == 0 && ok) {
+              if (whole) {
+                tma_store_2d(&p.tm_lat, box, col, (int)orow0);
+              } else {
+                tma_store_2d(&p.tm_part, box, col, k.slot * kItemRows);
+                tma_store_2d(&p.tm_part, box2, col + 32, k.slot * kItemRows);
               }
+              bulk_commit();
+              if (prev >= 0) {   // the step before has been read: its stages go back
+                bulk_wait_read<1>();
+                mbar_arrive(bar(kCE + prev));
+                if (!whole) mbar_arrive(bar(kCE + prev2));
+              }
+              prev = st;
+              prev2 = st2;
             }
+            u += whole ? 2 : 4;
           } else if (r < rows) {
             uint4* dst = whole ? reinterpret_cast<uint4*>(p.ws.lat + (orow0 + r) * kDc + col)
                                : reinterpret_cast<uint4*>(p.ws.part + ((int64_t)k.slot * kItemRows + r) * kDc + col);
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-              if (c < 4 || !whole) dst[c] = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+            for (int c = 0; c < 16; ++c)
+              if (c < 8 || !whole) dst[c] = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
           }
+        }
+        if (prev >= 0) {
+          bulk_wait_read0();
+          mbar_arrive(bar(kCE + prev));
+          if (!whole) mbar_arrive(bar(kCE + prev2));
         }
       }
       if (r == 0) bulk_wait0();   // every store complete before the CTA's shared memory goes
