@@ -1956,7 +1956,7 @@ int mla_decode(const void* q, const int32_t* q_pos, const void* kv_cache, int kv
     ok &= encode_map(&p.tm_o, fp8 ? byte : bf16, 3, kv_cache, dc, sc, bv, sw);
     const uint64_t dl[2] = {(uint64_t)kDc, n}, dp[2] = {(uint64_t)kDc, (uint64_t)kDecodeSlots * kItemRows};
     const uint64_t sl[1] = {(uint64_t)kDc * 2}, sp[1] = {(uint64_t)kDc * 4};
-    const uint32_t bl[2] = {64, 128}, bp[2] = {32, 128};
+    const uint32_t bl[2] = {64, 32}, bp[2] = {32, 32};
     const uint64_t dq[2] = {(uint64_t)kDc, fp8 ? 2 * n : n}, sq[1] = {fp8 ? (uint64_t)kDc : (uint64_t)kDc * 2};
     const uint32_t bq[2] = {(uint32_t)dc[0], 128};
     ok &= encode_map(&p.tm_q, fp8 ? byte : bf16, 2, space.qlat, dq, sq, bq, sw);

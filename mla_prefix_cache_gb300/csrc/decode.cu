@@ -106,6 +106,8 @@ __device__ __forceinline__ uint32_t bf16_up(float x) {
   return ((int32_t)u >= 0 ? u + 0xFFFFu : u) >> 16;
 }
 
+constexpr int kBoxes = 4;         // values stages of each half of the columns that a piece's states leave through
+
 // Where a cluster's run of units begins: in request r, whose first unit is `first`.
 struct Start {
   int begin, end, first, r;
@@ -193,9 +195,9 @@ struct Walk {
   RequestWork w;
   int at, end, first, cluster;
   int lo, hi, g, last_key, acc;   // the piece's tiles; next range, end of the keys so far, tiles so far
-  // stages of each half of the columns that take the piece's states (128 rows of 64 bf16 or 32 fp32), if all of its
-  // rows are live; fewer are written by their threads
-  __device__ __forceinline__ int boxes() const { return rows - row0 < kItemRows ? 0 : slot < 0 ? 4 : 8; }
+  // stages of each half of the columns that the piece's states leave through, if it has 32 live rows (fewer are
+  // written by their threads)
+  __device__ __forceinline__ int boxes() const { return rows - row0 < 32 ? 0 : kBoxes; }
   __device__ __forceinline__ void start(const Start& s, int cluster_) {
     w = s.w;
     at = s.begin;
@@ -232,13 +234,23 @@ __device__ __noinline__ bool next_range(const DecodeParams& p, Walk& k) {
       k.slot = (k.lo == 0 && k.hi == k.w.tiles) ? -1 : 2 * k.cluster + (k.lo == 0 ? 1 : 0);
       break;
     }
+    k.head = true;
     k.q_begin = k.w.q_begin;
     k.rows = k.w.q_count * p.batch.num_heads;
     k.len = k.w.len;
+    if (k.w.sg.x == k.w.sg.y) {   // no segments: one range
+      k.t0 = 128 * k.lo;
+      k.n = k.hi - k.lo;
+      k.k_lo = 0;
+      k.k_hi = k.len;
+      k.offset = 0;
+      k.tail = true;
+      k.acc = k.hi;
+      return true;
+    }
     k.g = k.w.sg.x;
     k.last_key = 0;
     k.acc = 0;
-    k.head = true;
     // ranges before the piece's first tile
     while (k.g <= k.w.sg.y) {
       const KeyRange kr = request_range(p.batch, k.w.sg, k.g, k.last_key, k.len);
@@ -337,14 +349,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     }
     fence_mbar_init();
   }
-  const bool cut = schedule(p, start, reinterpret_cast<int*>(smem), cluster);
-  cluster_sync_all();   // both CTAs' barriers exist before either is signalled
   if (warp == 2) {
     tmem_alloc(smem_u32(&start->tmem), 512);
     tmem_relinquish();
   }
   tc_fence_before();
-  __syncthreads();
+  const bool cut = schedule(p, start, reinterpret_cast<int*>(smem), cluster);
+  cluster_sync_all();   // both CTAs' barriers exist before either is signalled
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&start->tmem);
   Walk k;
@@ -834,71 +845,72 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         const int rows = k.rows - k.row0;      // live rows of the item
         const int64_t orow0 = (int64_t)k.q_begin * H + k.row0;
         const bool whole = k.slot < 0;
-        const bool full = k.boxes() > 0;
-        int prev = -1, prev2 = -1;   // the stages whose boxes are being stored
+        const int boxes = k.boxes();
+        // A warp of 32 live rows stages 128 bytes of each (32 fp32 or 64 bf16 columns) in its quarter of a box and
+        // stores them by TMA, four boxes in turn, at its own pace; a warp with fewer writes them by its threads.
+        // (One box for all 128 rows, with a barrier a step, took 5 us a piece.)
+        const bool tma = 32 * (warp & 3) + 32 <= rows;
+        if (boxes > 0 && ok) {   // the loading thread hands the stages over in order
 #pragma unroll 1
-        for (int cc = 0; cc < 4; ++cc) {   // 64 columns: one box of bf16, two of fp32
-          uint32_t o[64];
-          tmem_ld64(o_cols + 64 * cc, o);
-          if (cc == 3) {
+          for (int b = 0; b < kBoxes; ++b) ok = ok && await_warp(p, bar(kCF + (u + 2 * b) % kOStages), ((u + 2 * b) / kOStages) & 1);
+        }
+#pragma unroll 1
+        for (int cc = 0; cc < 8; ++cc) {
+          uint32_t o[32];
+          tmem_ld32(o_cols + 32 * cc, o);
+          if (cc == 7) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kEP));   // O has been read: the next piece may begin
           }
 #pragma unroll
-          for (int i = 0; i < 64; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
-          const int col = 256 * half + 64 * cc;
+          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
+          const int col = 256 * half + 32 * cc;
           if (whole) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = pack_bf16(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
+            for (int i = 0; i < 16; ++i) o[i] = pack_bf16(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
           }
-          if (full) {
-            const int st = u % kOStages, st2 = (u + 2) % kOStages;
-            const uint32_t box = sb + kORing + st * kOStage, box2 = sb + kORing + st2 * kOStage;
-            if (ok) ok = await_warp(p, bar(kCF + st), (u / kOStages) & 1);
-            if (ok && !whole) ok = await_warp(p, bar(kCF + st2), ((u + 2) / kOStages) & 1);
+          if (tma) {
+            const int b = whole ? cc >> 1 : cc & 3;
+            const uint32_t box = sb + kORing + (uint32_t)((u + 2 * b) % kOStages) * kOStage + (uint32_t)(warp & 3) * 4096;
+            if (!whole && cc >= 4) {   // the box's store of four steps ago has read it
+              if (lane == 0) bulk_wait_read<3>();
+              __syncwarp();
+            }
+            const uint32_t c0 = whole ? 4 * (cc & 1) : 0;
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-              sts128(box + sw128_off((uint32_t)r, (uint32_t)c), o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+            for (int c = 0; c < 4; ++c)
+              sts128(box + sw128_off((uint32_t)lane, c0 + c), o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
             if (!whole) {
 #pragma unroll
-              for (int c = 0; c < 8; ++c)
-                sts128(box2 + sw128_off((uint32_t)r, (uint32_t)c), o[32 + 4 * c], o[33 + 4 * c], o[34 + 4 * c], o[35 + 4 * c]);
+              for (int c = 4; c < 8; ++c)
+                sts128(box + sw128_off((uint32_t)lane, (uint32_t)c), o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
             }
-            fence_proxy_async_smem();
-            named_bar_sync(3 + half, 128);
-            if (r == 0 && ok) {
-              if (whole) {
-                tma_store_2d(&p.tm_lat, box, col, (int)orow0);
-              } else {
-                tma_store_2d(&p.tm_part, box, col, k.slot * kItemRows);
-                tma_store_2d(&p.tm_part, box2, col + 32, k.slot * kItemRows);
+            if (!whole || (cc & 1)) {
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0 && ok) {
+                if (whole) tma_store_2d(&p.tm_lat, box, col - 32, (int)orow0 + 32 * (warp & 3));
+                else tma_store_2d(&p.tm_part, box, col, k.slot * kItemRows + 32 * (warp & 3));
+                bulk_commit();
               }
-              bulk_commit();
-              if (prev >= 0) {   // the step before has been read: its stages go back
-                bulk_wait_read<1>();
-                mbar_arrive(bar(kCE + prev));
-                if (!whole) mbar_arrive(bar(kCE + prev2));
-              }
-              prev = st;
-              prev2 = st2;
             }
-            u += whole ? 2 : 4;
           } else if (r < rows) {
             uint4* dst = whole ? reinterpret_cast<uint4*>(p.ws.lat + (orow0 + r) * kDc + col)
                                : reinterpret_cast<uint4*>(p.ws.part + ((int64_t)k.slot * kItemRows + r) * kDc + col);
 #pragma unroll
-            for (int c = 0; c < 16; ++c)
-              if (c < 8 || !whole) dst[c] = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+            for (int c = 0; c < 8; ++c)
+              if (c < 4 || !whole) dst[c] = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
           }
         }
-        if (prev >= 0) {
-          bulk_wait_read0();
-          mbar_arrive(bar(kCE + prev));
-          if (!whole) mbar_arrive(bar(kCE + prev2));
+        if (boxes > 0) {   // the stages go back once every warp's stores have read them
+          if (lane == 0) bulk_wait_read0();
+          named_bar_sync(3 + half, 128);
+          if (r < kBoxes && ok) mbar_arrive(bar(kCE + (u + 2 * r) % kOStages));
+          u += 2 * kBoxes;
         }
       }
-      if (r == 0) bulk_wait0();   // every store complete before the CTA's shared memory goes
+      if (lane == 0) bulk_wait0();   // every store complete before the CTA's shared memory goes
     }
   }
   tc_fence_before();

@@ -103,7 +103,7 @@ struct RequestWork {
   int2 sg;
   __device__ __forceinline__ int units() const { return tiles > 0 ? tiles + kItemUnits : 0; }
 };
-__device__ __forceinline__ RequestWork request_work(const DecodeBatch& b, int r) {
+static __device__ __noinline__ RequestWork request_work(const DecodeBatch& b, int r) {
   RequestWork w;
   const int2 rr = request_rows(b.rows, r);
   w.q_begin = rr.x;
@@ -111,6 +111,10 @@ __device__ __forceinline__ RequestWork request_work(const DecodeBatch& b, int r)
   w.len = min(max(__ldg(b.rows.seq_lens + r), 0), b.max_blocks * kBlock);
   w.sg = request_segments(b, r);
   w.items = (w.q_count * b.num_heads + kItemRows - 1) / kItemRows;
+  if (w.sg.x == w.sg.y) {
+    w.tiles = (w.len + 127) >> 7;
+    return w;
+  }
   w.tiles = 0;
   int end = 0;
 #pragma unroll 2

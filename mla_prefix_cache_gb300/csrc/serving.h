@@ -67,8 +67,8 @@ struct DecodeParams {
   CUtensorMap tm_q;      // qlat as [rows * H][512] bf16, or [2 * rows * H][512] bytes, box 128 B x 128
   CUtensorMap tm_s;      // the cache's rows in blocks of 128 B, box 128 B x 64 rows x 1
   CUtensorMap tm_o;      // the same, box 128 B x 32 rows x 4 (bf16) or 128 B x 64 rows x 2 (FP8)
-  CUtensorMap tm_lat;    // lat as [rows * H][512], box 64 x 128
-  CUtensorMap tm_part;   // part as [kDecodeSlots * 128][512], box 32 x 128
+  CUtensorMap tm_lat;    // lat as [rows * H][512], box 64 x 32
+  CUtensorMap tm_part;   // part as [kDecodeSlots * 128][512], box 32 x 32
   DecodeBatch batch;
   DecodeSpace ws;
   const uint16_t* q;             // [rows][H][192], q_rope not rotated
