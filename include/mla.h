@@ -463,7 +463,7 @@ int mla_block_compare(const void* kv_cache, int kv_dtype, int num_blocks, const 
  *       (norm_weight NULL: c = x[0..511], normalised already or not at all);
  *   k = R(pos) x[512..575], interleaved pairs (2k, 2k+1) turned by
  *       pos * theta^(-2k/64);
- *   a bf16 row holds bf16(c) and bf16(k); an FP8 row E4M3(c / kv_scale),
+ *   a bf16 row holds bf16(c) and bf16(k); an FP8 row E4M3(c * (1 / kv_scale)),
  *   saturated to +-448, and bf16(k).  fp32 arithmetic, each stored value
  *   rounded once, to nearest even.
  * The lengths and tables are read on the device, so the call can be captured

@@ -115,6 +115,8 @@ _lib = None
 def load(path: str = LIB_PATH) -> ctypes.CDLL:
     """Loads libmla.so (once) and binds every declared signature."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

@@ -335,27 +335,57 @@ def block_compare(kv_cache: torch.Tensor, block_a: torch.Tensor, block_b: torch.
 
 # ------------------------------------------------------------------ serving
 
-def _same_device(device: torch.device, **tensors) -> None:
-    """The serving calls launch on the current device: their tensors have to be there."""
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
+# These calls sit in a decoding loop whose kernels take a few microseconds: their checks are one pass over each
+# tensor and pointers go to the library as plain integers.
+
+def _at(t: torch.Tensor, name: str, device: int, dtype, shape=None) -> int:
+    """Address of a contiguous tensor of `dtype` (and `shape`) on CUDA device `device`."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
+    if dtype is not None and t.dtype is not dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
-def _batch_args(block_table: torch.Tensor, seq_lens: torch.Tensor, cu_q: Optional[torch.Tensor], rows: int):
-    """Checked (num_reqs, max_blocks, seq_lens, cu_q pointers) of a serving call."""
+def _current(t: torch.Tensor, name: str) -> int:
+    """The device of `t`, which has to be the current one: the call launches there."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    device = t.get_device()
+    if device != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return device
+
+
+def _stream_on(device: int, stream: Optional[torch.cuda.Stream]) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    if stream.device.index != device:
+        raise ValueError(f"stream is on {stream.device}, expected cuda:{device}")
+    return stream.cuda_stream
+
+
+def _batch_args(block_table, seq_lens, cu_q, rows: int, device: int):
+    """Checked (num_reqs, block_table, max_blocks, seq_lens, cu_q) of a serving call."""
+    bt, sl = _at(block_table, "block_table", device, torch.int32), _at(seq_lens, "seq_lens", device, torch.int32)
     if block_table.dim() != 2 or seq_lens.dim() != 1 or block_table.shape[0] != seq_lens.shape[0]:
         raise ValueError("block_table must be [num_reqs, max_blocks] and seq_lens [num_reqs]")
-    B = int(seq_lens.shape[0])
-    if cu_q is None:
-        if rows and (B == 0 or rows % B):
-            raise ValueError(f"{rows} rows cannot be shared evenly by {B} requests: pass cu_q")
-    elif cu_q.dim() != 1 or cu_q.shape[0] != B + 1:
-        raise ValueError("cu_q must be [num_reqs + 1]")
-    return (B, int(block_table.shape[1]), _dev(seq_lens, "seq_lens", torch.int32),
-            None if cu_q is None else _dev(cu_q, "cu_q", torch.int32))
+    B, max_blocks = block_table.shape
+    if cu_q is not None:
+        return B, bt, max_blocks, sl, _at(cu_q, "cu_q", device, torch.int32, (B + 1,))
+    if rows and (B == 0 or rows % B):
+        raise ValueError(f"{rows} rows cannot be shared evenly by {B} requests: pass cu_q")
+    return B, bt, max_blocks, sl, None
+
+
+def _error_word(t: torch.Tensor, device: int) -> int:
+    return _at(t, "dev_error", device, torch.uint32 if t.dtype is torch.uint32 else torch.int32)
 
 
 def cache_append(kv: torch.Tensor, pos: torch.Tensor, kv_cache: torch.Tensor, block_table: torch.Tensor,
@@ -372,27 +402,26 @@ def cache_append(kv: torch.Tensor, pos: torch.Tensor, kv_cache: torch.Tensor, bl
     uint8 [NB,64,640]; block_table int32 [B, max_blocks]; seq_lens int32 [B],
     new rows included, and cu_q int32 [B+1] (default: rows / B each) on the
     device.  Returns kv_cache."""
-    if not isinstance(kv, torch.Tensor) or not kv.is_cuda:
-        raise ValueError("kv must be a CUDA tensor")
-    if kv.dim() != 2 or kv.shape[1] != 576 or kv.dtype != torch.bfloat16 or (kv.shape[0] and kv.stride(1) != 1):
+    device = _current(kv, "kv")
+    if kv.dim() != 2 or kv.dtype is not torch.bfloat16:
+        raise ValueError("kv must be bf16 [rows, 576]")
+    rows, cols = kv.shape
+    stride, unit = kv.stride()
+    if cols != 576 or (rows and unit != 1):
         raise ValueError("kv must be bf16 [rows, 576] with unit column stride")
-    rows = int(kv.shape[0])
-    if pos.shape != (rows,):
-        raise ValueError("pos must be [rows]")
-    if norm_weight is not None and norm_weight.shape != (512,):
-        raise ValueError("norm_weight must be [512]")
-    _same_device(kv.device, pos=pos, kv_cache=kv_cache, block_table=block_table, seq_lens=seq_lens, cu_q=cu_q,
-                 norm_weight=norm_weight, dev_error=dev_error)
-    B, max_blocks, sl, cq = _batch_args(block_table, seq_lens, cu_q, rows)
-    stride = int(kv.stride(0)) if rows > 1 else 576
-    if rows > 1 and (stride < 576 or stride % 8):
+    if rows < 2:
+        stride = 576
+    elif stride < 576 or stride % 8:
         raise ValueError("kv rows must be a multiple of 8 elements, at least 576, apart")
-    _lib.check("mla_cache_append", _lib.load().mla_cache_append(
-        ctypes.c_void_p(kv.data_ptr()), stride, _dev(pos, "pos", torch.int32),
-        None if norm_weight is None else _dev(norm_weight, "norm_weight", torch.bfloat16), float(norm_eps), cq, sl, B,
-        rows, _dev(block_table, "block_table", torch.int32), max_blocks, float(rope_theta), _dev(kv_cache, "kv_cache"),
-        kv_dtype_code(kv_cache), float(kv_scale), int(kv_cache.shape[0]),
-        None if dev_error is None else _dev(dev_error, "dev_error", (torch.int32, torch.uint32)), _stream_ptr(stream)))
+    B, bt, max_blocks, sl, cq = _batch_args(block_table, seq_lens, cu_q, rows, device)
+    st = _lib.load().mla_cache_append(
+        kv.data_ptr(), stride, _at(pos, "pos", device, torch.int32, (rows,)),
+        None if norm_weight is None else _at(norm_weight, "norm_weight", device, torch.bfloat16, (512,)), norm_eps, cq,
+        sl, B, rows, bt, max_blocks, rope_theta, _at(kv_cache, "kv_cache", device, None), kv_dtype_code(kv_cache),
+        kv_scale, kv_cache.shape[0], None if dev_error is None else _error_word(dev_error, device),
+        _stream_on(device, stream))
+    if st:
+        _lib.check("mla_cache_append", st)
     return kv_cache
 
 
@@ -419,48 +448,38 @@ def decode(q: torch.Tensor, q_pos: torch.Tensor, kv_cache: torch.Tensor, block_t
     [S, 3] (start, length, rope offset) with seg_ptr int32 [B+1], on the device.
     Returns out [T_q, H, 128], and lse fp32 [T_q, H] with it when return_lse is
     set or lse is given."""
-    if not isinstance(q, torch.Tensor) or not q.is_cuda:
-        raise ValueError("q must be a CUDA tensor")
+    device = _current(q, "q")
     if q.dim() != 3 or q.shape[2] != 192:
         raise ValueError("q must be [T_q, H, 192]")
-    T_q, H, dev = int(q.shape[0]), int(q.shape[1]), q.device
-    if q_pos.shape != (T_q,):
-        raise ValueError("q_pos must be [T_q]")
-    if kv_b_proj.shape != (512, H * 256):
-        raise ValueError("kv_b_proj must be [512, H*256]")
+    T_q, H, _ = q.shape
     if (segments is None) != (seg_ptr is None):
         raise ValueError("segments and seg_ptr go together")
-    _same_device(dev, q_pos=q_pos, kv_cache=kv_cache, block_table=block_table, seq_lens=seq_lens,
-                 kv_b_proj=kv_b_proj, cu_q=cu_q, segments=segments, seg_ptr=seg_ptr, out=out, lse=lse,
-                 workspace=workspace)
-    B, max_blocks, sl, cq = _batch_args(block_table, seq_lens, cu_q, T_q)
+    B, bt, max_blocks, sl, cq = _batch_args(block_table, seq_lens, cu_q, T_q, device)
     sp = gp = None
     ns = 0
     if segments is not None:
-        if segments.dim() != 2 or segments.shape[1] != 3 or seg_ptr.shape != (B + 1,):
-            raise ValueError("segments must be [S, 3] and seg_ptr [num_reqs + 1]")
-        ns, sp, gp = int(segments.shape[0]), _dev(segments, "segments", torch.int64), _dev(seg_ptr, "seg_ptr", torch.int32)
+        ns = segments.shape[0]
+        sp = _at(segments, "segments", device, torch.int64, (ns, 3))
+        gp = _at(seg_ptr, "seg_ptr", device, torch.int32, (B + 1,))
         if ns == 0:      # an empty tensor has no address: any one will do, nothing of it is read
             sp = gp
     if out is None:
-        out = torch.empty((T_q, H, 128), dtype=out_dtype, device=dev)
-    elif out.shape != (T_q, H, 128):
-        raise ValueError("out must be [T_q, H, 128]")
+        out = torch.empty((T_q, H, 128), dtype=out_dtype, device=q.device)
     if lse is None and return_lse:
-        lse = torch.empty((T_q, H), dtype=torch.float32, device=dev)
-    elif lse is not None and lse.shape != (T_q, H):
-        raise ValueError("lse must be [T_q, H]")
+        lse = torch.empty((T_q, H), dtype=torch.float32, device=q.device)
     if workspace is None:
-        workspace = torch.empty(decode_workspace_size(B, T_q, H), dtype=torch.uint8, device=dev)
-    od = OUT_BF16 if out.dtype == torch.bfloat16 else OUT_FP32
-    _lib.check("mla_decode", _lib.load().mla_decode(
-        _dev(q, "q", torch.bfloat16), _dev(q_pos, "q_pos", torch.int32), _dev(kv_cache, "kv_cache"),
-        kv_dtype_code(kv_cache), float(kv_scale), int(kv_cache.shape[0]),
-        _dev(block_table, "block_table", torch.int32), max_blocks, sl, cq, B, T_q, H, sp, gp, ns,
-        _dev(kv_b_proj, "kv_b_proj", torch.bfloat16), float(softmax_scale), float(rope_theta),
-        _dev(out, "out", (torch.float32, torch.bfloat16)), od,
-        None if lse is None else _dev(lse, "lse", torch.float32), _dev(workspace, "workspace"),
-        workspace.numel() * workspace.element_size(), _stream_ptr(stream)))
+        workspace = torch.empty(decode_workspace_size(B, T_q, H), dtype=torch.uint8, device=q.device)
+    bf16 = out.dtype is torch.bfloat16
+    st = _lib.load().mla_decode(
+        _at(q, "q", device, torch.bfloat16), _at(q_pos, "q_pos", device, torch.int32, (T_q,)),
+        _at(kv_cache, "kv_cache", device, None), kv_dtype_code(kv_cache), kv_scale, kv_cache.shape[0], bt, max_blocks,
+        sl, cq, B, T_q, H, sp, gp, ns, _at(kv_b_proj, "kv_b_proj", device, torch.bfloat16, (512, H * 256)),
+        softmax_scale, rope_theta, _at(out, "out", device, torch.bfloat16 if bf16 else torch.float32, (T_q, H, 128)),
+        OUT_BF16 if bf16 else OUT_FP32, None if lse is None else _at(lse, "lse", device, torch.float32, (T_q, H)),
+        _at(workspace, "workspace", device, None), workspace.numel() * workspace.element_size(),
+        _stream_on(device, stream))
+    if st:
+        _lib.check("mla_decode", st)
     decode.last_workspace = workspace
     return out if lse is None else (out, lse)
 

@@ -1843,7 +1843,7 @@ int mla_cache_append(const void* kv, int64_t kv_row_stride, const int32_t* pos, 
   p.max_blocks = max_blocks_per_req;
   p.cache = static_cast<uint8_t*>(kv_cache);
   p.num_blocks = num_blocks;
-  p.kv_scale = kv_scale;
+  p.inv_scale = 1.f / kv_scale;
   p.err = dev_error;
   rope_fracs((double)rope_theta, p.rope_frac);
   return cuda_status(launch_cache_append(p, kv_dtype == MLA_KV_FP8_E4M3, reinterpret_cast<cudaStream_t>(stream)));

@@ -28,7 +28,7 @@ struct AppendParams {
   int max_blocks;
   uint8_t* cache;
   int num_blocks;
-  float kv_scale;
+  float inv_scale;               // 1 / kv_scale
   uint32_t* err;                 // optional
   uint64_t rope_frac[kDr / 2];
 };
