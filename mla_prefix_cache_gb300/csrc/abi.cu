@@ -1969,7 +1969,6 @@ int mla_decode(const void* q, const int32_t* q_pos, const void* kv_cache, int kv
   qp.qscale = fp8 ? space.qscale : nullptr;
   qp.err = space.err;
   qp.clear = space.err;
-  qp.two = 1;
   qp.scale = 1.f;
   qp.row0 = 0;
   qp.tokens = total_q;

@@ -6,70 +6,79 @@
 // seq_lens[r] - n_r + i of request r for its row i of n_r.  Sums and products
 // are fp32; every stored value is rounded once, to nearest even.
 //
-// One warp takes a row, 16 latent values and one RoPE pair a lane, in 16-byte
-// and 4-byte accesses that are contiguous over the warp; large batches give a
-// warp four rows, all of whose loads are issued before the first row's request
-// and block are looked up (five dependent loads, which a wave of short warps
-// would pay each).  HBM-bound: 1152 B read and 1152 (bf16) or 640 B (FP8)
-// written a row.
+// One warp takes some consecutive rows (one in a small batch), 16 latent values
+// and one RoPE pair a lane, in 16-byte and 4-byte accesses that are contiguous
+// over the warp.  The next row's loads are in flight while a row is computed,
+// and a request and a block are looked up when they change only (a row with its
+// own five dependent loads took 39 us for 62,731 FP8 rows, four rows a warp with
+// all loads first and 100 registers 35).  HBM-bound: 1152 B read and 1152 (bf16)
+// or 640 B (FP8) written a row.
 #include "serving.cuh"
 
 namespace mla {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kManyRows = 8192;   // from here on a warp takes four rows
+constexpr int kBlocksPerSm = 4;
 
-template <bool kFp8, int kRows>
-__global__ void __launch_bounds__(32 * kWarps) cache_append_kernel(const __grid_constant__ AppendParams p) {
+struct Row {   // latent values 8 l .. 8 l + 7 and 256 + 8 l .., RoPE pair l
+  uint4 a, b;
+  uint32_t kr;
+  int pos;
+};
+__device__ __forceinline__ Row load_row(const AppendParams& p, int row, int lane) {
+  const uint16_t* x = p.kv + (int64_t)row * p.row_stride;
+  Row r;
+  r.a = __ldg(reinterpret_cast<const uint4*>(x) + lane);
+  r.b = __ldg(reinterpret_cast<const uint4*>(x) + 32 + lane);
+  r.kr = __ldg(reinterpret_cast<const uint32_t*>(x + kDc) + lane);
+  r.pos = __ldg(p.pos + row);
+  return r;
+}
+
+template <bool kFp8>
+__global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm) cache_append_kernel(const __grid_constant__ AppendParams p) {
   const int lane = threadIdx.x & 31;
-  const int row0 = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * kRows;
-  const int n = min(kRows, p.batch.rows - row0);
-  if (n <= 0) return;
-  // latent values 8 l .. 8 l + 7 and 256 + 8 l .., RoPE pair l
-  uint4 a[kRows], b[kRows];
-  uint32_t kr[kRows];
-  int pos[kRows];
-#pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    if (i < n) {
-      const uint16_t* x = p.kv + (int64_t)(row0 + i) * p.row_stride;
-      a[i] = __ldg(reinterpret_cast<const uint4*>(x) + lane);
-      b[i] = __ldg(reinterpret_cast<const uint4*>(x) + 32 + lane);
-      kr[i] = __ldg(reinterpret_cast<const uint32_t*>(x + kDc) + lane);
-      pos[i] = __ldg(p.pos + row0 + i);
-    }
+  const int first = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * p.per_warp;
+  const int end = min(first + p.per_warp, p.batch.rows);
+  if (first >= end) {
+    grid_wait();    // every CTA: the next dependent kernel counts on this grid's wait
+    return;
   }
+  grid_wait();      // launched dependently: the inputs are there
+  grid_trigger();
+  Row next = load_row(p, first, lane);
   uint4 ga = make_uint4(0, 0, 0, 0), gb = ga;
   const bool norm = p.norm_weight != nullptr;
   if (norm) {
     ga = __ldg(reinterpret_cast<const uint4*>(p.norm_weight) + lane);
     gb = __ldg(reinterpret_cast<const uint4*>(p.norm_weight) + 32 + lane);
   }
-  int r = request_of_row(p.batch, row0, lane);
-  int2 rr = r >= 0 ? request_rows(p.batch, r) : make_int2(0, 0);
-  int len = r >= 0 ? __ldg(p.batch.seq_lens + r) : 0;
-#pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    const int row = row0 + i;
-    if (i >= n) break;
-    if (i > 0 && row >= rr.y) {   // the next row's request
+  const uint64_t frac = p.rope_frac[lane];
+  int r = -1, past = first, len = 0;        // request, one past its last row, its tokens
+  int lb = -1, id = -1;                     // block of the request, and its id
+  for (int row = first; row < end; ++row) {
+    const Row x = next;
+    if (row + 1 < end) next = load_row(p, row + 1, lane);
+    if (row >= past) {
       r = request_of_row(p.batch, row, lane);
-      if (r >= 0) {
-        rr = request_rows(p.batch, r);
-        len = __ldg(p.batch.seq_lens + r);
+      if (r < 0) return;                    // behind the last request, and so are the rows after it
+      past = request_rows(p.batch, r).y;
+      len = __ldg(p.batch.seq_lens + r);
+      lb = -1;
+    }
+    const int tok = len - (past - row);
+    if (tok < 0) continue;                  // a padded request: its length does not hold this row
+    if (tok >> 6 != lb) {
+      lb = tok >> 6;
+      id = lb < p.max_blocks ? __ldg(p.block_table + (int64_t)r * p.max_blocks + lb) : -1;
+      if (id < 0 || id >= p.num_blocks) {
+        id = -1;
+        if (lane == 0 && p.err != nullptr) atomicOr(p.err, kErrBadBlock);
       }
     }
-    if (r < 0) return;            // behind the last request, and so are the rows after it
-    const int tok = len - (rr.y - row);
-    if (tok < 0) continue;        // a padded request: its length does not hold this row
-    const int lb = tok >> 6;
-    const int id = lb < p.max_blocks ? __ldg(p.block_table + (int64_t)r * p.max_blocks + lb) : -1;
-    if (id < 0 || id >= p.num_blocks) {
-      if (lane == 0 && p.err != nullptr) atomicOr(p.err, kErrBadBlock);
-      continue;
-    }
-    const uint32_t w[8] = {a[i].x, a[i].y, a[i].z, a[i].w, b[i].x, b[i].y, b[i].z, b[i].w};
+    if (id < 0) continue;
+    const uint32_t w[8] = {x.a.x, x.a.y, x.a.z, x.a.w, x.b.x, x.b.y, x.b.z, x.b.w};
     float v[16];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
@@ -96,8 +105,8 @@ __global__ void __launch_bounds__(32 * kWarps) cache_append_kernel(const __grid_
       for (int k = 0; k < 16; ++k) v[k] *= f;
     }
     float sn, cs;
-    rope_sincos_sfu(pos[i], p.rope_frac[lane], &sn, &cs);
-    const float x0 = bf16_lo(kr[i]), x1 = bf16_hi(kr[i]);
+    rope_sincos_sfu(x.pos, frac, &sn, &cs);
+    const float x0 = bf16_lo(x.kr), x1 = bf16_hi(x.kr);
     const uint32_t k2 = pack_bf16(x0 * cs - x1 * sn, x0 * sn + x1 * cs);
 
     uint8_t* dst = p.cache + ((int64_t)id * kBlock + (tok & (kBlock - 1))) * (kFp8 ? kRowBytesFp8 : kRowBytesBf16);
@@ -119,21 +128,15 @@ __global__ void __launch_bounds__(32 * kWarps) cache_append_kernel(const __grid_
   }
 }
 
-template <bool kFp8, int kRows>
-void launch(const AppendParams& p, cudaStream_t s) {
-  const int grid = (p.batch.rows + kWarps * kRows - 1) / (kWarps * kRows);
-  cache_append_kernel<kFp8, kRows><<<grid, 32 * kWarps, 0, s>>>(p);
-}
-
 }  // namespace
 
-cudaError_t launch_cache_append(const AppendParams& p, bool fp8, cudaStream_t s) {
+cudaError_t launch_cache_append(AppendParams p, bool fp8, cudaStream_t s) {
   if (p.batch.rows == 0) return cudaSuccess;
-  const bool many = p.batch.rows >= kManyRows;
-  if (fp8) many ? launch<true, 4>(p, s) : launch<true, 1>(p, s);
-  else many ? launch<false, 4>(p, s) : launch<false, 1>(p, s);
-  count_launch();
-  return cudaGetLastError();
+  // as many rows a warp as one wave of CTAs on a GB300's 152 SMs leaves it
+  constexpr int kMostWarps = 152 * kBlocksPerSm * kWarps;
+  p.per_warp = (p.batch.rows + kMostWarps - 1) / kMostWarps;
+  const int grid = ((p.batch.rows + p.per_warp - 1) / p.per_warp + kWarps - 1) / kWarps;
+  return launch_dependent(fp8 ? cache_append_kernel<true> : cache_append_kernel<false>, dim3(grid), 32 * kWarps, 0, p, s);
 }
 
 }  // namespace mla

@@ -127,6 +127,7 @@ __device__ bool schedule(const DecodeParams& p, Start* st, int* scratch, int clu
   RequestWork w;
   int sum = 0;
   bool cut = false;   // a sequence longer than its table
+#pragma unroll 1
   for (int r = r0; r < r1; ++r) {
     w = request_work(p.batch, r);
     sum += w.units() * w.items;
@@ -162,6 +163,7 @@ __device__ bool schedule(const DecodeParams& p, Start* st, int* scratch, int clu
   if (mine || blockIdx.x == 0) {
     int at = pre;
     bool found = false;
+#pragma unroll 1
     for (int r = r0; r < r1; ++r) {
       if (k > 1) w = request_work(p.batch, r);
       if (blockIdx.x == 0) p.ws.first[r] = at;
@@ -360,9 +362,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&start->tmem);
   Walk k;
   k.start(*start, cluster);
-  grid_wait();      // the queries' kernel is done (it also clears the error word)
-  grid_trigger();   // decode_out_kernel may take SMs as they fall free
-  if (cut && blockIdx.x == 0) atomicOr(p.ws.err, kErrBadBlock);
+  if (cut && blockIdx.x == 0) {
+    grid_wait();
+    atomicOr(p.ws.err, kErrBadBlock);
+  }
 
   if (scores) {
     if ((warp == 0 || warp == 3) && lane == 0) {
@@ -379,6 +382,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         return true;
       };
       while (ok && next_range(p, k)) {
+        grid_wait();      // qlat is there, and the error word cleared
+        grid_trigger();   // decode_out_kernel may take SMs as they fall free
         const int qrow = k.q_begin * H + k.row0;
         for (int i = 0; k.head && i < kQBoxes; ++i, ++u) {
           if ((u & 1) != mine) continue;
@@ -427,19 +432,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             tc_fence_after();
             const uint64_t sd = sdesc_add(sd0, s * kBlk);
             const uint32_t qa = tmem + 32 * blk;
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              const uint64_t bd = sdesc_add(sd, kk * 32);
-              const uint32_t acc = (blk | kk) ? 1u : 0u;
-              if (blk >= kLatBlocks) {
-                mma_ss_elect(d, sdesc_add(qd, kk * 32), bd, kIdS, 1u);
-              } else if (kFp8) {
-                mma_ts_8bit_elect(d, qa + 8 * kk, bd, kIdS8, acc);
-                mma_ts_8bit_elect(d, qa + 128 + 8 * kk, bd, kIdS8, 1u);
-              } else {
-                mma_ts_elect(d, qa + 8 * kk, bd, kIdS, acc);
-              }
-            }
+            if (blk >= kLatBlocks) mma_ss4_elect(d, qd, sd, kIdS, 1u);
+            else if (kFp8) mma_ts4x2_8bit_elect(d, qa, sd, kIdS8, blk ? 1u : 0u);
+            else mma_ts4_elect(d, qa, sd, kIdS, blk ? 1u : 0u);
             mma_commit_elect(bar(kSE + s));
             if (++s == kSStages) { s = 0; ph ^= 1u; }
           }
@@ -476,6 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         const bool live = prow < k.rows;
         const int64_t grow = (int64_t)k.q_begin + (live ? prow / H : 0);
         const int64_t orow = (int64_t)k.q_begin * H + prow;
+        if (kFp8) grid_wait();   // for the queries' scales
         const float rq = kFp8 && live ? 1.f / (p.ws.qscale[orow] * p.kv_scale) : 1.f;
         const uint4* qr = reinterpret_cast<const uint4*>(p.q + orow * kDqk + kDnope);
         const int64_t delta = live ? (int64_t)__ldg(p.q_pos + grow) - k.offset : 0;
@@ -550,6 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         const int prow = k.row0 + r;
         const bool live = prow < k.rows;
         const int64_t orow = (int64_t)k.q_begin * H + prow;
+        if (kFp8) grid_wait();   // for the queries' scales
         const float sl2 = p.scale_log2 * (kFp8 && live ? p.ws.qscale[orow] * p.kv_scale : 1.f);
         const int qk = live ? k.len - (k.rows - 1 - prow) / H - 1 : -1;   // the last key token the row sees
         const int n = k.n, t0 = k.t0, k_lo = k.k_lo, k_hi = k.k_hi, slot = k.slot;
@@ -677,6 +674,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       bool ok = true;
       int u = nh;
       while (ok && next_range(p, k)) {
+        grid_wait();   // the error word is cleared
+        grid_trigger();
         const int stages = kOPerTile * k.n, boxes = k.tail ? k.boxes() : 0;
         for (int i = 0; i < stages + boxes; ++i, u += 2) {
           const int s = u % kOStages;
@@ -753,19 +752,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
               if ((lo > 0 || hi < kORows) && hi > 0) zero_rows<kORows>(sb + kORing + s * kOStage, lo, hi, lane);
               tc_fence_after();
               const uint64_t cd = sdesc_add(cd0, s * kOStage);
-#pragma unroll
-              for (int kk = 0; kk < 2; ++kk) {
-                const int k = 2 * i + kk;   // the tile's k-step: 16 keys (bf16) or 32 (FP8)
-                const uint32_t acc = (head && k == 0) ? 0u : 1u;
-                const uint64_t bd = sdesc_add(cd, kk * (kORows * 64));
-                if (kFp8) {
-                  mma_ss_8bit_elect(tmem + 256 * nh, sdesc_add(pd0, b * kPBytes + k * 32), bd, kIdPV8, acc);
-                  mma_ss_8bit_elect(tmem + 256 * nh, sdesc_add(pd0, b * kPBytes + kBlk + k * 32), bd, kIdPV8r, 1u);
-                } else {
-                  mma_ss_elect(tmem + 256 * nh, sdesc_add(pd0, b * kPBytes + (k >> 2) * kBlk + (k & 3) * 32), bd,
-                               kIdPV, acc);
-                }
-              }
+              // k-steps 2 i, 2 i + 1 of the tile: 16 keys (bf16) or 32 (FP8) each
+              const uint32_t acc = (head && i == 0) ? 0u : 1u;
+              const uint64_t pd = sdesc_add(pd0, b * kPBytes + (kFp8 ? i * 64 : (i >> 1) * kBlk + (i & 1) * 64));
+              if (kFp8) mma_ss2x2_mn_8bit_elect(tmem + 256 * nh, pd, cd, kIdPV8, acc, kIdPV8r);
+              else mma_ss2_mn_elect(tmem + 256 * nh, pd, cd, kIdPV, acc);
               mma_commit_elect(bar(kCE + s));
               advance(1);
             }
@@ -913,6 +904,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       if (lane == 0) bulk_wait0();   // every store complete before the CTA's shared memory goes
     }
   }
+  grid_wait();   // also the CTAs without work
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();   // nothing of the other CTA is under way into this one

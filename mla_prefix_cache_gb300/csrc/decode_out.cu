@@ -104,7 +104,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_out_kernel(const __grid_co
     r = find_request(p.batch.rows, r0 + tid);
     if (r >= 0) rr = request_rows(p.batch.rows, r);
   }
-  grid_wait();   // the attention kernel's states are there
+  grid_wait();      // the attention kernel's states are there
+  grid_trigger();
   const int total = p.ws.first[B], n_clusters = p.ws.first[B + 1];
   if (tid < R) {
     RowOf o;

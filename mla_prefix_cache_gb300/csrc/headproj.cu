@@ -14,6 +14,7 @@
 #include "absorb.h"
 #include "internal.h"
 #include "ptx.cuh"
+#include "serving.cuh"
 
 namespace mla {
 namespace {
@@ -60,12 +61,13 @@ __global__ void __launch_bounds__(128, 1) qabsorb_kernel(const __grid_constant__
   const int h = blockIdx.z;
   const int c0 = blockIdx.y * L::kCols;
   const int t0 = p.row0 + blockIdx.x * 128;   // first token of the tile (TMA coordinates)
+  if (p.clear != nullptr) {                   // decode: launched dependently
+    grid_wait();      // the inputs are there
+    grid_trigger();   // the attention kernel may start its own set-up
+    if (threadIdx.x == 0 && (blockIdx.x | blockIdx.y | blockIdx.z) == 0) *p.clear = 0u;
+  }
 
   if (threadIdx.x == 0) {
-    if (p.clear != nullptr) {
-      asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the attention kernel may start its own set-up
-      if ((blockIdx.x | blockIdx.y | blockIdx.z) == 0) *p.clear = 0u;
-    }
     mbar_init(bar_full, 1);
     mbar_init(bar_done, 1);
     fence_mbar_init();
@@ -352,8 +354,10 @@ cudaError_t launch_qabsorb(const QAbsorbParams& p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const bool f8 = p.qscale != nullptr;
   const dim3 grid((p.tokens + 127) / 128, f8 ? 1 : kDc / 256, p.num_heads);
-  if (f8 && p.two) qabsorb_kernel<kTwoE4m3><<<grid, 128, QA<kTwoE4m3>::kSmem, s>>>(p);
-  else if (f8) qabsorb_kernel<kE4m3><<<grid, 128, QA<kE4m3>::kSmem, s>>>(p);
+  if (p.clear != nullptr)
+    return f8 ? launch_dependent(qabsorb_kernel<kTwoE4m3>, grid, 128, QA<kTwoE4m3>::kSmem, p, s)
+              : launch_dependent(qabsorb_kernel<kBf16>, grid, 128, QA<kBf16>::kSmem, p, s);
+  if (f8) qabsorb_kernel<kE4m3><<<grid, 128, QA<kE4m3>::kSmem, s>>>(p);
   else qabsorb_kernel<kBf16><<<grid, 128, QA<kBf16>::kSmem, s>>>(p);
   count_launch();
   return cudaGetLastError();

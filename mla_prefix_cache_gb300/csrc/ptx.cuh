@@ -637,47 +637,64 @@ __device__ __forceinline__ void mma2_ts_e4m3_elect(uint32_t d_tmem, uint32_t a_t
       : "memory");
 }
 // The single-CTA forms (cta_group::1, M = 128) from one elected lane of a
-// converged warp: A from shared memory or TMEM, bf16 or 8-bit operands.
-__device__ __forceinline__ void mma_ss_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                             uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred e, p;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
+// converged warp, some consecutive K steps a statement: the lane is elected and
+// branched to once, and the operands move by constants (descriptors count 16
+// bytes).  One statement an MMA takes a third more code, and the instruction
+// cache paces kernels whose roles all run unrolled.
+//   ts4: A in TMEM, 8 columns a step, B 32 bytes a step
+//   ss4: A and B 32 bytes a step
+#define MLA_ELECT(body) "{\n\t.reg .pred e, p, q;\n\t.reg .b64 x, y;\n\t.reg .b32 a;\n\t"          \
+                        "elect.sync _|e, 0xffffffff;\n\t@!e bra DONE%=;\n\t"                       \
+                        "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 q, 0, 0;\n\t" body "DONE%=:\n\t}"
+#define MLA_TS(kind, acols, badd, acc)                                                          \
+  "add.u32 a, %1, " acols ";\n\tadd.u64 x, %2, " badd ";\n\t"                                   \
+  "tcgen05.mma.cta_group::1.kind::" kind " [%0], [a], x, %3, " acc ";\n\t"
+#define MLA_SS(kind, aadd, badd, idesc, acc)                                                    \
+  "add.u64 x, %1, " aadd ";\n\tadd.u64 y, %2, " badd ";\n\t"                                    \
+  "tcgen05.mma.cta_group::1.kind::" kind " [%0], x, y, " idesc ", " acc ";\n\t"
+__device__ __forceinline__ void mma_ts4_elect(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                              uint32_t accumulate) {
+  asm volatile(MLA_ELECT(MLA_TS("f16", "0", "0", "p") MLA_TS("f16", "8", "2", "q") MLA_TS("f16", "16", "4", "q")
+                             MLA_TS("f16", "24", "6", "q"))::"r"(d_tmem),
+               "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+               : "memory");
 }
-__device__ __forceinline__ void mma_ts_elect(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                             uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred e, p;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
+__device__ __forceinline__ void mma_ss4_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                              uint32_t accumulate) {
+  asm volatile(MLA_ELECT(MLA_SS("f16", "0", "0", "%3", "p") MLA_SS("f16", "2", "2", "%3", "q")
+                             MLA_SS("f16", "4", "4", "%3", "q") MLA_SS("f16", "6", "6", "%3", "q"))::"r"(d_tmem),
+               "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+               : "memory");
 }
-__device__ __forceinline__ void mma_ss_8bit_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                                  uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred e, p;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
+// Two 8-bit terms of A, the second 128 TMEM columns on, against the same B.
+__device__ __forceinline__ void mma_ts4x2_8bit_elect(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                                     uint32_t accumulate) {
+  asm volatile(MLA_ELECT(MLA_TS("f8f6f4", "0", "0", "p") MLA_TS("f8f6f4", "128", "0", "q")
+                             MLA_TS("f8f6f4", "8", "2", "q") MLA_TS("f8f6f4", "136", "2", "q")
+                             MLA_TS("f8f6f4", "16", "4", "q") MLA_TS("f8f6f4", "144", "4", "q")
+                             MLA_TS("f8f6f4", "24", "6", "q") MLA_TS("f8f6f4", "152", "6", "q"))::"r"(d_tmem),
+               "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+               : "memory");
 }
-__device__ __forceinline__ void mma_ts_8bit_elect(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                                  uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred e, p;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
+// Two K steps with B MN-major (2048 bytes a step of 16 rows).
+__device__ __forceinline__ void mma_ss2_mn_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                                 uint32_t accumulate) {
+  asm volatile(MLA_ELECT(MLA_SS("f16", "0", "0", "%3", "p") MLA_SS("f16", "2", "128", "%3", "q"))::"r"(d_tmem),
+               "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+               : "memory");
 }
+// Two K steps of two 8-bit terms of A, the second 16 KB on and of another
+// format, with B MN-major (4096 bytes a step of 32 rows).
+__device__ __forceinline__ void mma_ss2x2_mn_8bit_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                                        uint32_t accumulate, uint32_t idesc2) {
+  asm volatile(MLA_ELECT(MLA_SS("f8f6f4", "0", "0", "%3", "p") MLA_SS("f8f6f4", "1024", "0", "%5", "q")
+                             MLA_SS("f8f6f4", "2", "256", "%3", "q") MLA_SS("f8f6f4", "1026", "256", "%5", "q"))::"r"(d_tmem),
+               "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(idesc2)
+               : "memory");
+}
+#undef MLA_ELECT
+#undef MLA_TS
+#undef MLA_SS
 // Completion of the CTA's MMAs issued so far: on a barrier of this CTA, or on
 // the barrier at the same offset in every CTA of the cluster that `mask` names.
 __device__ __forceinline__ void mma_commit_elect(uint32_t bar) {

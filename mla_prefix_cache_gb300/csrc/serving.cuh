@@ -8,9 +8,11 @@
 namespace mla {
 
 // Programmatic dependent launch: a kernel launched by launch_dependent may
-// start while the kernel before it in the stream still runs; grid_wait() in it
-// returns when that one's memory is visible, grid_trigger() in the earlier one
-// lets it start.
+// start once every CTA of the kernel before it in the stream has called
+// grid_trigger() (or ended); grid_wait() in it returns when that one is done and
+// its memory visible.  Each kernel here waits before it triggers, and every CTA
+// waits: so what a dependent kernel reads before its own wait was there before
+// the kernel that it depends on, and one wait covers all earlier kernels.
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
@@ -129,7 +131,10 @@ static __device__ __noinline__ RequestWork request_work(const DecodeBatch& b, in
 // The units [0, total) of the batch are cut evenly: cluster c of n has
 // [unit_begin(c), unit_begin(c + 1)); cluster_of(x) is the one that has unit x.
 // (The host keeps total below 2^31.)
-__device__ __forceinline__ int unit_begin(int c, int n, int total) { return (int)((uint64_t)c * (uint32_t)total / (uint32_t)n); }
+__device__ __forceinline__ int unit_begin(int c, int n, int total) {   // floor(c total / n) in 32 bits: c <= n is small
+  const int q = total / n;
+  return c * q + c * (total - q * n) / n;
+}
 __device__ __forceinline__ int cluster_of(int x, int n, int total) { return (int)(((uint64_t)(x + 1) * (uint32_t)n - 1) / (uint32_t)total); }
 // The slot of the state that cluster c has of an item whose first tile is unit
 // x: each cluster shares one item with the clusters before it at most, and one

@@ -30,9 +30,10 @@ struct AppendParams {
   int num_blocks;
   float inv_scale;               // 1 / kv_scale
   uint32_t* err;                 // optional
+  int per_warp;                  // consecutive rows of a warp (set by the launcher)
   uint64_t rope_frac[kDr / 2];
 };
-cudaError_t launch_cache_append(const AppendParams& p, bool fp8, cudaStream_t s);
+cudaError_t launch_cache_append(AppendParams p, bool fp8, cudaStream_t s);
 
 // The decode attention's clusters (two CTAs each): the persistent grid of a
 // GB300's 152 SMs.  Each has two slots for the states of pieces that it shares
