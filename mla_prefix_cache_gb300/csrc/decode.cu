@@ -85,8 +85,8 @@ enum : uint32_t {
 };
 constexpr uint32_t kShared = kBars + 8 * kNBars;   // Start, then the hand-over word
 constexpr uint32_t kHand = kShared + 64;
-constexpr uint32_t kSmem = kHand + 16;
-static_assert(kSmem <= 232448, "more than 227 KB of shared memory per CTA");
+constexpr uint32_t kWalks = kHand + 16;            // the roles' walks
+constexpr int kRoles = 6;
 constexpr uint32_t kTxP = kPBytes + kFacBytes;
 
 constexpr uint32_t kIdS = idesc_bf16(128, 128, false, false);
@@ -184,32 +184,36 @@ __device__ bool schedule(const DecodeParams& p, Start* st, int* scratch, int clu
 // A cluster's run of units, walked alike by every role, as ranges of key tiles
 // with one RoPE offset: tiles j = 0 .. n - 1 of 128 keys from key t0 on, of
 // which [k_lo, k_hi) count.  The ranges of a piece (a run of one item's tiles)
-// follow one another, the first marked `head`, the last `tail`.
+// follow one another, the first marked `head`, the last `tail`.  A role's walk
+// sits in shared memory, advanced by one of its threads: in local memory, which
+// the few KB of L1 beside 226 KB of shared memory do not hold, the first range
+// alone took 2 us.
 struct Walk {
   // range
-  int t0, n, k_lo, k_hi;
   int64_t offset;
-  bool head, tail;
+  int t0, n, k_lo, k_hi;
+  bool more, head, tail;
   // its piece
-  int r, row0, slot;      // request, first row of the item, slot of its state (-1: a whole item)
-  int q_begin, rows, len; // first query row of the request, its (token, head) rows, its tokens
+  int r, row0, slot, rows;   // request, first row of the item, slot of its state (-1: a whole item), the request's rows
+  RequestWork w;             // of request r
   // where the walk is
-  RequestWork w;
-  int at, end, first, cluster;
+  int at, end, first;        // next unit, one past the run's last, first unit of request r
   int lo, hi, g, last_key, acc;   // the piece's tiles; next range, end of the keys so far, tiles so far
   // stages of each half of the columns that the piece's states leave through, if it has 32 live rows (fewer are
   // written by their threads)
   __device__ __forceinline__ int boxes() const { return rows - row0 < 32 ? 0 : kBoxes; }
-  __device__ __forceinline__ void start(const Start& s, int cluster_) {
+  __device__ __forceinline__ void start(const Start& s) {
     w = s.w;
     at = s.begin;
     end = s.end;
     first = s.first;
     r = s.r;
-    cluster = cluster_;
     lo = hi = acc = 0;
   }
 };
+
+constexpr uint32_t kSmem = kWalks + kRoles * sizeof(Walk);
+static_assert(kWalks % alignof(Walk) == 0 && kSmem <= 232448, "shared memory per CTA");
 
 // One copy of this code serves every role: inlined into each, the kernel's code
 // was 170 KB and its roles waited for instructions (1.5 times the time).
@@ -233,18 +237,16 @@ __device__ __noinline__ bool next_range(const DecodeParams& p, Walk& k) {
       k.at = stop;
       if (k.hi <= k.lo) continue;   // only units of the item's start
       k.row0 = item * kItemRows;
-      k.slot = (k.lo == 0 && k.hi == k.w.tiles) ? -1 : 2 * k.cluster + (k.lo == 0 ? 1 : 0);
+      k.slot = (k.lo == 0 && k.hi == k.w.tiles) ? -1 : 2 * (int)(blockIdx.x >> 1) + (k.lo == 0 ? 1 : 0);
       break;
     }
     k.head = true;
-    k.q_begin = k.w.q_begin;
     k.rows = k.w.q_count * p.batch.num_heads;
-    k.len = k.w.len;
     if (k.w.sg.x == k.w.sg.y) {   // no segments: one range
       k.t0 = 128 * k.lo;
       k.n = k.hi - k.lo;
       k.k_lo = 0;
-      k.k_hi = k.len;
+      k.k_hi = k.w.len;
       k.offset = 0;
       k.tail = true;
       k.acc = k.hi;
@@ -255,7 +257,7 @@ __device__ __noinline__ bool next_range(const DecodeParams& p, Walk& k) {
     k.acc = 0;
     // ranges before the piece's first tile
     while (k.g <= k.w.sg.y) {
-      const KeyRange kr = request_range(p.batch, k.w.sg, k.g, k.last_key, k.len);
+      const KeyRange kr = request_range(p.batch, k.w.sg, k.g, k.last_key, k.w.len);
       const int t = range_tiles(kr);
       if (k.acc + t > k.lo) break;
       k.acc += t;
@@ -264,7 +266,7 @@ __device__ __noinline__ bool next_range(const DecodeParams& p, Walk& k) {
     }
   }
   while (true) {   // the next range with tiles: the piece's tiles say there is one
-    const KeyRange kr = request_range(p.batch, k.w.sg, k.g, k.last_key, k.len);
+    const KeyRange kr = request_range(p.batch, k.w.sg, k.g, k.last_key, k.w.len);
     const int t = range_tiles(kr), from = k.acc;
     k.last_key = kr.hi;
     k.acc += t;
@@ -279,6 +281,21 @@ __device__ __noinline__ bool next_range(const DecodeParams& p, Walk& k) {
     k.tail = k.acc >= k.hi;
     return true;
   }
+}
+
+// The next range of a walk: by the one thread of a role, by a warp, by `count`
+// threads at named barrier `id` (everyone is done with the range before).
+__device__ __forceinline__ bool next_of_warp(const DecodeParams& p, Walk& k, int lane) {
+  __syncwarp();
+  if (lane == 0) k.more = next_range(p, k);
+  __syncwarp();
+  return *const_cast<volatile bool*>(&k.more);
+}
+__device__ __forceinline__ bool next_of_group(const DecodeParams& p, Walk& k, bool leader, uint32_t id, uint32_t count) {
+  named_bar_sync(id, count);
+  if (leader) k.more = next_range(p, k);
+  named_bar_sync(id, count);
+  return *const_cast<volatile bool*>(&k.more);
 }
 
 // Waits for a barrier's phase; false, and the error word, when it gives up.
@@ -360,8 +377,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   cluster_sync_all();   // both CTAs' barriers exist before either is signalled
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&start->tmem);
-  Walk k;
-  k.start(*start, cluster);
+  // scores: loads 0, 1, MMA, copies, Q, softmax; values: loads 0, 1, MMA, P landed, -, rescale
+  const int role = warp == 0 ? 0 : warp == (scores ? 3 : 2) ? 1 : warp == 1 ? 2 : warp < 4 ? 3 : warp >= 12 ? 4 : 5;
+  Walk& k = reinterpret_cast<Walk*>(smem + kWalks)[role];
+  if (lane == 0 && (warp <= 4 || warp == 12)) k.start(*start);
   if (cut && blockIdx.x == 0) {
     grid_wait();
     atomicOr(p.ws.err, kErrBadBlock);
@@ -384,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       while (ok && next_range(p, k)) {
         grid_wait();      // qlat is there, and the error word cleared
         grid_trigger();   // decode_out_kernel may take SMs as they fall free
-        const int qrow = k.q_begin * H + k.row0;
+        const int qrow = k.w.q_begin * H + k.row0;
         for (int i = 0; k.head && i < kQBoxes; ++i, ++u) {
           if ((u & 1) != mine) continue;
           if (!(ok = open())) break;
@@ -414,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       const uint64_t sd0 = sdesc_sw128(sb + kSRing, 16, 1024);
       int g = 0, s = 0, e = 0;
       uint32_t ph = 0;
-      while (ok && next_range(p, k)) {
+      while (ok && next_of_warp(p, k, lane)) {
         if (k.head) {
           s += kQBoxes;   // the Q stages
           if (s >= kSStages) { s -= kSStages; ph ^= 1u; }
@@ -466,11 +485,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
       bool ok = true;
       int e = 0, u = 0;
-      while (next_range(p, k)) {
+      while (next_of_group(p, k, r == 0, 7, 128)) {
         const int prow = k.row0 + r;
         const bool live = prow < k.rows;
-        const int64_t grow = (int64_t)k.q_begin + (live ? prow / H : 0);
-        const int64_t orow = (int64_t)k.q_begin * H + prow;
+        const int64_t grow = (int64_t)k.w.q_begin + (live ? prow / H : 0);
+        const int64_t orow = (int64_t)k.w.q_begin * H + prow;
         if (kFp8) grid_wait();   // for the queries' scales
         const float rq = kFp8 && live ? 1.f / (p.ws.qscale[orow] * p.kv_scale) : 1.f;
         const uint4* qr = reinterpret_cast<const uint4*>(p.q + orow * kDqk + kDnope);
@@ -542,13 +561,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       bool ok = true;
       int g = 0;
       float m_used = -INFINITY, l = 0.f, lsum = 0.f;
-      while (next_range(p, k)) {
+      while (next_of_group(p, k, tid == 128, 5, 256)) {
         const int prow = k.row0 + r;
         const bool live = prow < k.rows;
-        const int64_t orow = (int64_t)k.q_begin * H + prow;
+        const int64_t orow = (int64_t)k.w.q_begin * H + prow;
         if (kFp8) grid_wait();   // for the queries' scales
         const float sl2 = p.scale_log2 * (kFp8 && live ? p.ws.qscale[orow] * p.kv_scale : 1.f);
-        const int qk = live ? k.len - (k.rows - 1 - prow) / H - 1 : -1;   // the last key token the row sees
+        const int qk = live ? k.w.len - (k.rows - 1 - prow) / H - 1 : -1;   // the last key token the row sees
         const int n = k.n, t0 = k.t0, k_lo = k.k_lo, k_hi = k.k_hi, slot = k.slot;
         const bool tail = k.tail;
         if (k.head) {
@@ -706,7 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       if (lane == 0)
         for (int b = 0; b < 2; ++b) mbar_arrive_expect_tx(bar(kPF + b), kTxP);
       bool head = true;
-      while (ok && next_range(p, k)) {
+      while (ok && next_of_warp(p, k, lane)) {
         if (k.head) head = true;
 #pragma unroll 1
         for (int j = 0; j < k.n && ok; ++j, ++g) {
@@ -794,7 +813,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       const volatile int* hand = reinterpret_cast<const volatile int*>(smem + kHand);
       bool ok = true;
       int g = 0, ev = 0, u = half;   // tiles, hand-overs, this half's next stage
-      while (next_range(p, k)) {
+      while (next_of_group(p, k, tid == 128, 5, 256)) {
         g += k.n;
         u += 2 * kOPerTile * k.n;
         if (!k.tail) continue;   // a piece's states leave at its end
@@ -834,7 +853,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         tc_fence_after();
         const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
         const int rows = k.rows - k.row0;      // live rows of the item
-        const int64_t orow0 = (int64_t)k.q_begin * H + k.row0;
+        const int64_t orow0 = (int64_t)k.w.q_begin * H + k.row0;
         const bool whole = k.slot < 0;
         const int boxes = k.boxes();
         // A warp of 32 live rows stages 128 bytes of each (32 fp32 or 64 bf16 columns) in its quarter of a box and

@@ -105,7 +105,7 @@ struct RequestWork {
   int2 sg;
   __device__ __forceinline__ int units() const { return tiles > 0 ? tiles + kItemUnits : 0; }
 };
-static __device__ __noinline__ RequestWork request_work(const DecodeBatch& b, int r) {
+__device__ __forceinline__ RequestWork request_work(const DecodeBatch& b, int r) {
   RequestWork w;
   const int2 rr = request_rows(b.rows, r);
   w.q_begin = rr.x;
@@ -119,7 +119,7 @@ static __device__ __noinline__ RequestWork request_work(const DecodeBatch& b, in
   }
   w.tiles = 0;
   int end = 0;
-#pragma unroll 2
+#pragma unroll 1
   for (int g = w.sg.x; g <= w.sg.y; ++g) {
     const KeyRange k = request_range(b, w.sg, g, end, w.len);
     end = k.hi;
