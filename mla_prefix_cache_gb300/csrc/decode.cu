@@ -632,13 +632,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
               const float a = ex2(x0), bb = ex2(x1);
               s2[c & 1] = fadd2(s2[c & 1], f2pack(a, bb));
               if constexpr (kFp8) {
-                // a value to 2 mantissa bits (half up), exact in E5M2 above 2^-14, and the rest
-                const float ah = __uint_as_float((__float_as_uint(a) + 0x00100000u) & 0xFFE00000u);
-                const float bh = __uint_as_float((__float_as_uint(bb) + 0x00100000u) & 0xFFE00000u);
-                const uint32_t h2 = pack_e5m2x2(ah, bh), r2 = pack_e4m3x2(a - ah, bb - bh);
+                // f16 (2^-11), its nearest E5M2, and the rest of it, which f16 holds exactly, in E4M3
+                const uint32_t h16 = pack_f16(a, bb);
+                const uint32_t h2 = e5m2x2_of_f16x2(h16);
+                const uint32_t r2 = e4m3x2_of_f16x2(sub_f16x2(h16, __byte_perm(h2, 0u, 0x1404)));
                 if (c & 1) {
-                  pk[c >> 1] |= h2 << 16;
-                  pk[16 + (c >> 1)] |= r2 << 16;
+                  pk[c >> 1] = __byte_perm(pk[c >> 1], h2, 0x5410);
+                  pk[16 + (c >> 1)] = __byte_perm(pk[16 + (c >> 1)], r2, 0x5410);
                 } else {
                   pk[c >> 1] = h2;
                   pk[16 + (c >> 1)] = r2;

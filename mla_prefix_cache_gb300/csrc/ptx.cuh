@@ -368,10 +368,26 @@ __device__ __forceinline__ uint16_t pack_e4m3x2(float lo, float hi) {
   return r;
 }
 
-// Two floats to two E5M2 codes (the low byte holds `lo`).
-__device__ __forceinline__ uint16_t pack_e5m2x2(float lo, float hi) {
+// f16 pairs (the low half holds the first): from floats, their difference, and
+// their E5M2 and E4M3 codes (two bytes), all rounded to nearest even.
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t e5m2x2_of_f16x2(uint32_t a) {
   uint16_t r;
-  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(a));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3x2_of_f16x2(uint32_t a) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(a));
   return r;
 }
 
