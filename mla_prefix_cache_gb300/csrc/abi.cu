@@ -1861,7 +1861,7 @@ static bool decode_layout(int num_reqs, int total_q, int num_heads, DecodeLayout
   d->qlat = up256(d->first + ((size_t)num_reqs + 2) * 4);
   d->qscale = up256(d->qlat + rows * kDc * 2);
   d->lat = up256(d->qscale + rows * 4);
-  d->lat_lse = up256(d->lat + rows * kDc * 2);
+  d->lat_lse = up256(d->lat + rows * kDc * 4);
   d->part = up256(d->lat_lse + rows * 4);
   d->part_lse = up256(d->part + (size_t)kDecodeSlots * kItemRows * kDc * 4);
   d->total = up256(d->part_lse + (size_t)kDecodeSlots * kItemRows * 4);
@@ -1916,7 +1916,7 @@ int mla_decode(const void* q, const int32_t* q_pos, const void* kv_cache, int kv
   space.first = reinterpret_cast<int32_t*>(ws + d.first);
   space.qlat = ws + d.qlat;
   space.qscale = reinterpret_cast<float*>(ws + d.qscale);
-  space.lat = reinterpret_cast<uint16_t*>(ws + d.lat);
+  space.lat = reinterpret_cast<float*>(ws + d.lat);
   space.lat_lse = reinterpret_cast<float*>(ws + d.lat_lse);
   space.part = reinterpret_cast<float*>(ws + d.part);
   space.part_lse = reinterpret_cast<float*>(ws + d.part_lse);
@@ -1955,13 +1955,13 @@ int mla_decode(const void* q, const int32_t* q_pos, const void* kv_cache, int kv
     ok &= encode_map(&p.tm_s, fp8 ? byte : bf16, 3, kv_cache, dc, sc, bs, sw);
     ok &= encode_map(&p.tm_o, fp8 ? byte : bf16, 3, kv_cache, dc, sc, bv, sw);
     const uint64_t dl[2] = {(uint64_t)kDc, n}, dp[2] = {(uint64_t)kDc, (uint64_t)kDecodeSlots * kItemRows};
-    const uint64_t sl[1] = {(uint64_t)kDc * 2}, sp[1] = {(uint64_t)kDc * 4};
-    const uint32_t bl[2] = {64, 32}, bp[2] = {32, 32};
+    const uint64_t sl[1] = {(uint64_t)kDc * 4};
+    const uint32_t bl[2] = {32, 32};
     const uint64_t dq[2] = {(uint64_t)kDc, fp8 ? 2 * n : n}, sq[1] = {fp8 ? (uint64_t)kDc : (uint64_t)kDc * 2};
     const uint32_t bq[2] = {(uint32_t)dc[0], 128};
     ok &= encode_map(&p.tm_q, fp8 ? byte : bf16, 2, space.qlat, dq, sq, bq, sw);
-    ok &= encode_map(&p.tm_lat, bf16, 2, space.lat, dl, sl, bl, sw);
-    ok &= encode_map(&p.tm_part, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, space.part, dp, sp, bp, sw);
+    ok &= encode_map(&p.tm_lat, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, space.lat, dl, sl, bl, sw);
+    ok &= encode_map(&p.tm_part, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, space.part, dp, sl, bl, sw);
   }
   if (!ok) return MLA_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -1993,7 +1993,7 @@ int mla_decode(const void* q, const int32_t* q_pos, const void* kv_cache, int kv
 
   op.batch = batch;
   // as many tokens a CTA as still give every SM one
-  op.tile = 128;
+  op.tile = 64;
   while (op.tile > 16 && (int64_t)((total_q + op.tile / 2 - 1) / (op.tile / 2)) * H <= 2 * kDecodeClusters) op.tile /= 2;
   op.ws = space;
   op.out = out;

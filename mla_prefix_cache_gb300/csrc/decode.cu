@@ -12,9 +12,9 @@
 // tiles of 128.  The tiles of all items, in order, with a few units for each
 // item's start and end, are cut evenly over the clusters of a persistent grid,
 // whatever the lengths are: a cluster has one contiguous run of tiles, the last
-// part of one item, whole items, the first part of another.  A piece that is a
-// whole item leaves its state as bf16 rows; the others leave fp32 states in the
-// cluster's two slots, which decode_out_kernel joins.  The cut is computed by
+// part of one item, whole items, the first part of another.  A piece leaves the
+// fp32 states of its rows, a whole item's in the rows' own place, the others in
+// the cluster's two slots, which decode_out_kernel joins.  The cut is computed by
 // every CTA from the lengths (one pass of its threads over the requests), so no
 // launch waits for a plan.
 //
@@ -94,7 +94,12 @@ constexpr uint32_t kIdPV = idesc_bf16(128, 256, false, true);
 constexpr uint32_t kIdS8 = idesc_8bit(128, 128, 0, 0, false);
 constexpr uint32_t kIdPV8 = idesc_8bit(128, 256, 1, 0, true);     // E5M2 P
 constexpr uint32_t kIdPV8r = idesc_8bit(128, 256, 0, 0, true);    // E4M3 rest of P
-constexpr float kRescale = 8.f;   // log2 units: P stays <= 256
+// Rows are rescaled when their maximum rises by more than this (log2 units).
+// 8-bit terms of P: P counts in units of 2^-7, so that it spans 2^11 down to
+// what E5M2 holds, and what the first term leaves of it stays between E4M3's
+// 448 and its least normal 2^-6 for weights down to 2^-10 of the largest.
+constexpr float kRescaleBf16 = 8.f, kRescaleFp8 = 4.f;
+constexpr float kPBiasFp8 = 7.f;
 
 // The larger of two bf16 values (16 bits each), as float bits.
 __device__ __forceinline__ uint32_t max_bf16(uint32_t a, uint32_t b) {
@@ -614,11 +619,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           named_bar_sync(pair, 64);
           const float m_tile = __uint_as_float(max_bf16(mx16[lane], mx16[32 + lane])) * sl2;
           float alpha = 1.f;
-          if (m_tile > m_used + kRescale) {
+          if (m_tile > m_used + (kFp8 ? kRescaleFp8 : kRescaleBf16)) {
             alpha = ex2(m_used - m_tile);   // 0 when m_used = -inf
             m_used = m_tile;
           }
-          const float mref = (m_used == -INFINITY) ? 0.f : m_used;
+          const float mref = ((m_used == -INFINITY) ? 0.f : m_used) - (kFp8 ? kPBiasFp8 : 0.f);
           const uint64_t sc2 = f2pack(sl2, sl2), nm2 = f2pack(-mref, -mref);
           // P in registers while the previous tile's copy is still in flight: bf16 pairs, or per four keys a
           // word of E5M2 and a word of E4M3 codes
@@ -679,7 +684,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           if (lane == 0 && ok) mbar_arrive(bar(kPST + b));
         }
         if (tail && live && half == 0) {
-          const float lse = (ok && lsum > 0.f) ? (m_used + __log2f(lsum)) * 0.6931471805599453f : -INFINITY;
+          const float lse = (ok && lsum > 0.f) ? (m_used - (kFp8 ? kPBiasFp8 : 0.f) + __log2f(lsum)) * 0.6931471805599453f
+                                              : -INFINITY;
           if (slot < 0) p.ws.lat_lse[orow] = lse;
           else p.ws.part_lse[slot * kItemRows + r] = lse;
         }
@@ -853,12 +859,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         tc_fence_after();
         const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
         const int rows = k.rows - k.row0;      // live rows of the item
-        const int64_t orow0 = (int64_t)k.w.q_begin * H + k.row0;
         const bool whole = k.slot < 0;
+        const int row0 = whole ? k.w.q_begin * H + k.row0 : k.slot * kItemRows;   // first row of the states
         const int boxes = k.boxes();
-        // A warp of 32 live rows stages 128 bytes of each (32 fp32 or 64 bf16 columns) in its quarter of a box and
-        // stores them by TMA, four boxes in turn, at its own pace; a warp with fewer writes them by its threads.
-        // (One box for all 128 rows, with a barrier a step, took 5 us a piece.)
+        // A warp of 32 live rows stages 32 columns of them in its quarter of a box and stores them by TMA, four
+        // boxes in turn, at its own pace; a warp with fewer writes them by its threads.  256 KB in 4.6 us: the SM's
+        // stores to L2 pace it, about 30 B a cycle (contiguous 4 KB copies, loads of the next columns started
+        // before, or 64 columns a step took as long).
         const bool tma = 32 * (warp & 3) + 32 <= rows;
         if (boxes > 0 && ok) {   // the loading thread hands the stages over in order
 #pragma unroll 1
@@ -876,41 +883,25 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
           const int col = 256 * half + 32 * cc;
-          if (whole) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = pack_bf16(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
-          }
           if (tma) {
-            const int b = whole ? cc >> 1 : cc & 3;
-            const uint32_t box = sb + kORing + (uint32_t)((u + 2 * b) % kOStages) * kOStage + (uint32_t)(warp & 3) * 4096;
-            if (!whole && cc >= 4) {   // the box's store of four steps ago has read it
+            const uint32_t box = sb + kORing + (uint32_t)((u + 2 * (cc & 3)) % kOStages) * kOStage + (uint32_t)(warp & 3) * 4096;
+            if (cc >= 4) {   // the box's store of four steps ago has read it
               if (lane == 0) bulk_wait_read<3>();
               __syncwarp();
             }
-            const uint32_t c0 = whole ? 4 * (cc & 1) : 0;
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              sts128(box + sw128_off((uint32_t)lane, c0 + c), o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
-            if (!whole) {
-#pragma unroll
-              for (int c = 4; c < 8; ++c)
-                sts128(box + sw128_off((uint32_t)lane, (uint32_t)c), o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
-            }
-            if (!whole || (cc & 1)) {
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0 && ok) {
-                if (whole) tma_store_2d(&p.tm_lat, box, col - 32, (int)orow0 + 32 * (warp & 3));
-                else tma_store_2d(&p.tm_part, box, col, k.slot * kItemRows + 32 * (warp & 3));
-                bulk_commit();
-              }
-            }
-          } else if (r < rows) {
-            uint4* dst = whole ? reinterpret_cast<uint4*>(p.ws.lat + (orow0 + r) * kDc + col)
-                               : reinterpret_cast<uint4*>(p.ws.part + ((int64_t)k.slot * kItemRows + r) * kDc + col);
 #pragma unroll
             for (int c = 0; c < 8; ++c)
-              if (c < 4 || !whole) dst[c] = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+              sts128(box + sw128_off((uint32_t)lane, (uint32_t)c), o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && ok) {
+              tma_store_2d(whole ? &p.tm_lat : &p.tm_part, box, col, row0 + 32 * (warp & 3));
+              bulk_commit();
+            }
+          } else if (r < rows) {
+            uint4* dst = reinterpret_cast<uint4*>((whole ? p.ws.lat : p.ws.part) + (int64_t)(row0 + r) * kDc + col);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) dst[c] = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
           }
         }
         if (boxes > 0) {   // the stages go back once every warp's stores have read them

@@ -2,15 +2,16 @@
 // row's keys are joined, and every row goes through W_UV of its head,
 //   w_i = e^{lse_i - m} / sum_j e^{lse_j - m},  o = sum_i w_i o_i,  lse = m + ln sum_j e^{lse_j - m}
 //   out[t][h] = out_scale o W_UV,h
-// A CTA takes some tokens of one head: up to 128, fewer where the grid would
-// not fill the GPU.  Its 32 warps join the fp32 states of their rows (few rows:
-// several warps a row, each some of the pieces), or take the bf16 state that
-// one cluster left, into one K-major swizzled operand of 512 columns; W_UV,h
-// comes by TMA in four chunks of 128 rows, two buffers deep, and one chain of
-// M = 128, N = 128 MMAs makes the 128 output columns.  o is rounded to bf16 for
-// the product, once, after the join.  Latency-bound: a row is two dependent
-// loads from L2 (weights, states), so the rows are spread over many warps (8
-// warps took 30 us for 64 tokens of 128 heads).
+// A CTA takes some tokens of one head: up to 64, fewer where the grid would not
+// fill the GPU.  Its 32 warps join the fp32 states of their rows (few rows:
+// several warps a row, each some of the pieces) into one K-major swizzled
+// operand of 512 columns, each value as its bf16 (rows 0 .. 63) and the bf16 of
+// what that leaves (rows 64 .. 127), so that one chain of M = 128, N = 128 MMAs
+// multiplies o to 2^-16; W_UV,h comes by TMA in four chunks of 128 rows, two
+// buffers deep, and the two halves of the product are added at the end.
+// Latency-bound: a row is two dependent loads from L2 (weights, states), so the
+// rows are spread over many warps (8 warps took 30 us for 64 tokens of 128
+// heads).
 #include "serving.cuh"
 
 namespace mla {
@@ -39,9 +40,12 @@ struct RowOf {
 static_assert(sizeof(RowOf) == 20, "row table");
 
 // Partial sums of warps that share rows (at most 4 rows then): 2 KB each in the
-// operand's rows from 8 on, which nothing else uses.
-__device__ __forceinline__ uint32_t share_at(int warp) { return kA + (uint32_t)(warp / 7) * kBlk + 1024 + (uint32_t)(warp % 7) * 2048; }
-static_assert((kWarps + 6) / 7 <= 8, "the warps' partial sums fit beside the rows");
+// operand's rows 8 .. 63 and 72 .. 127, which nothing else uses.
+__device__ __forceinline__ uint32_t share_at(int warp) {
+  const int s = warp % 6;
+  return kA + (uint32_t)(warp / 6) * kBlk + (s < 3 ? 1024 : 9216 - 3 * 2048) + (uint32_t)s * 2048;
+}
+static_assert((kWarps + 5) / 6 <= 8, "the warps' partial sums fit beside the rows");
 
 __device__ __forceinline__ bool wait(uint32_t* err, uint32_t bar, uint32_t parity) {
   if (mbar_wait(bar, parity)) return true;
@@ -61,11 +65,15 @@ __device__ __forceinline__ int find_request(const BatchRows& b, int x) {
   return x >= rr.x && x < rr.y ? lo : -1;
 }
 
-// 4 columns 4 lane + 128 k of row i as bf16 into the operand.
+// 4 columns 4 lane + 128 k of row i into the operand: their bf16, and that of the rest.
 __device__ __forceinline__ void put4(uint32_t a, int i, int lane, int k, float4 v) {
   const int c = 4 * lane + 128 * k;
   const uint32_t addr = a + (uint32_t)(c >> 6) * kBlk + sw128_off((uint32_t)i, (uint32_t)((c & 63) >> 3)) + (c & 4) * 2;
-  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(pack_bf16(v.x, v.y)), "r"(pack_bf16(v.z, v.w)) : "memory");
+  const uint32_t h0 = pack_bf16(v.x, v.y), h1 = pack_bf16(v.z, v.w);
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(h0), "r"(h1) : "memory");
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr + 64 * 128), "r"(pack_bf16(v.x - bf16_lo(h0), v.y - bf16_hi(h0))),
+               "r"(pack_bf16(v.z - bf16_lo(h1), v.w - bf16_hi(h1)))
+               : "memory");
 }
 
 __global__ void __launch_bounds__(kThreads, 1) decode_out_kernel(const __grid_constant__ DecodeOutParams p) {
@@ -142,13 +150,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_out_kernel(const __grid_co
     const RowOf o = rows[i];
     if (o.n == 1) {
       if (part == 0) {
-        const uint4* src = reinterpret_cast<const uint4*>(p.ws.lat + ((int64_t)(r0 + i) * H + h) * kDc);
+        const float4* src = reinterpret_cast<const float4*>(p.ws.lat + ((int64_t)(r0 + i) * H + h) * kDc) + lane;
+        float4 v[4];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int c = lane + 32 * k;   // 16-byte chunk of the row
-          const uint4 v = src[c];
-          sts128(sb + kA + (uint32_t)(c >> 3) * kBlk + sw128_off((uint32_t)i, (uint32_t)(c & 7)), v.x, v.y, v.z, v.w);
-        }
+        for (int k = 0; k < 4; ++k) v[k] = src[32 * k];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) put4(sb + kA, i, lane, k, v[k]);
       }
       continue;
     }
@@ -247,31 +254,47 @@ __global__ void __launch_bounds__(kThreads, 1) decode_out_kernel(const __grid_co
     }
   }
   ok = __syncthreads_and(ok);
-  if (ok) ok = __all_sync(0xffffffffu, wait(p.ws.err, bars + 16, 1) && wait(p.ws.err, bars + 24, 1));
+  if (ok) ok = wait(p.ws.err, bars + 16, 1) && wait(p.ws.err, bars + 24, 1);
+  ok = __syncthreads_and(ok);
   tc_fence_after();
   if (ok) {
-    // sixteen warps: TMEM lanes 32 (w mod 4) .., columns 32 (w / 4) ..
-    const int i = 32 * (warp & 3) + lane, cb = 32 * (warp >> 2);
-    if (warp < 16 && 32 * (warp & 3) < R) {
-      uint32_t v[32];
-      tmem_ld32(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + cb, v);
-      if (i < R && rows[i].n >= 0) {
-        const int64_t orow = (int64_t)(r0 + i) * H + h, o = orow * kDv + cb;
-        const bool empty = rows[i].lse == -INFINITY;   // no key seen: 0
+    // sixteen warps: TMEM lanes 32 (w mod 4) .., columns 32 (w / 4) ..; lanes 64 .. 127, the products of the rests,
+    // pass through shared memory (the weights' buffers)
+    const int q = warp & 3, i = 32 * (q & 1) + lane, cb = 32 * (warp >> 2);
+    float* rest = reinterpret_cast<float*>(smem + kB) + i * 132 + cb;   // 64 rows of 128, padded
+    const bool rows_here = warp < 16 && 32 * (q & 1) < R;
+    uint32_t v[32];
+    if (rows_here) {
+      tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + cb, v);
+      if (q >= 2) {
 #pragma unroll
-        for (int k = 0; k < 32; ++k) v[k] = empty ? 0u : __float_as_uint(__uint_as_float(v[k]) * p.out_scale);
-        if (p.out_bf16) {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + o);
-          auto o2 = [&](int k) { return pack_bf16(__uint_as_float(v[k]), __uint_as_float(v[k + 1])); };
-#pragma unroll
-          for (int k = 0; k < 4; ++k) dst[k] = make_uint4(o2(8 * k), o2(8 * k + 2), o2(8 * k + 4), o2(8 * k + 6));
-        } else {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<float*>(p.out) + o);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) dst[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-        }
-        if (p.lse != nullptr && warp < 4) p.lse[orow] = rows[i].lse;
+        for (int k = 0; k < 8; ++k)
+          reinterpret_cast<uint4*>(rest)[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
       }
+    }
+    __syncthreads();
+    if (rows_here && q < 2 && i < R && rows[i].n >= 0) {
+      const int64_t orow = (int64_t)(r0 + i) * H + h, o = orow * kDv + cb;
+      const bool empty = rows[i].lse == -INFINITY;   // no key seen: 0
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float4 x = reinterpret_cast<const float4*>(rest)[k];
+        const float f[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          v[4 * k + e] = empty ? 0u : __float_as_uint((__uint_as_float(v[4 * k + e]) + f[e]) * p.out_scale);
+      }
+      if (p.out_bf16) {
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + o);
+        auto o2 = [&](int k) { return pack_bf16(__uint_as_float(v[k]), __uint_as_float(v[k + 1])); };
+#pragma unroll
+        for (int k = 0; k < 4; ++k) dst[k] = make_uint4(o2(8 * k), o2(8 * k + 2), o2(8 * k + 4), o2(8 * k + 6));
+      } else {
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<float*>(p.out) + o);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) dst[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+      }
+      if (p.lse != nullptr && warp < 4) p.lse[orow] = rows[i].lse;
     }
   }
   tc_fence_before();

@@ -58,7 +58,7 @@ struct DecodeSpace {
   int32_t* first;        // [num_reqs + 2]: the requests' first work units, all units, clusters in use
   uint8_t* qlat;         // bf16 [rows * H][512], or E4M3 [2][rows * H][512]
   float* qscale;         // [rows * H]: the E4M3 rows' scales
-  uint16_t* lat;         // bf16 [rows * H][512]: states of rows whose keys one cluster had
+  float* lat;            // [rows * H][512]: states of rows whose keys one cluster had
   float* lat_lse;        // [rows * H]
   float* part;           // [kDecodeSlots][128][512]: states of shared rows
   float* part_lse;       // [kDecodeSlots][128]
@@ -68,7 +68,7 @@ struct DecodeParams {
   CUtensorMap tm_q;      // qlat as [rows * H][512] bf16, or [2 * rows * H][512] bytes, box 128 B x 128
   CUtensorMap tm_s;      // the cache's rows in blocks of 128 B, box 128 B x 64 rows x 1
   CUtensorMap tm_o;      // the same, box 128 B x 32 rows x 4 (bf16) or 128 B x 64 rows x 2 (FP8)
-  CUtensorMap tm_lat;    // lat as [rows * H][512], box 64 x 32
+  CUtensorMap tm_lat;    // lat as [rows * H][512], box 32 x 32
   CUtensorMap tm_part;   // part as [kDecodeSlots * 128][512], box 32 x 32
   DecodeBatch batch;
   DecodeSpace ws;
@@ -88,7 +88,7 @@ struct DecodeOutParams {
   CUtensorMap tm_w;      // kv_b_proj as [512][H * 256], box 64 x 128
   DecodeBatch batch;
   DecodeSpace ws;
-  int tile;              // tokens of a CTA (at most 128)
+  int tile;              // tokens of a CTA (at most 64)
   void* out;             // [rows][H][128]
   int out_bf16;
   float* lse;            // optional [rows][H]
