@@ -477,7 +477,7 @@ int mla_block_compare(const void* kv_cache, int kv_dtype, int num_blocks, const 
  *  norm_weight   device bf16 [512], 16-byte aligned, or NULL.
  *  cu_q          device int32 [num_reqs + 1]: ascending first rows of the
  *                requests; NULL: every request has rows / num_reqs rows.  Rows
- *                behind cu_q[num_reqs] are not read into the cache.
+ *                before cu_q[0] and behind cu_q[num_reqs] are left out.
  *  seq_lens      device int32 [num_reqs]: the requests' tokens with the new
  *                rows.  A row whose token index is negative (a padded request
  *                of length 0) is left out.
@@ -518,7 +518,8 @@ int mla_cache_append(const void* kv, int64_t kv_row_stride, const int32_t* pos, 
  *                (already in the cache, see mla_cache_append) included.
  *  cu_q          device int32 [num_reqs + 1], ascending first rows of the
  *                requests; NULL: every request has total_q / num_reqs rows.
- *                Rows behind cu_q[num_reqs] of out and lse are not written.
+ *                Rows of out and lse before cu_q[0] and behind
+ *                cu_q[num_reqs] are not written.
  *  out           device [total_q, H, 128], fp32 or bf16 per out_dtype.  A row
  *                that sees no key is 0.
  *  lse           device fp32 [total_q, H], optional (NULL): natural log, -inf
@@ -550,8 +551,8 @@ int mla_decode(const void* q, const int32_t* q_pos, const void* kv_cache, int kv
 /* Optional instrumentation.  With both arguments non-NULL (cudaEvent_t handles
  * created by the caller), every later mla_prefill_ctx call on this process
  * records `begin` on its stream just before its first fused prefill kernel
- * launch and `end` just after the last one (mla_prefill_ctx_absorbed: around
- * its latent attention kernel launches), so the caller can time the fused
+ * launch and `end` just after the last one (mla_prefill_ctx_absorbed and
+ * mla_decode: around their latent attention kernel launches), so the caller can time the fused
  * kernel alone with cudaEventElapsedTime.  NULL, NULL turns it off.  The
  * setting is process-wide; the caller keeps the events alive while it is on. */
 void mla_set_kernel_events(void* begin_event, void* end_event);

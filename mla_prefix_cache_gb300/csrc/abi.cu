@@ -1834,6 +1834,7 @@ int mla_cache_append(const void* kv, int64_t kv_row_stride, const int32_t* pos, 
   if (norm_weight != nullptr && (!aligned(norm_weight, 16) || !(norm_eps >= 0.f) || !std::isfinite(norm_eps)))
     return MLA_ERR_INVALID_ARG;
   if (!(rope_theta > 1.f) || !std::isfinite(rope_theta)) return MLA_ERR_INVALID_ARG;
+  if (kv_dtype == MLA_KV_FP8_E4M3 && !std::isfinite(1.f / kv_scale)) return MLA_ERR_INVALID_ARG;
   p.kv = static_cast<const uint16_t*>(kv);
   p.row_stride = kv_row_stride;
   p.pos = pos;

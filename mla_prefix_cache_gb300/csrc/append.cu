@@ -62,7 +62,13 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm) cache_append_kernel
     if (row + 1 < end) next = load_row(p, row + 1, lane);
     if (row >= past) {
       r = request_of_row(p.batch, row, lane);
-      if (r < 0) return;                    // behind the last request, and so are the rows after it
+      if (r < 0) {                          // no request's row: before the first one, or behind the last
+        past = row + 1;
+        id = -1;
+        len = 0;
+        lb = 0;
+        continue;
+      }
       past = request_rows(p.batch, r).y;
       len = __ldg(p.batch.seq_lens + r);
       lb = -1;

@@ -36,6 +36,8 @@
 // range keeps weights down to 2^-24 of the largest, and the rest in E4M3
 // (together below 2^-7, 1.3e-3 in the mean).  Two 8-bit MMAs take the time of
 // one bf16 MMA on a cache of half the bytes.
+#include <atomic>
+
 #include "serving.cuh"
 
 namespace mla {
@@ -684,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           if (lane == 0 && ok) mbar_arrive(bar(kPST + b));
         }
         if (tail && live && half == 0) {
-          const float lse = (ok && lsum > 0.f) ? (m_used - (kFp8 ? kPBiasFp8 : 0.f) + __log2f(lsum)) * 0.6931471805599453f
+          const float lse = (ok && lsum != 0.f) ? (m_used - (kFp8 ? kPBiasFp8 : 0.f) + __log2f(lsum)) * 0.6931471805599453f
                                               : -INFINITY;
           if (slot < 0) p.ws.lat_lse[orow] = lse;
           else p.ws.part_lse[slot * kItemRows + r] = lse;
@@ -857,7 +859,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           break;
         }
         tc_fence_after();
-        const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
+        const float inv = lsum != 0.f ? 1.f / lsum : 0.f;   // no key seen: 0; a NaN stays one
         const int rows = k.rows - k.row0;      // live rows of the item
         const bool whole = k.slot < 0;
         const int row0 = whole ? k.w.q_begin * H + k.row0 : k.slot * kItemRows;   // first row of the states
@@ -927,12 +929,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 }  // namespace
 
 cudaError_t launch_decode_attn(const DecodeParams& p, bool fp8, cudaStream_t s) {
-  static int configured = -1;
-  static int clusters = kDecodeClusters;
+  static std::atomic<int> resident_on[64];   // per device, 0: not configured yet
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (configured != dev) {
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  int clusters = resident_on[dev].load();
+  if (clusters == 0) {
     e = cudaFuncSetAttribute(decode_attn_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(decode_attn_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
@@ -952,7 +955,7 @@ cudaError_t launch_decode_attn(const DecodeParams& p, bool fp8, cudaStream_t s) 
     e = cudaOccupancyMaxActiveClusters(&resident, decode_attn_kernel<false>, &cfg);
     if (e != cudaSuccess) return e;
     clusters = resident < 1 ? 1 : resident < kDecodeClusters ? resident : kDecodeClusters;
-    configured = dev;
+    resident_on[dev].store(clusters);
   }
   return launch_dependent(fp8 ? decode_attn_kernel<true> : decode_attn_kernel<false>, dim3(2 * clusters), kThreads, kSmem,
                           p, s);

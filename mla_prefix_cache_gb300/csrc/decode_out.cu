@@ -12,6 +12,8 @@
 // Latency-bound: a row is two dependent loads from L2 (weights, states), so the
 // rows are spread over many warps (8 warps took 30 us for 64 tokens of 128
 // heads).
+#include <atomic>
+
 #include "serving.cuh"
 
 namespace mla {
@@ -129,8 +131,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_out_kernel(const __grid_co
       o.n = 0;
       if (u > 0) {
         o.x = f + (idx / kItemRows) * u + kItemUnits;
-        o.c0 = cluster_of(o.x, n_clusters, total);
-        o.n = cluster_of(o.x + u - kItemUnits - 1, n_clusters, total) - o.c0 + 1;
+        // (clamped: a cu_q that does not ascend must not lead outside the tables)
+        o.c0 = min(max(cluster_of(o.x, n_clusters, max(total, 1)), 0), kDecodeClusters - 1);
+        o.n = cluster_of(o.x + u - kItemUnits - 1, n_clusters, max(total, 1)) - o.c0 + 1;
+        o.n = min(max(o.n, 0), kDecodeClusters - o.c0);
         if (o.n == 1) o.lse = p.ws.lat_lse[(int64_t)(r0 + tid) * H + h];
       }
     }
@@ -180,13 +184,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode_out_kernel(const __grid_co
       float sum = 0.f;
 #pragma unroll
       for (int k = 0; k < kPerLane; ++k) {
-        w[k] = m == -INFINITY ? 0.f : __expf(w[k] - m);
+        w[k] = w[k] == -INFINITY ? 0.f : __expf(w[k] - m);   // a NaN stays one
         sum += w[k];
       }
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-      const float inv = sum > 0.f ? 1.f / sum : 0.f;
-      if (part == 0 && lane == 0) rows[i].lse = sum > 0.f ? m + __logf(sum) : -INFINITY;
+      const float inv = sum != 0.f ? 1.f / sum : 0.f;
+      if (part == 0 && lane == 0) rows[i].lse = sum != 0.f ? m + __logf(sum) : -INFINITY;
 #pragma unroll
       for (int k = 0; k < kPerLane; ++k) {
         if (32 * k >= o.n) break;
@@ -308,14 +312,15 @@ __global__ void __launch_bounds__(kThreads, 1) decode_out_kernel(const __grid_co
 }  // namespace
 
 cudaError_t launch_decode_out(const DecodeOutParams& p, cudaStream_t s) {
-  static int configured = -1;
+  static std::atomic<bool> configured[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (configured != dev) {
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!configured[dev].load()) {
     e = cudaFuncSetAttribute(decode_out_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e != cudaSuccess) return e;
-    configured = dev;
+    configured[dev].store(true);
   }
   return launch_dependent(decode_out_kernel, dim3((p.batch.rows.rows + p.tile - 1) / p.tile, 1, p.batch.num_heads), kThreads,
                           kSmem, p, s);

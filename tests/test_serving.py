@@ -194,7 +194,7 @@ def test_append_validates_without_gpu(lib):
            dict(eps=float("inf")), dict(cu=None), dict(sl=None), dict(B=0), dict(B=-1), dict(rows=-1), dict(bt=None),
            dict(mb=0), dict(mb=1 << 26), dict(theta=1.0), dict(theta=float("nan")), dict(cache=None),
            dict(cache=ctypes.c_void_p(4104)), dict(kvt=2), dict(nb=0), dict(kvt=1, scale=0.0),
-           dict(kvt=1, scale=float("nan"))]
+           dict(kvt=1, scale=float("nan")), dict(kvt=1, scale=1e-39)]      # (whose reciprocal overflows)
     for b in bad:
         assert call(**b) == _lib.MLA_ERR_INVALID_ARG, b
     assert call(rows=0, kv=None, pos=None) == _lib.MLA_OK      # nothing to do
@@ -219,6 +219,9 @@ def test_decode_validates_without_gpu(lib):
     for b in bad:
         assert call(**b) == _lib.MLA_ERR_INVALID_ARG, b
     assert call(H=129) == _lib.MLA_ERR_UNSUPPORTED
+    assert call(nb=1 << 25) == _lib.MLA_ERR_UNSUPPORTED            # 2^31 cached tokens
+    assert call(T=1 << 24, H=64) == _lib.MLA_ERR_UNSUPPORTED       # 2^30 rows
+    assert call(mb=1 << 24, T=1 << 15, H=128) == _lib.MLA_ERR_UNSUPPORTED     # 2^15 items of 2^23 tiles
     for b in (dict(ws=None), dict(ws=ctypes.c_void_p(4104)), dict(wb=n - 1)):
         assert call(**b) == _lib.MLA_ERR_WORKSPACE, b
     assert call(T=0, q=None) == _lib.MLA_OK
@@ -364,6 +367,13 @@ def test_append_bad_block_is_reported_and_nothing_written(api, bad):
 
 
 @gpu
+def test_append_leaves_rows_before_the_first_request_out(api):
+    c = append_case([70, 66], [2, 3], "bf16", seed=9, extra_rows=4)
+    c["kv"], c["pos"], c["cu"] = np.roll(c["kv"], 2, 0), np.roll(c["pos"], 2), c["cu"] + 2
+    check_append(c, run_append(api, c))
+
+
+@gpu
 def test_append_saturates_and_keeps_infinities_to_themselves(api):
     c = append_case([3], [3], "fp8_e4m3", norm=False, seed=6)
     x = bf16_values(c["kv"])
@@ -504,6 +514,67 @@ def test_decode_empty_rows(api):
     ref = decode_ref(wl, lens=lens)
     assert np.isneginf(ref[1][[0, 1, 3, 4]]).all() and np.isfinite(ref[1][[2, 5, 6]]).all()
     assert_decode(out, lse, ref)
+
+
+@gpu
+@pytest.mark.parametrize("kv", ["bf16", "fp8_e4m3"])
+def test_decode_more_requests_than_threads(api, kv):
+    # over 512 requests a thread of the schedule takes several; requests without rows or keys among them
+    n = 1100
+    check_decode(api, W.make_workload("mr", 2, [(13 * i) % 70 for i in range(n)], [(i * 5) % 3 for i in range(n)], kv_dtype=kv, seed=48))
+
+
+@gpu
+@pytest.mark.parametrize("kv", ["bf16", "fp8_e4m3"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_decode_keeps_a_bad_query_to_its_row(api, kv, value):
+    wl = W.make_workload("nan", 16, [700, 90, 9000], [2, 1, 1], kv_dtype=kv, seed=49)
+    d = Dev(api, wl)
+    d.q[1, 3, 5] = value          # no-RoPE part of one head's query; a RoPE value of another's
+    d.q[3, 7, 150] = value
+    out, lse = d.decode()
+    bad = torch.zeros((4, 16), dtype=torch.bool)
+    bad[1, 3] = bad[3, 7] = True
+    assert bool(torch.isnan(out[bad.cuda()]).any(-1).all()), "a bad query's row is not NaN"
+    keep = ~bad.numpy()
+    ref = decode_ref(wl)
+    o, x = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    assert np.isfinite(o[keep]).all()
+    assert np.linalg.norm(o[keep] - ref[0][keep]) <= REL_RMS * np.linalg.norm(ref[0][keep])
+    assert (np.abs(x[keep] - ref[1][keep]) <= ref[2][keep]).all()
+
+
+@gpu
+@pytest.mark.parametrize("kv", ["bf16", "fp8_e4m3"])
+def test_decode_sink_does_not_drown_the_others(api, kv):
+    """One key takes about 0.9 of every row's weight, 6000 others share the rest: each of their weights is about
+    2^-16 of the largest, and what they add together is there."""
+    wl = W.make_workload("sink", 16, [6000], [1], kv_dtype=kv, seed=51)
+    rng = np.random.Generator(np.random.PCG64(52))
+    wl.q[...] = 0
+    wl.q_pos[...] = 0
+    qr = W.f32_to_bf16_bits(rng.standard_normal(64, dtype=np.float32))
+    wl.q[..., 128:] = qr                                          # every head asks for the same k_rope
+    v = bf16_values(qr)
+    want = math.log(0.9 / 0.1 * 6000) / wl.softmax_scale          # the sink's score over the others' mean
+    sink = W.f32_to_bf16_bits((v / (v @ v) * want).astype(np.float32))
+    rows = wl.block_table[0][np.arange(6001) // 64], np.arange(6001) % 64
+    b, t = rows[0][77], rows[1][77]
+    wl.kv_cache[b, t, 512:] = sink if kv == "bf16" else sink.view(np.uint8)
+    # the others' latents share a direction, which stands out of their sum
+    c, _ = cache_values(wl.kv_cache[rows], kv, wl.kv_scale)
+    c = c * 0.7 + 1.0
+    c[77] = 0.125
+    if kv == "bf16":
+        wl.kv_cache[rows[0], rows[1], :512] = W.f32_to_bf16_bits(c.astype(np.float32))
+    else:
+        codes = torch.from_numpy((c / wl.kv_scale).clip(-448, 448).astype(np.float32)).to(torch.float8_e4m3fn)
+        wl.kv_cache[rows[0], rows[1], :512] = codes.view(torch.uint8).numpy()
+    d, out, lse = check_decode(api, wl)
+    # the sink alone would give 0.125 of the columns' sums: a good part of the output is the others'
+    ref = decode_ref(wl)[0]
+    alone = 0.125 * bf16_values(wl.kv_b_proj)[:, 16 * 128:].reshape(512, 16, 128).sum(0)
+    assert np.linalg.norm(ref - alone) > 0.3 * np.linalg.norm(ref)
 
 
 @gpu
