@@ -70,7 +70,7 @@ enum : uint32_t {
   kSE = 9,      // 9: the stage has been read (its MMAs are done, or Q is in TMEM)
   kSSF = 18,    // 2: S buffer written
   kSSR = 20,    // 2: the 8 softmax warps have read the S buffer
-  kQRd = 22,    // Q of the run in place (4 warps)
+  kQRd = 22,    // Q of the range in place (4 warps: qlat, 8 warps: q_rope)
   kQE = 23,     // the MMAs that read it are done
   kPST = 24,    // 2: P staged (8 warps)
   kPFR = 26,    // 2: the PV of the P tile is done (from the values CTA)
@@ -236,7 +236,7 @@ __device__ __noinline__ bool next_range(const DecodeParams& p, Walk& k) {
         if (++k.r < p.batch.rows.num_reqs) k.w = request_work(p.batch, k.r);
         continue;
       }
-      const int item = (k.at - k.first) / u;
+      const int item = k.at - k.first < u ? 0 : (k.at - k.first) / u;
       const int base = k.first + item * u;
       const int stop = min(base + u, k.end);
       k.lo = max(0, k.at - base - kItemUnits);
@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       uint32_t cnt = 1;
       if (scores) {
         if (i == kSSR || i == kSSR + 1 || i == kPST || i == kPST + 1) cnt = 8;
-        else if (i == kQRd) cnt = 4;
+        else if (i == kQRd) cnt = 12;
       } else if (i == kCD || i == kEP) {
         cnt = 8;
       }
@@ -486,46 +486,16 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       // the last two PV commits land before this CTA exits
       for (int v = max(0, g - 2); v < g && ok; ++v) ok = await(p, bar(kPFR + (v & 1)), (v >> 1) & 1);
     } else if (warp >= 12) {
-      // ---------------------------------------------------------- Q: qlat from its stages into TMEM, rotated q_rope
-      // into shared memory
+      // ---------------------------------------------------------- Q: qlat from its stages into TMEM
       const int r = tid - 384;
       const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
       bool ok = true;
       int e = 0, u = 0;
       while (next_of_group(p, k, r == 0, 7, 128)) {
-        const int prow = k.row0 + r;
-        const bool live = prow < k.rows;
-        const int64_t grow = (int64_t)k.w.q_begin + (live ? prow / H : 0);
-        const int64_t orow = (int64_t)k.w.q_begin * H + prow;
-        if (kFp8) grid_wait();   // for the queries' scales
-        const float rq = kFp8 && live ? 1.f / (p.ws.qscale[orow] * p.kv_scale) : 1.f;
-        const uint4* qr = reinterpret_cast<const uint4*>(p.q + orow * kDqk + kDnope);
-        const int64_t delta = live ? (int64_t)__ldg(p.q_pos + grow) - k.offset : 0;
-        uint4 x[8];
-#pragma unroll
-        for (int c = 0; c < 8; ++c) x[c] = live ? __ldg(qr + c) : make_uint4(0, 0, 0, 0);
         // the MMAs that read the Q before this are done
         if (ok && e > 0) ok = await_warp(p, bar(kQE), (e - 1) & 1);
         ++e;
         tc_fence_after();
-        // q_rope as a K-major swizzled block, turned in place by pos - offset (a row is one thread's); FP8
-        // scores count in units of the row's scale, so it is divided by that
-#pragma unroll
-        for (int c = 0; c < 8; ++c) sts128(sb + kQR + sw128_off((uint32_t)r, (uint32_t)c), x[c].x, x[c].y, x[c].z, x[c].w);
-#pragma unroll 2
-        for (int c = 0; c < 8; ++c) {
-          const uint32_t at = sb + kQR + sw128_off((uint32_t)r, (uint32_t)c);
-          uint32_t w4[4];
-          lds128(at, w4);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float sn, cs;
-            rope_sincos_sfu(delta, p.rope_frac[4 * c + i], &sn, &cs);
-            const float x0 = bf16_lo(w4[i]), x1 = bf16_hi(w4[i]);
-            w4[i] = pack_bf16((x0 * cs - x1 * sn) * rq, (x0 * sn + x1 * cs) * rq);
-          }
-          sts128(at, w4[0], w4[1], w4[2], w4[3]);
-        }
         if (k.head) {
 #pragma unroll 1
           for (int i = 0; i < kQBoxes; i += 2, u += 2) {
@@ -551,7 +521,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           }
         }
         tmem_wait_st();
-        fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
         if (lane == 0 && ok) mbar_arrive(bar(kQRd));
@@ -573,7 +542,33 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         const bool live = prow < k.rows;
         const int64_t orow = (int64_t)k.w.q_begin * H + prow;
         if (kFp8) grid_wait();   // for the queries' scales
-        const float sl2 = p.scale_log2 * (kFp8 && live ? p.ws.qscale[orow] * p.kv_scale : 1.f);
+        const float qs = kFp8 && live ? p.ws.qscale[orow] * p.kv_scale : 1.f, sl2 = p.scale_log2 * qs;
+        {
+          // q_rope turned by pos - offset, as a K-major swizzled block: chunks 4 half .. of the row.  This warp has
+          // seen the last S buffer of the range before, so no MMA reads the block.  FP8 scores count in units of
+          // the row's scale, so q_rope is divided by that.
+          const uint4* qr = reinterpret_cast<const uint4*>(p.q + orow * kDqk + kDnope) + 4 * half;
+          const int64_t delta = live ? (int64_t)__ldg(p.q_pos + k.w.q_begin + prow / H) - k.offset : 0;
+          const float rq = 1.f / qs;
+          uint4 x[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) x[c] = live ? __ldg(qr + c) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t w4[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float sn, cs;
+              rope_sincos_sfu(delta, p.rope_frac[16 * half + 4 * c + i], &sn, &cs);
+              const float x0 = bf16_lo(w4[i]), x1 = bf16_hi(w4[i]);
+              w4[i] = pack_bf16((x0 * cs - x1 * sn) * rq, (x0 * sn + x1 * cs) * rq);
+            }
+            sts128(sb + kQR + sw128_off((uint32_t)r, (uint32_t)(4 * half + c)), w4[0], w4[1], w4[2], w4[3]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && ok) mbar_arrive(bar(kQRd));
+        }
         const int qk = live ? k.w.len - (k.rows - 1 - prow) / H - 1 : -1;   // the last key token the row sees
         const int n = k.n, t0 = k.t0, k_lo = k.k_lo, k_hi = k.k_hi, slot = k.slot;
         const bool tail = k.tail;
