@@ -485,7 +485,7 @@ int mla_block_compare(const void* kv_cache, int kv_dtype, int num_blocks, const 
  *                id lies outside [0, num_blocks) or whose token lies behind
  *                the block table (the row is not written).
  *  kv_cache      written at those rows only; two rows of one call must not
- *                share a cache slot (either may be found there).
+ *                share a cache slot (its bytes may come from either).
  * Errors: MLA_ERR_INVALID_ARG, MLA_ERR_CUDA.
  * ---------------------------------------------------------------------- */
 int mla_cache_append(const void* kv, int64_t kv_row_stride, const int32_t* pos, const void* norm_weight,
@@ -524,18 +524,22 @@ int mla_cache_append(const void* kv, int64_t kv_row_stride, const int32_t* pos, 
  *                that sees no key is 0.
  *  lse           device fp32 [total_q, H], optional (NULL): natural log, -inf
  *                for a row that sees no key.
+ *  kv_scale      FP8 caches: 2^-32 .. 2^32.
  *  workspace     device, 256-B aligned, at least mla_decode_workspace_size(...)
  *                bytes; holds the device error word read by
  *                mla_get_device_error().  Calls that may overlap on the GPU
  *                must not share it.
  *  softmax_scale positive.
  *  num_heads     H in [1, 128].
- * Rows of the cache that some query of the request sees have to be finite;
- * others may hold anything.  A block id outside [0, num_blocks) reads as zero
+ * What a query does not see may hold anything, also where another query of the
+ * request sees it.  A query that sees a value that is not finite has NaN where
+ * the score is NaN or infinite, and nothing of that key where it is -infinite.
+ * A cu_q that does not ascend sets the error word as a bad block id does, and
+ * no row is attended.  A block id outside [0, num_blocks) reads as zero
  * rows and sets the error word, as does a sequence longer than its block
  * table, which is cut off there.
- * Errors: MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED (H > 128, a cache of 2^31
- * tokens or more, total_q * H of 2^30 or more, a batch whose block table and
+ * Errors: MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED (H > 128, a kv_scale outside
+ * its range, a cache of 2^31 tokens or more, total_q * H of 2^30 or more, a batch whose block table and
  * segments could hold 2^31 or more pairs of 128 rows and 128 keys),
  * MLA_ERR_WORKSPACE, MLA_ERR_CUDA.
  * ---------------------------------------------------------------------- */

@@ -432,6 +432,16 @@ def decode_workspace_size(num_reqs: int, total_q: int, num_heads: int) -> int:
     return int(n)
 
 
+def _decode_tensors(device, B, T_q, H, out, out_dtype, lse, return_lse, workspace):
+    if out is None:
+        out = torch.empty((T_q, H, 128), dtype=out_dtype, device=device)
+    if lse is None and return_lse:
+        lse = torch.empty((T_q, H), dtype=torch.float32, device=device)
+    if workspace is None:
+        workspace = torch.empty(decode_workspace_size(B, T_q, H), dtype=torch.uint8, device=device)
+    return out, lse, workspace
+
+
 def decode(q: torch.Tensor, q_pos: torch.Tensor, kv_cache: torch.Tensor, block_table: torch.Tensor,
            seq_lens: torch.Tensor, kv_b_proj: torch.Tensor, *, softmax_scale: float, rope_theta: float = 10000.0,
            kv_scale: float = 1.0, cu_q: Optional[torch.Tensor] = None, segments: Optional[torch.Tensor] = None,
@@ -463,12 +473,11 @@ def decode(q: torch.Tensor, q_pos: torch.Tensor, kv_cache: torch.Tensor, block_t
         gp = _at(seg_ptr, "seg_ptr", device, torch.int32, (B + 1,))
         if ns == 0:      # an empty tensor has no address: any one will do, nothing of it is read
             sp = gp
-    if out is None:
-        out = torch.empty((T_q, H, 128), dtype=out_dtype, device=q.device)
-    if lse is None and return_lse:
-        lse = torch.empty((T_q, H), dtype=torch.float32, device=q.device)
-    if workspace is None:
-        workspace = torch.empty(decode_workspace_size(B, T_q, H), dtype=torch.uint8, device=q.device)
+    if stream is None:
+        out, lse, workspace = _decode_tensors(q.device, B, T_q, H, out, out_dtype, lse, return_lse, workspace)
+    else:      # on the stream that uses them: freed memory goes to its later work only
+        with torch.cuda.stream(stream):
+            out, lse, workspace = _decode_tensors(q.device, B, T_q, H, out, out_dtype, lse, return_lse, workspace)
     bf16 = out.dtype is torch.bfloat16
     st = _lib.load().mla_decode(
         _at(q, "q", device, torch.bfloat16), _at(q_pos, "q_pos", device, torch.int32, (T_q,)),

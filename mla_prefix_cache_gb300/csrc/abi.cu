@@ -1895,11 +1895,14 @@ int mla_decode(const void* q, const int32_t* q_pos, const void* kv_cache, int kv
   if (!(softmax_scale > 0.f) || !std::isfinite(softmax_scale) || !(rope_theta > 1.f) || !std::isfinite(rope_theta))
     return MLA_ERR_INVALID_ARG;
   if (num_blocks > INT32_MAX / kBlock) return MLA_ERR_UNSUPPORTED;   // TMA row coordinates
+  // q_rope is divided by kv_scale and a query row's scale (1e-18 at least), in fp32 and bf16
+  if (kv_dtype == MLA_KV_FP8_E4M3 && !(kv_scale >= 0x1p-32f && kv_scale <= 0x1p32f)) return MLA_ERR_UNSUPPORTED;
   DecodeLayout d;
   if (!decode_layout(num_reqs, total_q, num_heads, &d)) return MLA_ERR_UNSUPPORTED;
-  // the most work units that any lengths can give (items x tiles of the longest sequence) stay within 31 bits
+  // the most work units that any lengths can give (items x tiles of the longest sequence, of which each segment's
+  // ends cost it up to 190 / 128) stay within 31 bits
   const double items = (double)total_q * num_heads / kItemRows + num_reqs;
-  if (items * ((double)max_blocks_per_req / 2 + num_segments + 4) >= 2147483648.0) return MLA_ERR_UNSUPPORTED;
+  if (items * ((double)max_blocks_per_req / 2 + 1.5 * num_segments + 5) >= 2147483648.0) return MLA_ERR_UNSUPPORTED;
   if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < d.total) return MLA_ERR_WORKSPACE;
   const int H = num_heads;
   const bool fp8 = kv_dtype == MLA_KV_FP8_E4M3;

@@ -80,7 +80,7 @@ struct QAbsorbParams {
   CUtensorMap tm_out2;     // the second codes, as tm_out
   float* qscale;           // [T_q * H]: E4M3 row scales, or null for bf16 qlat
   uint32_t* err;
-  uint32_t* clear;         // decode: the error word, which the launch sets to 0 (bf16 qlat, or two E4M3 terms);
+  uint32_t* clear = nullptr;   // decode: the error word, which the launch sets to 0 (bf16 qlat, or two E4M3 terms);
                            // the launch is a dependent one
   float scale;
   int row0;                // first token row of this launch

@@ -62,6 +62,7 @@ constexpr uint32_t kOStage = 16384;              // 256 latent columns of 32 bf1
 // both: per P buffer the rows' factors, sums and four rescale flags (staged and copied like P), then barriers
 constexpr uint32_t kFac = kSRing + kSStages * kBlk;
 static_assert(kFac == kORing + kOStages * kOStage, "the factors sit at one offset in both CTAs");
+// (a flag word has the 32 rows' rescaling in its low byte, a key that is not finite in the others)
 constexpr uint32_t kFacSum = 512, kFacFlags = 1024, kFacBytes = 1040;
 constexpr uint32_t kBars = kFac + 2 * kFacBytes;
 enum : uint32_t {
@@ -125,20 +126,22 @@ struct Start {
 // The units of all requests, and this cluster's run.  Every thread of the CTA;
 // thread t takes requests [t k, (t + 1) k).  CTA 0 of the grid leaves the
 // requests' first units for decode_out_kernel; true if this thread met a
-// sequence longer than its table.  It may run before the kernel that clears the
-// error word has.
+// sequence longer than its table.  A cu_q that does not ascend could count rows
+// twice and pass 31 bits: such a batch has no work, and every thread returns
+// true.  It may run before the kernel that clears the error word has.
 __device__ bool schedule(const DecodeParams& p, Start* st, int* scratch, int cluster) {
   const int B = p.batch.rows.num_reqs, k = (B + kThreads - 1) / kThreads;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int r0 = min(B, tid * k), r1 = min(B, r0 + k);
   RequestWork w;
   int sum = 0;
-  bool cut = false;   // a sequence longer than its table
+  bool cut = false, mixed = false;   // a sequence longer than its table, a request that ends before it starts
 #pragma unroll 1
   for (int r = r0; r < r1; ++r) {
     w = request_work(p.batch, r);
     sum += w.units() * w.items;
     cut |= __ldg(p.batch.rows.seq_lens + r) > p.batch.max_blocks * kBlock;
+    if (p.batch.rows.cu_q != nullptr) mixed |= __ldg(p.batch.rows.cu_q + r + 1) < __ldg(p.batch.rows.cu_q + r);
   }
   int pre = sum;
 #pragma unroll
@@ -148,7 +151,7 @@ __device__ bool schedule(const DecodeParams& p, Start* st, int* scratch, int clu
   }
   if (lane == 31) scratch[warp] = pre;
   if (tid == 0) st->r = B;
-  __syncthreads();
+  mixed = __syncthreads_or(mixed);
   int total = 0;
 #pragma unroll 4
   for (int i = 0; i < kThreads / 32; ++i) {
@@ -156,6 +159,7 @@ __device__ bool schedule(const DecodeParams& p, Start* st, int* scratch, int clu
     total += scratch[i];
   }
   pre -= sum;   // units of the requests before r0
+  if (mixed) pre = sum = total = 0;
   const int n = min(total, (int)gridDim.x / 2);
   const int begin = cluster < n ? unit_begin(cluster, n, total) : total;
   if (tid == 0) {
@@ -174,7 +178,7 @@ __device__ bool schedule(const DecodeParams& p, Start* st, int* scratch, int clu
     for (int r = r0; r < r1; ++r) {
       if (k > 1) w = request_work(p.batch, r);
       if (blockIdx.x == 0) p.ws.first[r] = at;
-      const int next = at + w.units() * w.items;
+      const int next = mixed ? at : at + w.units() * w.items;
       if (mine && !found && begin < next) {
         found = true;
         st->r = r;
@@ -185,7 +189,7 @@ __device__ bool schedule(const DecodeParams& p, Start* st, int* scratch, int clu
     }
   }
   __syncthreads();
-  return cut;
+  return cut || mixed;
 }
 
 // A cluster's run of units, walked alike by every role, as ranges of key tiles
@@ -344,6 +348,33 @@ __device__ __noinline__ void zero_rows(uint32_t stage, int lo, int hi, int lane)
   __syncwarp();
 }
 
+// Zeroes the 16-byte pieces of a tile's values stages (from stage s on, of parity ph) that hold a value that is not
+// finite, as above.  The ring holds a whole tile.
+template <bool kFp8>
+__device__ __noinline__ bool zero_not_finite(const DecodeParams& p, uint32_t sb, int s, uint32_t ph, int lane) {
+  constexpr uint32_t kOnes = kFp8 ? 0x7F7F7F7Fu : 0x7F807F80u;   // E4M3's NaN, bf16's exponent
+  constexpr int kStages = 128 * 1024 / (kFp8 ? 2 : 1) / kOStage;
+  static_assert(kStages <= kOStages, "a tile's stages");
+  bool ok = true;
+#pragma unroll 1
+  for (int i = 0; i < kStages && ok; ++i) {
+    ok = await_warp(p, sb + kBars + 8 * (kCF + s), ph);
+    const uint32_t stage = sb + kORing + s * kOStage;
+#pragma unroll 1
+    for (uint32_t at = stage + 16 * lane; ok && at < stage + kOStage; at += 512) {
+      uint32_t w[4], any = 0;
+      lds128(at, w);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) any |= kFp8 ? __vcmpeq4(w[k] & kOnes, kOnes) : __vcmpeq2(w[k] & kOnes, kOnes);
+      if (any) sts128(at, 0u, 0u, 0u, 0u);
+    }
+    if (++s == kOStages) { s = 0; ph ^= 1u; }
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+  return ok;
+}
+
 template <bool kFp8>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     decode_attn_kernel(const __grid_constant__ DecodeParams p) {
@@ -359,6 +390,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   constexpr int kQBoxes = 8;                                         // and of an item's Q
   constexpr int kORows = kFp8 ? 64 : 32, kOPerTile = 128 / kORows;   // key rows of a values stage
 
+  // for the reads that come before the wait for the kernels before this one: no stale L1
+  if (warp == 3) asm volatile("fence.acq_rel.gpu;" ::: "memory");
   if (tid == 0) {
     prefetch_tensormap(scores ? &p.tm_s : &p.tm_o);
     prefetch_tensormap(scores ? &p.tm_q : &p.tm_part);
@@ -380,6 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     tmem_relinquish();
   }
   tc_fence_before();
+  __syncthreads();
   const bool cut = schedule(p, start, reinterpret_cast<int*>(smem), cluster);
   cluster_sync_all();   // both CTAs' barriers exist before either is signalled
   tc_fence_after();
@@ -591,6 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           // relaxed: the reads are ordered for the next MMAs by the tcgen05 fences around it
           if (lane == 0 && ok) mbar_arrive_relaxed(bar(kSSR + b));
           const int kt0 = t0 + 128 * j + 64 * half;
+          float odd = 0.f;   // NaN: a score that is not finite among columns that may be hidden from the row
           if (!(kt0 >= k_lo && kt0 + 63 < k_hi && kt0 + 63 <= qk)) {
             const int hi = min(k_hi - 1, qk) - kt0, lo = k_lo - kt0;   // visible columns lo .. hi
             float m4[4];
@@ -598,6 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             for (int i = 0; i < 4; ++i) m4[i] = -INFINITY;
 #pragma unroll
             for (int c = 0; c < 64; c += 2) {
+              odd = fmaf(__uint_as_float(v[c]), 0.f, fmaf(__uint_as_float(v[c + 1]), 0.f, odd));
               const float xa = (c >= lo && c <= hi) ? __uint_as_float(v[c]) : -INFINITY;
               const float xb = (c + 1 >= lo && c + 1 <= hi) ? __uint_as_float(v[c + 1]) : -INFINITY;
               v[c] = __float_as_uint(xa);
@@ -671,10 +707,15 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                                      : stg + half * kBlk + sw128_off((uint32_t)r, (uint32_t)c);
             sts128(at, pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
           }
+          // P = 0 does not hide a key that is not finite from O: a query before it would have NaN
+          const uint32_t any_odd = __any_sync(0xffffffffu, odd != 0.f) ? 0x100u : 0u;
+          uint16_t* flag = reinterpret_cast<uint16_t*>(fac + kFacFlags + 4 * (warp & 3)) + half;
           if (half == 0) {
             reinterpret_cast<float*>(fac)[r] = alpha;
             const uint32_t any_rescale = __any_sync(0xffffffffu, alpha != 1.f) ? 1u : 0u;
-            if (lane == 0) reinterpret_cast<uint32_t*>(fac + kFacFlags)[warp & 3] = any_rescale;
+            if (lane == 0) *flag = (uint16_t)(any_odd | any_rescale);
+          } else if (lane == 0) {
+            *flag = (uint16_t)any_odd;
           }
           fence_proxy_async_smem();   // the staged tile is read by the bulk copies (async proxy)
           __syncwarp();
@@ -734,10 +775,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         for (int j = 0; j < k.n && ok; ++j, ++g) {
           const int b = g & 1;
           if (!await_warp(p, bar(kPF + b), (g >> 1) & 1)) { ok = false; break; }
+          uint32_t f[4];
+          lds128(sb + kFac + b * kFacBytes + kFacFlags, f);
+          const uint32_t flags = f[0] | f[1] | f[2] | f[3];
           if (!head) {
-            uint32_t f[4];
-            lds128(sb + kFac + b * kFacBytes + kFacFlags, f);
-            if (f[0] | f[1] | f[2] | f[3]) {
+            if (flags & 0xFFu) {
               // O must hold the PV of every earlier tile before its rows are rescaled
               if (!await_warp(p, bar(kPVD + ((g - 1) & 1)), ((g - 1) >> 1) & 1)) { ok = false; break; }
               if (lane == 0) {
@@ -758,6 +800,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             }
             if (!await_warp(p, bar(kCD), events++ & 1)) { ok = false; break; }
           }
+          if ((flags & ~0xFFu) && !zero_not_finite<kFp8>(p, sb, s, ph, lane)) { ok = false; break; }
           fence_proxy_async_smem();   // P was written by the other CTA's copy, the MMA reads it as an operand
           if (lane == 0) mbar_arrive_expect_tx_relaxed(bar(kPF + b), kTxP);
           __syncwarp();

@@ -61,9 +61,9 @@ __device__ __forceinline__ int find_request(const BatchRows& b, int x) {
   int lo = 0, hi = b.num_reqs - 1;   // the last request that starts at or before x
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(b.cu_q + mid) <= x) lo = mid; else hi = mid - 1;
+    if (__ldcg(b.cu_q + mid) <= x) lo = mid; else hi = mid - 1;
   }
-  const int2 rr = request_rows(b, lo);
+  const int2 rr = request_rows<true>(b, lo);
   return x >= rr.x && x < rr.y ? lo : -1;
 }
 
@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_out_kernel(const __grid_co
   int2 rr = make_int2(0, 0);
   if (tid < R) {
     r = find_request(p.batch.rows, r0 + tid);
-    if (r >= 0) rr = request_rows(p.batch.rows, r);
+    if (r >= 0) rr = request_rows<true>(p.batch.rows, r);
   }
   grid_wait();      // the attention kernel's states are there
   grid_trigger();

@@ -12,7 +12,10 @@ namespace mla {
 // grid_trigger() (or ended); grid_wait() in it returns when that one is done and
 // its memory visible.  Each kernel here waits before it triggers, and every CTA
 // waits: so what a dependent kernel reads before its own wait was there before
-// the kernel that it depends on, and one wait covers all earlier kernels.
+// the kernel that it depends on, and one wait covers all earlier kernels.  Nothing
+// says that an SM's L1, which may hold what an earlier call found at the same
+// address, is cleared before the wait: those reads go to L2 (kL2), or come after
+// a fence of the CTA.
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
@@ -32,11 +35,13 @@ cudaError_t launch_dependent(void (*kernel)(Params), dim3 grid, int threads, siz
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-// First row of request r and one past its last, clamped to the batch's rows.
+// First row of request r and one past its last, clamped to the batch's rows; kL2: see grid_wait.
+template <bool kL2 = false>
 __device__ __forceinline__ int2 request_rows(const BatchRows& b, int r) {
   if (b.cu_q == nullptr) return make_int2(r * b.per_req, (r + 1) * b.per_req);
-  const int lo = min(max(__ldg(b.cu_q + r), 0), b.rows);
-  return make_int2(lo, min(max(__ldg(b.cu_q + r + 1), lo), b.rows));
+  const int c0 = kL2 ? __ldcg(b.cu_q + r) : __ldg(b.cu_q + r), c1 = kL2 ? __ldcg(b.cu_q + r + 1) : __ldg(b.cu_q + r + 1);
+  const int lo = min(max(c0, 0), b.rows);
+  return make_int2(lo, min(max(c1, lo), b.rows));
 }
 
 // The request that row `row` belongs to, or -1 (behind the last request).  A

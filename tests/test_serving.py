@@ -219,6 +219,7 @@ def test_decode_validates_without_gpu(lib):
     for b in bad:
         assert call(**b) == _lib.MLA_ERR_INVALID_ARG, b
     assert call(H=129) == _lib.MLA_ERR_UNSUPPORTED
+    assert call(kvt=1, scale=2.0 ** -33) == call(kvt=1, scale=2.0 ** 33) == _lib.MLA_ERR_UNSUPPORTED
     assert call(nb=1 << 25) == _lib.MLA_ERR_UNSUPPORTED            # 2^31 cached tokens
     assert call(T=1 << 24, H=64) == _lib.MLA_ERR_UNSUPPORTED       # 2^30 rows
     assert call(mb=1 << 24, T=1 << 15, H=128) == _lib.MLA_ERR_UNSUPPORTED     # 2^15 items of 2^23 tiles
@@ -546,6 +547,51 @@ def test_decode_keeps_a_bad_query_to_its_row(api, kv, value):
 
 @gpu
 @pytest.mark.parametrize("kv", ["bf16", "fp8_e4m3"])
+@pytest.mark.parametrize("where", [0, 511, 515])      # latent values, a RoPE value
+@pytest.mark.parametrize("value", ["nan", "inf"])
+def test_decode_keeps_a_bad_new_token_from_the_queries_before_it(api, kv, where, value):
+    # the last token but one of each request's new ones, in the first tile, behind whole ones, at a tile's start and
+    # among many queries: only its own query and the last one see it
+    new = [4, 3, 2, 150]
+    wl = W.make_workload("nt", 16, [20, 1000, 127, 90], new, kv_dtype=kv, seed=53)
+    codes = W.BF16_NAN if value == "nan" else 0xFF80
+    rows = np.zeros(sum(new), dtype=bool)
+    for r, n in enumerate(wl.seq_lens):
+        t = int(n) - 2
+        row = wl.kv_cache[wl.block_table[r][t // 64], t % 64]
+        if kv == "bf16":
+            row[where] = codes
+        elif where < 512:
+            row[where] = W.E4M3_NAN                    # (E4M3 has no infinity)
+        else:
+            row[512:].view(np.uint16)[where - 512] = codes
+        rows[int(wl.cu_q[r + 1]) - 2:int(wl.cu_q[r + 1])] = True
+    out, lse = Dev(api, wl).decode()
+    assert api.device_error(api.decode.last_workspace) == 0
+    with np.errstate(all="ignore"):
+        ref = decode_ref(wl)
+    nan = value == "nan" or (kv != "bf16" and where < 512)
+    if nan:
+        assert bool(torch.isnan(out[torch.from_numpy(rows).cuda()]).all())
+    for x in ref[:2]:
+        x[rows] = np.nan                               # left out of the comparison
+    assert_decode(out, lse, ref)
+
+
+@gpu
+def test_decode_cu_q_that_does_not_ascend_is_reported(api):
+    wl = W.make_workload("mix", 16, [300, 90, 1000], [2, 1, 2], seed=54)
+    d = Dev(api, wl)
+    for cu in ([0, 3, 2, 5], [0, 2, 3, -1], [5, 0, 5, 2]):
+        out, lse = d.decode(cu_q=torch.tensor(cu, dtype=torch.int32, device="cuda"))
+        assert api.device_error(api.decode.last_workspace) == _lib.MLA_ERR_BAD_BLOCK_ID
+    out, lse = d.decode()
+    assert api.device_error(api.decode.last_workspace) == 0
+    assert_decode(out, lse, decode_ref(wl))
+
+
+@gpu
+@pytest.mark.parametrize("kv", ["bf16", "fp8_e4m3"])
 def test_decode_sink_does_not_drown_the_others(api, kv):
     """One key takes about 0.9 of every row's weight, 6000 others share the rest: each of their weights is about
     2^-16 of the largest, and what they add together is there."""
@@ -788,3 +834,59 @@ def test_serving_calls_on_two_streams(api):
     torch.cuda.synchronize()
     for (o, x), (eo, ex) in zip(outs, want):
         assert torch.equal(o, eo) and torch.equal(x, ex)
+
+
+@gpu
+@pytest.mark.parametrize("kv", ["bf16", "fp8_e4m3"])
+def test_decode_sees_inputs_that_copies_changed_between_calls(api, kv):
+    """Calls one behind the other with nothing but copies between them that put other queries, positions, lengths,
+    row counts and segments at the same addresses: each call has its own, bit for bit."""
+    wl = W.make_workload("cp", 16, [700, 300, 2000], [3, 2, 1], kv_dtype=kv, seed=56)
+    d = Dev(api, wl, [[(0, 100, 0)], [(0, 50, 3)], []])
+    rng = np.random.Generator(np.random.PCG64(57))
+    versions = []
+    for cu, lens, segs in (([0, 3, 5, 6], [703, 302, 2001], [(0, 100, 0), (0, 50, 3)]),
+                           ([0, 1, 2, 6], [200, 9, 1500], [(10, 30, 5), (0, 5, 1)]),
+                           ([0, 0, 6, 6], [40, 290, 1000], [(0, 9, 9), (100, 100, 100)]),
+                           ([1, 2, 3, 4], [64, 0, 1999], [(3, 4, 5), (6, 7, 8)])):
+        q = W.f32_to_bf16_bits(rng.standard_normal(wl.q.shape, dtype=np.float32))
+        x = [torch.from_numpy(q.view(np.int16)).view(torch.bfloat16), torch.from_numpy(rng.integers(0, 10 ** 5, 6, dtype=np.int32)),
+             torch.tensor(lens, dtype=torch.int32), torch.tensor(cu, dtype=torch.int32), torch.tensor(segs, dtype=torch.int64)]
+        versions.append([t.pin_memory() for t in x])
+    at = [d.q, d.q_pos, d.seq_lens, d.cu_q, d.segments]
+    want = []
+    for v in versions:
+        own = [t.cuda() for t in v]
+        d.q, d.q_pos, d.seq_lens, d.cu_q, d.segments = own
+        want.append(d.decode(out=torch.zeros((6, 16, 128), device="cuda"), lse=torch.zeros((6, 16), device="cuda")))
+        torch.cuda.synchronize()
+    d.q, d.q_pos, d.seq_lens, d.cu_q, d.segments = at
+    ws = torch.empty(api.decode_workspace_size(3, 6, 16), dtype=torch.uint8, device="cuda")
+    got = [(torch.zeros((6, 16, 128), device="cuda"), torch.zeros((6, 16), device="cuda")) for _ in range(24)]
+    torch.cuda.synchronize()
+    for i, (o, x) in enumerate(got):
+        for t, v in zip(at, versions[i % 4]):
+            t.copy_(v, non_blocking=True)
+        d.decode(out=o, lse=x, workspace=ws)
+    torch.cuda.synchronize()
+    assert api.device_error(ws) == 0
+    for i, (o, x) in enumerate(got):
+        assert torch.equal(o, want[i % 4][0]) and torch.equal(x, want[i % 4][1]), i
+
+
+@gpu
+def test_decode_allocates_on_the_stream_that_it_runs_on(api):
+    """Outputs and workspaces that the call makes itself are not handed to later work of another stream while it runs."""
+    wl = W.make_workload("st", 64, [6000, 40], [1, 2], seed=55)
+    d = Dev(api, wl)
+    want = d.decode()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got, junk = [], []
+    for _ in range(8):
+        got.append(d.decode(stream=side))
+        junk.append(torch.full((api.decode_workspace_size(2, 3, 64),), 255, dtype=torch.uint8, device="cuda"))
+        del junk[:-1]
+    torch.cuda.synchronize()
+    for o, x in got:
+        assert torch.equal(o, want[0]) and torch.equal(x, want[1])
