@@ -1925,7 +1925,7 @@ int mla_decode(const void* q, const int32_t* q_pos, const void* kv_cache, int kv
   space.part = reinterpret_cast<float*>(ws + d.part);
   space.part_lse = reinterpret_cast<float*>(ws + d.part_lse);
 
-  QAbsorbParams qp;
+  DecodeQParams qp;
   DecodeParams p;
   DecodeOutParams op;
   bool ok = true;
@@ -1972,12 +1972,11 @@ int mla_decode(const void* q, const int32_t* q_pos, const void* kv_cache, int kv
 
   qp.qscale = fp8 ? space.qscale : nullptr;
   qp.err = space.err;
-  qp.clear = space.err;
   qp.scale = 1.f;
   qp.row0 = 0;
   qp.tokens = total_q;
   qp.num_heads = H;
-  if ((st = cuda_status(launch_qabsorb(qp, s))) != MLA_OK) return st;
+  if ((st = cuda_status(launch_decode_qabsorb(qp, s))) != MLA_OK) return st;
 
   p.batch = batch;
   p.ws = space;

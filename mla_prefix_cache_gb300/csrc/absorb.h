@@ -70,18 +70,13 @@ static_assert(sizeof(AbsorbParams) <= 32000, "kernel parameter space");
 // q absorption (headproj.cu), over tokens row0 .. row0 + tokens - 1:
 //   qlat[t][h][c] = bf16(scale sum_d q[t][h][d] W[c][128 h + d])        (qscale null)
 //   qlat8[t][h][c] = e4m3(qlat / s), qscale[t H + h] = s = amax / 448  (qscale set; scale unused)
-// and, with `clear`, also the codes of what that leaves, e4m3(qlat / s - qlat8):
-// the two together hold qlat to about 2^-8 of itself.
 struct QAbsorbParams {
   CUtensorMap tm_q;        // q as (column, head, token) up to token row0 + tokens, box 64 x 1 x 128
   CUtensorMap tm_w;        // kv_b_proj as [512][H * 256], box 64 x 256
   CUtensorMap tm_out;      // qlat (bf16, box 64 x 1 x 128) or qlat8 (bytes, box 128 x 1 x 128) as
                            // (column, head, token) up to token row0 + tokens
-  CUtensorMap tm_out2;     // the second codes, as tm_out
   float* qscale;           // [T_q * H]: E4M3 row scales, or null for bf16 qlat
   uint32_t* err;
-  uint32_t* clear = nullptr;   // decode: the error word, which the launch sets to 0 (bf16 qlat, or two E4M3 terms);
-                           // the launch is a dependent one
   float scale;
   int row0;                // first token row of this launch
   int tokens;              // rows row0 .. row0 + tokens - 1

@@ -1,9 +1,9 @@
 // The two per-head projections of the absorbed (latent-space) path ("DeepSeek
 // MLA — Prefix Cache 与 Chunked Prefill 深度解析", section 3: W_UK folded into
 // the query, W_UV applied after the attention), on the tensor cores:
-//   qabsorb_kernel<kBf16>  qlat[t][h][:]  = bf16(scale q_nope[t][h] W_UK,h^T)   [512]
-//   qabsorb_kernel<kE4m3>  qlat8[t][h][:] = e4m3(qlat / s), s = amax / 448 of the row
-//   qabsorb_kernel<kTwoE4m3>  the same, and e4m3(qlat / s - qlat8)
+//   qabsorb_kernel<false>  qlat[t][h][:]  = bf16(scale q_nope[t][h] W_UK,h^T)   [512]
+//   qabsorb_kernel<true>   qlat8[t][h][:] = e4m3(qlat / s), s = amax / 448 of the row
+//                          (for decode also e4m3(qlat / s - qlat8))
 //   absorb_proj_kernel     out[t][h][:]   = scale o[t H + h] W_UV,h             [128]
 // Both are one tcgen05 MMA chain per CTA (M = 128 rows of one head), operands
 // staged in shared memory with 128-byte swizzle, the accumulator in TMEM.
@@ -11,6 +11,8 @@
 // kv_b_proj is [512][H * 256]: W_UK,h[c][d] at column 128 h + d, W_UV,h[c][j]
 // at column 128 H + 128 h + j.  So W_UK,h is K-major for the q absorption (K =
 // d) and W_UV,h is MN-major for the projection (K = c, N = j contiguous).
+#include <type_traits>
+
 #include "absorb.h"
 #include "internal.h"
 #include "ptx.cuh"
@@ -33,11 +35,8 @@ __device__ __forceinline__ bool hwait(uint32_t* err, uint32_t bar, uint32_t pari
 // Shared memory: A = q_nope [128 x 128] as two [128 x 64] blocks, then B = the
 // CTA's rows of W_UK,h as [256 c x 64 d] blocks (d block, c half); after the
 // MMAs the same memory stages the output rows for the TMA stores.
-enum QaForm { kBf16, kE4m3, kTwoE4m3 };
-
-template <int kForm>
+template <bool kF8>
 struct QA {
-  static constexpr bool kF8 = kForm != kBf16;
   static constexpr int kCols = kF8 ? 512 : 256;           // latent columns of a CTA
   static constexpr int kHalves = kCols / 256;
   static constexpr uint32_t kA = 0;
@@ -48,10 +47,10 @@ struct QA {
 };
 constexpr uint32_t kIdescQA = idesc_bf16(128, 256, false, false);
 
-template <int kForm>
-__global__ void __launch_bounds__(128, 1) qabsorb_kernel(const __grid_constant__ QAbsorbParams p) {
-  using L = QA<kForm>;
-  constexpr bool kF8 = L::kF8;
+template <bool kF8, class Params>
+__global__ void __launch_bounds__(128, 1) qabsorb_kernel(const __grid_constant__ Params p) {
+  using L = QA<kF8>;
+  constexpr bool kDecode = std::is_same<Params, DecodeQParams>::value, kTwo = kF8 && kDecode;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* sgen = smem_raw + (sbase - smem_u32(smem_raw));
@@ -61,10 +60,10 @@ __global__ void __launch_bounds__(128, 1) qabsorb_kernel(const __grid_constant__
   const int h = blockIdx.z;
   const int c0 = blockIdx.y * L::kCols;
   const int t0 = p.row0 + blockIdx.x * 128;   // first token of the tile (TMA coordinates)
-  if (p.clear != nullptr) {                   // decode: launched dependently
+  if constexpr (kDecode) {                    // launched dependently
     grid_wait();      // the inputs are there
     grid_trigger();   // the attention kernel may start its own set-up
-    if (threadIdx.x == 0 && (blockIdx.x | blockIdx.y | blockIdx.z) == 0) *p.clear = 0u;
+    if (threadIdx.x == 0 && (blockIdx.x | blockIdx.y | blockIdx.z) == 0) *p.err = 0u;
   }
 
   if (threadIdx.x == 0) {
@@ -138,7 +137,7 @@ __global__ void __launch_bounds__(128, 1) qabsorb_kernel(const __grid_constant__
         for (int i = 0; i < 32; ++i) m = fmaxf(m, fabsf(__uint_as_float(v[i])));
       }
       // two terms: the scale is kept where q_rope can still be divided by it
-      const float sc = kForm == kTwoE4m3 ? fmaxf(m / 448.f, 1e-18f) : (m > 0.f ? m / 448.f : 1.f);
+      const float sc = kTwo ? fmaxf(m / 448.f, 1e-18f) : (m > 0.f ? m / 448.f : 1.f);
       const float inv = 1.f / sc;
       // 32 columns a load: 32 B of E4M3 = two 16-byte chunks of a [128 x 128 B] block
 #pragma unroll 1
@@ -157,14 +156,14 @@ __global__ void __launch_bounds__(128, 1) qabsorb_kernel(const __grid_constant__
             for (int e = 0; e < 4; ++e) x[e] = __uint_as_float(v[k + e]) * inv;
             const uint32_t lo = pack_e4m3x2(x[0], x[1]), hi = pack_e4m3x2(x[2], x[3]);
             w[i] = lo | (hi << 16);
-            if constexpr (kForm == kTwoE4m3) {
+            if constexpr (kTwo) {
               const float2 fl = e4m3x2_floats(lo), fh = e4m3x2_floats(hi);   // exact, and so are the differences
               w2[i] = (uint32_t)pack_e4m3x2(x[0] - fl.x, x[1] - fl.y) |
                       ((uint32_t)pack_e4m3x2(x[2] - fh.x, x[3] - fh.y) << 16);
             }
           }
           sts128(blk + sw128_off(r, (j & 3) * 2 + c), w[0], w[1], w[2], w[3]);
-          if constexpr (kForm == kTwoE4m3)
+          if constexpr (kTwo)
             sts128(blk + 4 * kAtomRows128 + sw128_off(r, (j & 3) * 2 + c), w2[0], w2[1], w2[2], w2[3]);
         }
       }
@@ -179,7 +178,7 @@ __global__ void __launch_bounds__(128, 1) qabsorb_kernel(const __grid_constant__
     // rows past the launch's last token are clipped by the map
 #pragma unroll
     for (int b = 0; b < 4; ++b) tma_store_3d(&p.tm_out, sbase + b * kAtomRows128, c0 + (kF8 ? 128 : 64) * b, h, t0);
-    if constexpr (kForm == kTwoE4m3) {
+    if constexpr (kTwo) {
 #pragma unroll
       for (int b = 0; b < 4; ++b) tma_store_3d(&p.tm_out2, sbase + (4 + b) * kAtomRows128, 128 * b, h, t0);
     }
@@ -338,9 +337,10 @@ cudaError_t configure_headproj() {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess || configured_device == dev) return e;
-  e = set_smem(qabsorb_kernel<kBf16>, QA<kBf16>::kSmem);
-  if (e == cudaSuccess) e = set_smem(qabsorb_kernel<kE4m3>, QA<kE4m3>::kSmem);
-  if (e == cudaSuccess) e = set_smem(qabsorb_kernel<kTwoE4m3>, QA<kTwoE4m3>::kSmem);
+  e = set_smem(qabsorb_kernel<false, QAbsorbParams>, QA<false>::kSmem);
+  if (e == cudaSuccess) e = set_smem(qabsorb_kernel<true, QAbsorbParams>, QA<true>::kSmem);
+  if (e == cudaSuccess) e = set_smem(qabsorb_kernel<false, DecodeQParams>, QA<false>::kSmem);
+  if (e == cudaSuccess) e = set_smem(qabsorb_kernel<true, DecodeQParams>, QA<true>::kSmem);
   if (e == cudaSuccess) e = set_smem(absorb_proj_kernel, kPSmem);
   if (e == cudaSuccess) configured_device = dev;
   return e;
@@ -354,13 +354,19 @@ cudaError_t launch_qabsorb(const QAbsorbParams& p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const bool f8 = p.qscale != nullptr;
   const dim3 grid((p.tokens + 127) / 128, f8 ? 1 : kDc / 256, p.num_heads);
-  if (p.clear != nullptr)
-    return f8 ? launch_dependent(qabsorb_kernel<kTwoE4m3>, grid, 128, QA<kTwoE4m3>::kSmem, p, s)
-              : launch_dependent(qabsorb_kernel<kBf16>, grid, 128, QA<kBf16>::kSmem, p, s);
-  if (f8) qabsorb_kernel<kE4m3><<<grid, 128, QA<kE4m3>::kSmem, s>>>(p);
-  else qabsorb_kernel<kBf16><<<grid, 128, QA<kBf16>::kSmem, s>>>(p);
+  if (f8) qabsorb_kernel<true><<<grid, 128, QA<true>::kSmem, s>>>(p);
+  else qabsorb_kernel<false><<<grid, 128, QA<false>::kSmem, s>>>(p);
   count_launch();
   return cudaGetLastError();
+}
+
+cudaError_t launch_decode_qabsorb(const DecodeQParams& p, cudaStream_t s) {
+  cudaError_t e = configure_headproj();
+  if (e != cudaSuccess) return e;
+  const bool f8 = p.qscale != nullptr;
+  const dim3 grid((p.tokens + 127) / 128, f8 ? 1 : kDc / 256, p.num_heads);
+  return f8 ? launch_dependent(qabsorb_kernel<true, DecodeQParams>, grid, 128, QA<true>::kSmem, p, s)
+            : launch_dependent(qabsorb_kernel<false, DecodeQParams>, grid, 128, QA<false>::kSmem, p, s);
 }
 
 cudaError_t launch_absorb_proj(const ProjParams& p, cudaStream_t s) {

@@ -2,8 +2,8 @@
 // key ranges, E4M3 values.
 #pragma once
 
-#include "ptx.cuh"
 #include "serving.h"
+#include "serving_ptx.cuh"
 
 namespace mla {
 

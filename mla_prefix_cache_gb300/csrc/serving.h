@@ -2,6 +2,7 @@
 // cache: appending new rows (append.cu) and decode attention (decode.cu).
 #pragma once
 
+#include "absorb.h"
 #include "internal.h"
 
 namespace mla {
@@ -51,6 +52,15 @@ struct DecodeBatch {
   int max_blocks;
   int num_heads;
 };
+
+// Query absorption for decode (headproj.cu): as QAbsorbParams, but the E4M3 form
+// has also the codes of what the first ones leave, e4m3(qlat / s - qlat8) (the two
+// together hold qlat to about 2^-8 of itself), and the launch, a dependent one,
+// sets the error word to 0.
+struct DecodeQParams : QAbsorbParams {
+  CUtensorMap tm_out2;     // the second codes, as tm_out
+};
+cudaError_t launch_decode_qabsorb(const DecodeQParams& p, cudaStream_t s);
 
 // Latent attention (decode.cu).  Workspace arrays:
 struct DecodeSpace {
