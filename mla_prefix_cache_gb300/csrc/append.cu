@@ -8,11 +8,20 @@
 //
 // One warp takes some consecutive rows (one in a small batch), 16 latent values
 // and one RoPE pair a lane, in 16-byte and 4-byte accesses that are contiguous
-// over the warp.  The next row's loads are in flight while a row is computed,
-// and a request and a block are looked up when they change only (a row with its
-// own five dependent loads took 39 us for 62,731 FP8 rows, four rows a warp with
-// all loads first and 100 registers 35).  HBM-bound: 1152 B read and 1152 (bf16)
-// or 640 B (FP8) written a row.
+// over the warp, with the next row's loads in flight while a row is computed.
+// Rows of one block of one request are a run: the request and the block are
+// looked up between runs, and the loop over a run's rows reads no parameters.
+// HBM-bound in principle: 1152 B read and 1152 (bf16) or 640 B (FP8) written a
+// row.  62,731 FP8 rows (112 MB, 16.6 us at the copy rate) take 20.9 us, 5.4
+// TB/s; what it takes beyond that is issue slots (about 200 instructions a row
+// and warp) and the rows' latency:
+//   a row a warp, its five loads dependent                              39 us
+//   four rows a warp, all loads first (100 registers)                   35
+//   consecutive rows, the next one in flight, look-ups when they change 27
+//   runs (their loop had waited for parameters)                         22
+//   norm weights as floats in shared memory, packed arithmetic          20.9
+// Two rows in flight, or five through shared memory, gained nothing (23.5, 28
+// against 22, 27); 3 and 5 CTAs an SM take 23.1 and 22.2.
 #include "serving.cuh"
 
 namespace mla {
@@ -26,18 +35,19 @@ struct Row {   // latent values 8 l .. 8 l + 7 and 256 + 8 l .., RoPE pair l
   uint32_t kr;
   int pos;
 };
-__device__ __forceinline__ Row load_row(const AppendParams& p, int row, int lane) {
-  const uint16_t* x = p.kv + (int64_t)row * p.row_stride;
+// x: the row's element 8 l
+__device__ __forceinline__ Row load_row(const uint16_t* x, const int32_t* pos, int lane) {
   Row r;
-  r.a = __ldg(reinterpret_cast<const uint4*>(x) + lane);
-  r.b = __ldg(reinterpret_cast<const uint4*>(x) + 32 + lane);
-  r.kr = __ldg(reinterpret_cast<const uint32_t*>(x + kDc) + lane);
-  r.pos = __ldg(p.pos + row);
+  r.a = __ldg(reinterpret_cast<const uint4*>(x));
+  r.b = __ldg(reinterpret_cast<const uint4*>(x + 256));
+  r.kr = __ldg(reinterpret_cast<const uint32_t*>(x + kDc - 6 * lane));
+  r.pos = __ldg(pos);
   return r;
 }
 
 template <bool kFp8>
 __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm) cache_append_kernel(const __grid_constant__ AppendParams p) {
+  constexpr int kRow = kFp8 ? kRowBytesFp8 : kRowBytesBf16;
   const int lane = threadIdx.x & 31;
   const int first = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * p.per_warp;
   const int end = min(first + p.per_warp, p.batch.rows);
@@ -47,89 +57,108 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm) cache_append_kernel
   }
   grid_wait();      // launched dependently: the inputs are there
   grid_trigger();
-  Row next = load_row(p, first, lane);
-  uint4 ga = make_uint4(0, 0, 0, 0), gb = ga;
+  const int64_t stride = p.row_stride;
+  const uint16_t* x = p.kv + first * stride + 8 * lane;    // of the next row to load
+  const int32_t* xpos = p.pos + first;
+  Row next = load_row(x, xpos, lane);
   const bool norm = p.norm_weight != nullptr;
-  if (norm) {
-    ga = __ldg(reinterpret_cast<const uint4*>(p.norm_weight) + lane);
-    gb = __ldg(reinterpret_cast<const uint4*>(p.norm_weight) + 32 + lane);
+  // the lane's 16 norm weights (1 without a norm) as floats, in places that only it uses
+  __shared__ float4 weights[kWarps][4][32];
+  float4(&g)[4][32] = weights[threadIdx.x >> 5];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    uint4 w = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+    if (norm) w = __ldg(reinterpret_cast<const uint4*>(p.norm_weight) + 32 * k + lane);
+    g[2 * k][lane] = make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
+    g[2 * k + 1][lane] = make_float4(bf16_lo(w.z), bf16_hi(w.z), bf16_lo(w.w), bf16_hi(w.w));
   }
   const uint64_t frac = p.rope_frac[lane];
+  // E4M3 codes are of c times the reciprocal of kv_scale: the factor joins the norm's
+  const float scale = kFp8 ? p.inv_scale : 1.f, eps = p.norm_eps;
   int r = -1, past = first, len = 0;        // request, one past its last row, its tokens
-  int lb = -1, id = -1;                     // block of the request, and its id
-  for (int row = first; row < end; ++row) {
-    const Row x = next;
-    if (row + 1 < end) next = load_row(p, row + 1, lane);
+  for (int row = first; row < end;) {
+    // the rows up to `stop` go to one block of one request, or nowhere
     if (row >= past) {
       r = request_of_row(p.batch, row, lane);
-      if (r < 0) {                          // no request's row: before the first one, or behind the last
-        past = row + 1;
-        id = -1;
-        len = 0;
-        lb = 0;
-        continue;
+      past = row + 1;                       // no request's row: before the first one, or behind the last
+      if (r >= 0) {
+        past = request_rows(p.batch, r).y;
+        len = __ldg(p.batch.seq_lens + r);
       }
-      past = request_rows(p.batch, r).y;
-      len = __ldg(p.batch.seq_lens + r);
-      lb = -1;
     }
+    int stop = min(past, end);
     const int tok = len - (past - row);
-    if (tok < 0) continue;                  // a padded request: its length does not hold this row
-    if (tok >> 6 != lb) {
-      lb = tok >> 6;
-      id = lb < p.max_blocks ? __ldg(p.block_table + (int64_t)r * p.max_blocks + lb) : -1;
-      if (id < 0 || id >= p.num_blocks) {
-        id = -1;
-        if (lane == 0 && p.err != nullptr) atomicOr(p.err, kErrBadBlock);
+    uint8_t* dst = nullptr;
+    if (r >= 0 && tok >= 0) {               // (a padded request: its length does not hold this row)
+      stop = min(stop, row + kBlock - (tok & (kBlock - 1)));
+      const int lb = tok >> 6;
+      const int id = lb < p.max_blocks ? __ldg(p.block_table + (int64_t)r * p.max_blocks + lb) : -1;
+      if (id >= 0 && id < p.num_blocks) dst = p.cache + ((int64_t)id * kBlock + (tok & (kBlock - 1))) * kRow;
+      else if (lane == 0 && p.err != nullptr) atomicOr(p.err, kErrBadBlock);
+    } else if (r >= 0) {
+      stop = min(stop, row - tok);
+    }
+    if (dst == nullptr) {                   // left out
+      const int n = stop - row;
+      row = stop;
+      if (row < end) {
+        x += n * stride;
+        xpos += n;
+        next = load_row(x, xpos, lane);
       }
+      continue;
     }
-    if (id < 0) continue;
-    const uint32_t w[8] = {x.a.x, x.a.y, x.a.z, x.a.w, x.b.x, x.b.y, x.b.z, x.b.w};
-    float v[16];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      v[2 * k] = bf16_lo(w[k]);
-      v[2 * k + 1] = bf16_hi(w[k]);
-    }
-    // E4M3 codes are of c times the reciprocal of kv_scale: the factor joins the norm's
-    float f = kFp8 ? p.inv_scale : 1.f;
-    if (norm) {
-      const uint32_t g[8] = {ga.x, ga.y, ga.z, ga.w, gb.x, gb.y, gb.z, gb.w};
-      float ss = 0.f;
-#pragma unroll
-      for (int k = 0; k < 16; ++k) ss = fmaf(v[k], v[k], ss);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      f *= rsqrtf(ss * (1.f / kDc) + p.norm_eps);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        v[2 * k] *= f * bf16_lo(g[k]);
-        v[2 * k + 1] *= f * bf16_hi(g[k]);
+    dst += (kFp8 ? 8 : 16) * lane;
+#pragma unroll 1
+    for (; row < stop; ++row, dst += kRow) {
+      const Row q = next;
+      if (row + 1 < end) {
+        x += stride;
+        ++xpos;
+        next = load_row(x, xpos, lane);
       }
-    } else if (kFp8) {
+      const uint32_t w[8] = {q.a.x, q.a.y, q.a.z, q.a.w, q.b.x, q.b.y, q.b.z, q.b.w};
+      uint64_t v2[8];                       // pairs
 #pragma unroll
-      for (int k = 0; k < 16; ++k) v[k] *= f;
-    }
-    float sn, cs;
-    rope_sincos_sfu(x.pos, frac, &sn, &cs);
-    const float x0 = bf16_lo(x.kr), x1 = bf16_hi(x.kr);
-    const uint32_t k2 = pack_bf16(x0 * cs - x1 * sn, x0 * sn + x1 * cs);
-
-    uint8_t* dst = p.cache + ((int64_t)id * kBlock + (tok & (kBlock - 1))) * (kFp8 ? kRowBytesFp8 : kRowBytesBf16);
-    if constexpr (kFp8) {
-      uint32_t c[4];
+      for (int k = 0; k < 8; ++k) v2[k] = f2pack(bf16_lo(w[k]), bf16_hi(w[k]));
+      float f = scale;
+      if (norm) {
+        uint64_t s2 = 0ull;
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        c[k] = (uint32_t)pack_e4m3x2(v[4 * k], v[4 * k + 1]) | ((uint32_t)pack_e4m3x2(v[4 * k + 2], v[4 * k + 3]) << 16);
-      reinterpret_cast<uint2*>(dst)[lane] = make_uint2(c[0], c[1]);
-      reinterpret_cast<uint2*>(dst)[32 + lane] = make_uint2(c[2], c[3]);
-      reinterpret_cast<uint32_t*>(dst + kDc)[lane] = k2;
-    } else {
-      reinterpret_cast<uint4*>(dst)[lane] = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
-                                                       pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-      reinterpret_cast<uint4*>(dst)[32 + lane] = make_uint4(pack_bf16(v[8], v[9]), pack_bf16(v[10], v[11]),
-                                                            pack_bf16(v[12], v[13]), pack_bf16(v[14], v[15]));
-      reinterpret_cast<uint32_t*>(dst + 2 * kDc)[lane] = k2;
+        for (int k = 0; k < 8; ++k) s2 = ffma2(v2[k], v2[k], s2);
+        float ss, s1;
+        f2unpack(s2, ss, s1);
+        ss += s1;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        f *= rsqrtf(ss * (1.f / kDc) + eps);
+      }
+      float v[16];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {         // without a norm, times 1
+        const float4 gk = g[k][lane];
+        f2unpack(fmul2(v2[2 * k], fmul2(f2pack(gk.x, gk.y), f2pack(f, f))), v[4 * k], v[4 * k + 1]);
+        f2unpack(fmul2(v2[2 * k + 1], fmul2(f2pack(gk.z, gk.w), f2pack(f, f))), v[4 * k + 2], v[4 * k + 3]);
+      }
+      float sn, cs;
+      rope_sincos_sfu(q.pos, frac, &sn, &cs);
+      const float x0 = bf16_lo(q.kr), x1 = bf16_hi(q.kr);
+      const uint32_t k2 = pack_bf16(x0 * cs - x1 * sn, x0 * sn + x1 * cs);
+      if constexpr (kFp8) {
+        uint32_t c[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          c[k] = (uint32_t)pack_e4m3x2(v[4 * k], v[4 * k + 1]) | ((uint32_t)pack_e4m3x2(v[4 * k + 2], v[4 * k + 3]) << 16);
+        *reinterpret_cast<uint2*>(dst) = make_uint2(c[0], c[1]);
+        *reinterpret_cast<uint2*>(dst + 256) = make_uint2(c[2], c[3]);
+        *reinterpret_cast<uint32_t*>(dst + kDc - 4 * lane) = k2;
+      } else {
+        *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
+                                                    pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+        *reinterpret_cast<uint4*>(dst + 512) = make_uint4(pack_bf16(v[8], v[9]), pack_bf16(v[10], v[11]),
+                                                          pack_bf16(v[12], v[13]), pack_bf16(v[14], v[15]));
+        *reinterpret_cast<uint32_t*>(dst + 2 * kDc - 12 * lane) = k2;
+      }
     }
   }
 }
