@@ -1852,14 +1852,15 @@ int mla_cache_append(const void* kv, int64_t kv_row_stride, const int32_t* pos, 
 
 // Workspace of mla_decode: byte offsets, 0 for sizes that it does not take.
 struct DecodeLayout {
-  size_t first, qlat, qscale, lat, lat_lse, part, part_lse, total;
+  size_t first, walks, qlat, qscale, lat, lat_lse, part, part_lse, total;
 };
 static bool decode_layout(int num_reqs, int total_q, int num_heads, DecodeLayout* d) {
   if (num_reqs < 0 || total_q < 0 || num_heads < 1 || num_heads > kMaxHeads) return false;
   const size_t rows = (size_t)total_q * num_heads;
   if (rows > (size_t)INT32_MAX / 2) return false;   // TMA row coordinates
   d->first = 256;
-  d->qlat = up256(d->first + ((size_t)num_reqs + 2) * 4);
+  d->walks = up256(d->first + ((size_t)num_reqs + 2) * 4);
+  d->qlat = up256(d->walks + (size_t)kDecodeClusters * kWalkBytes);
   d->qscale = up256(d->qlat + rows * kDc * 2);
   d->lat = up256(d->qscale + rows * 4);
   d->lat_lse = up256(d->lat + rows * kDc * 4);
@@ -1918,6 +1919,7 @@ int mla_decode(const void* q, const int32_t* q_pos, const void* kv_cache, int kv
   DecodeSpace space;
   space.err = reinterpret_cast<uint32_t*>(ws);
   space.first = reinterpret_cast<int32_t*>(ws + d.first);
+  space.walks = reinterpret_cast<uint32_t*>(ws + d.walks);
   space.qlat = ws + d.qlat;
   space.qscale = reinterpret_cast<float*>(ws + d.qscale);
   space.lat = reinterpret_cast<float*>(ws + d.lat);
@@ -1976,6 +1978,10 @@ int mla_decode(const void* q, const int32_t* q_pos, const void* kv_cache, int kv
   qp.row0 = 0;
   qp.tokens = total_q;
   qp.num_heads = H;
+  qp.batch = batch;
+  qp.first = space.first;
+  qp.walks = space.walks;
+  if ((st = cuda_status(decode_clusters(&qp.clusters))) != MLA_OK) return st;
   if ((st = cuda_status(launch_decode_qabsorb(qp, s))) != MLA_OK) return st;
 
   p.batch = batch;
@@ -1991,7 +1997,7 @@ int mla_decode(const void* q, const int32_t* q_pos, const void* kv_cache, int kv
   cudaEvent_t ev_e = static_cast<cudaEvent_t>(g_ev_end.load());
   const bool timed = ev_b != nullptr && ev_e != nullptr;
   if (timed && (st = cuda_status(cudaEventRecord(ev_b, s))) != MLA_OK) return st;
-  if ((st = cuda_status(launch_decode_attn(p, fp8, s))) != MLA_OK) return st;
+  if ((st = cuda_status(launch_decode_attn(p, fp8, qp.clusters, s))) != MLA_OK) return st;
   if (timed && (st = cuda_status(cudaEventRecord(ev_e, s))) != MLA_OK) return st;
 
   op.batch = batch;

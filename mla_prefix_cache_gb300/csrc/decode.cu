@@ -14,9 +14,8 @@
 // whatever the lengths are: a cluster has one contiguous run of tiles, the last
 // part of one item, whole items, the first part of another.  A piece leaves the
 // fp32 states of its rows, a whole item's in the rows' own place, the others in
-// the cluster's two slots, which decode_out_kernel joins.  The cut is computed by
-// every CTA from the lengths (one pass of its threads over the requests), so no
-// launch waits for a plan.
+// the cluster's two slots, which decode_out_kernel joins.  The cut is computed on
+// the device from the lengths, by a CTA of the query absorption's launch.
 //
 // A cluster is two CTAs, split by operation because O [128 x 512] fp32 fills a
 // CTA's TMEM and Q [128 x 512] half of another's:
@@ -86,8 +85,8 @@ enum : uint32_t {
   kEP = 26,     // the 8 correction warps have read the piece's O
   kNBars = 30
 };
-constexpr uint32_t kShared = kBars + 8 * kNBars;   // Start, then the hand-over word
-constexpr uint32_t kHand = kShared + 64;
+constexpr uint32_t kShared = kBars + 8 * kNBars;   // TMEM address, then the hand-over word
+constexpr uint32_t kHand = kShared + 16;
 constexpr uint32_t kWalks = kHand + 16;            // the roles' walks
 constexpr int kRoles = 6;
 constexpr uint32_t kTxP = kPBytes + kFacBytes;
@@ -114,198 +113,43 @@ __device__ __forceinline__ uint32_t bf16_up(float x) {
   return ((int32_t)u >= 0 ? u + 0xFFFFu : u) >> 16;
 }
 
-constexpr int kBoxes = 4;         // values stages of each half of the columns that a piece's states leave through
 
-// Where a cluster's run of units begins: in request r, whose first unit is `first`.
-struct Start {
-  int begin, end, first, r;
-  RequestWork w;   // of request r
-  uint32_t tmem;
-};
-
-// The units of all requests, and this cluster's run.  Every thread of the CTA;
-// thread t takes requests [t k, (t + 1) k).  CTA 0 of the grid leaves the
-// requests' first units for decode_out_kernel; true if this thread met a
-// sequence longer than its table.  A cu_q that does not ascend could count rows
-// twice and pass 31 bits: such a batch has no work, and every thread returns
-// true.  It may run before the kernel that clears the error word has.
-__device__ bool schedule(const DecodeParams& p, Start* st, int* scratch, int cluster) {
-  const int B = p.batch.rows.num_reqs, k = (B + kThreads - 1) / kThreads;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int r0 = min(B, tid * k), r1 = min(B, r0 + k);
-  RequestWork w;
-  int sum = 0;
-  bool cut = false, mixed = false;   // a sequence longer than its table, a request that ends before it starts
-#pragma unroll 1
-  for (int r = r0; r < r1; ++r) {
-    w = request_work(p.batch, r);
-    sum += w.units() * w.items;
-    cut |= __ldg(p.batch.rows.seq_lens + r) > p.batch.max_blocks * kBlock;
-    if (p.batch.rows.cu_q != nullptr) mixed |= __ldg(p.batch.rows.cu_q + r + 1) < __ldg(p.batch.rows.cu_q + r);
-  }
-  int pre = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, pre, o);
-    if (lane >= o) pre += v;
-  }
-  if (lane == 31) scratch[warp] = pre;
-  if (tid == 0) st->r = B;
-  mixed = __syncthreads_or(mixed);
-  int total = 0;
-#pragma unroll 4
-  for (int i = 0; i < kThreads / 32; ++i) {
-    if (i < warp) pre += scratch[i];
-    total += scratch[i];
-  }
-  pre -= sum;   // units of the requests before r0
-  if (mixed) pre = sum = total = 0;
-  const int n = min(total, (int)gridDim.x / 2);
-  const int begin = cluster < n ? unit_begin(cluster, n, total) : total;
-  if (tid == 0) {
-    st->begin = begin;
-    st->end = cluster < n ? unit_begin(cluster + 1, n, total) : total;
-    if (blockIdx.x == 0) {
-      p.ws.first[B] = total;
-      p.ws.first[B + 1] = n;
-    }
-  }
-  const bool mine = begin >= pre && begin < pre + sum;
-  if (mine || blockIdx.x == 0) {
-    int at = pre;
-    bool found = false;
-#pragma unroll 1
-    for (int r = r0; r < r1; ++r) {
-      if (k > 1) w = request_work(p.batch, r);
-      if (blockIdx.x == 0) p.ws.first[r] = at;
-      const int next = mixed ? at : at + w.units() * w.items;
-      if (mine && !found && begin < next) {
-        found = true;
-        st->r = r;
-        st->first = at;
-        st->w = w;
-      }
-      at = next;
-    }
-  }
-  __syncthreads();
-  return cut || mixed;
-}
-
-// A cluster's run of units, walked alike by every role, as ranges of key tiles
-// with one RoPE offset: tiles j = 0 .. n - 1 of 128 keys from key t0 on, of
-// which [k_lo, k_hi) count.  The ranges of a piece (a run of one item's tiles)
-// follow one another, the first marked `head`, the last `tail`.  A role's walk
-// sits in shared memory, advanced by one of its threads: in local memory, which
-// the few KB of L1 beside 226 KB of shared memory do not hold, the first range
-// alone took 2 us.
-struct Walk {
-  // range
-  int64_t offset;
-  int t0, n, k_lo, k_hi;
-  bool more, head, tail;
-  // its piece
-  int r, row0, slot, rows;   // request, first row of the item, slot of its state (-1: a whole item), the request's rows
-  RequestWork w;             // of request r
-  // where the walk is
-  int at, end, first;        // next unit, one past the run's last, first unit of request r
-  int lo, hi, g, last_key, acc;   // the piece's tiles; next range, end of the keys so far, tiles so far
-  // stages of each half of the columns that the piece's states leave through, if it has 32 live rows (fewer are
-  // written by their threads)
-  __device__ __forceinline__ int boxes() const { return rows - row0 < 32 ? 0 : kBoxes; }
-  __device__ __forceinline__ void start(const Start& s) {
-    w = s.w;
-    at = s.begin;
-    end = s.end;
-    first = s.first;
-    r = s.r;
-    lo = hi = acc = 0;
-  }
-};
+// Stages of each half of the columns that a piece's states leave through, if it has 32 live rows (fewer are written by
+// their threads).
+constexpr int kBoxes = 4;
+__device__ __forceinline__ int boxes_of(const Walk& k) { return k.rows - k.row0 < 32 ? 0 : kBoxes; }
 
 constexpr uint32_t kSmem = kWalks + kRoles * sizeof(Walk);
 static_assert(kWalks % alignof(Walk) == 0 && kSmem <= 232448, "shared memory per CTA");
 
 // One copy of this code serves every role: inlined into each, the kernel's code
 // was 170 KB and its roles waited for instructions (1.5 times the time).
-__device__ __noinline__ bool next_range(const DecodeParams& p, Walk& k) {
-  k.head = false;
-  while (k.acc >= k.hi) {   // the next piece
-    while (true) {
-      if (k.at >= k.end || k.r >= p.batch.rows.num_reqs) return false;
-      const int u = k.w.units();
-      const int past = k.first + u * k.w.items;
-      if (k.at >= past) {   // also a request without units
-        k.first = past;
-        if (++k.r < p.batch.rows.num_reqs) k.w = request_work(p.batch, k.r);
-        continue;
-      }
-      const int item = k.at - k.first < u ? 0 : (k.at - k.first) / u;
-      const int base = k.first + item * u;
-      const int stop = min(base + u, k.end);
-      k.lo = max(0, k.at - base - kItemUnits);
-      k.hi = max(0, stop - base - kItemUnits);
-      k.at = stop;
-      if (k.hi <= k.lo) continue;   // only units of the item's start
-      k.row0 = item * kItemRows;
-      k.slot = (k.lo == 0 && k.hi == k.w.tiles) ? -1 : 2 * (int)(blockIdx.x >> 1) + (k.lo == 0 ? 1 : 0);
-      break;
-    }
-    k.head = true;
-    k.rows = k.w.q_count * p.batch.num_heads;
-    if (k.w.sg.x == k.w.sg.y) {   // no segments: one range
-      k.t0 = 128 * k.lo;
-      k.n = k.hi - k.lo;
-      k.k_lo = 0;
-      k.k_hi = k.w.len;
-      k.offset = 0;
-      k.tail = true;
-      k.acc = k.hi;
-      return true;
-    }
-    k.g = k.w.sg.x;
-    k.last_key = 0;
-    k.acc = 0;
-    // ranges before the piece's first tile
-    while (k.g <= k.w.sg.y) {
-      const KeyRange kr = request_range(p.batch, k.w.sg, k.g, k.last_key, k.w.len);
-      const int t = range_tiles(kr);
-      if (k.acc + t > k.lo) break;
-      k.acc += t;
-      k.last_key = kr.hi;
-      ++k.g;
-    }
-  }
-  while (true) {   // the next range with tiles: the piece's tiles say there is one
-    const KeyRange kr = request_range(p.batch, k.w.sg, k.g, k.last_key, k.w.len);
-    const int t = range_tiles(kr), from = k.acc;
-    k.last_key = kr.hi;
-    k.acc += t;
-    ++k.g;
-    const int lo = max(from, k.lo), hi = min(k.acc, k.hi);
-    if (lo >= hi) continue;
-    k.t0 = (kr.lo & ~(kBlock - 1)) + 128 * (lo - from);
-    k.n = hi - lo;
-    k.k_lo = kr.lo;
-    k.k_hi = kr.hi;
-    k.offset = kr.offset;
-    k.tail = k.acc >= k.hi;
-    return true;
-  }
-}
-
-// The next range of a walk: by the one thread of a role, by a warp, by `count`
-// threads at named barrier `id` (everyone is done with the range before).
-__device__ __forceinline__ bool next_of_warp(const DecodeParams& p, Walk& k, int lane) {
-  __syncwarp();
-  if (lane == 0) k.more = next_range(p, k);
-  __syncwarp();
+__device__ __noinline__ bool next(const DecodeParams& p, Walk& k) { return next_range(p.batch, k); }
+// The next range of a walk (the first one is there already): by the one thread
+// of a role, by a warp, by `count` threads at named barrier `id` (everyone is
+// done with the range before).
+__device__ __forceinline__ bool next_of_one(const DecodeParams& p, Walk& k, bool& first) {
+  if (!first) return next(p, k);
+  first = false;
   return *const_cast<volatile bool*>(&k.more);
 }
-__device__ __forceinline__ bool next_of_group(const DecodeParams& p, Walk& k, bool leader, uint32_t id, uint32_t count) {
-  named_bar_sync(id, count);
-  if (leader) k.more = next_range(p, k);
-  named_bar_sync(id, count);
+__device__ __forceinline__ bool next_of_warp(const DecodeParams& p, Walk& k, bool& first, int lane) {
+  if (!first) {
+    __syncwarp();
+    if (lane == 0) k.more = next(p, k);
+    __syncwarp();
+  }
+  first = false;
+  return *const_cast<volatile bool*>(&k.more);
+}
+__device__ __forceinline__ bool next_of_group(const DecodeParams& p, Walk& k, bool& first, bool leader, uint32_t id,
+                                              uint32_t count) {
+  if (!first) {
+    named_bar_sync(id, count);
+    if (leader) k.more = next(p, k);
+    named_bar_sync(id, count);
+  }
+  first = false;
   return *const_cast<volatile bool*>(&k.more);
 }
 
@@ -385,13 +229,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   const int cluster = blockIdx.x >> 1;
   const int H = p.batch.num_heads;
   auto bar = [&](uint32_t i) { return sb + kBars + 8u * i; };
-  Start* start = reinterpret_cast<Start*>(smem + kShared);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kShared);
   constexpr int kBlocks = kFp8 ? 5 : 9, kLatBlocks = kFp8 ? 4 : 8;   // 128-byte blocks of a row [c | k_rope], of c
   constexpr int kQBoxes = 8;                                         // and of an item's Q
   constexpr int kORows = kFp8 ? 64 : 32, kOPerTile = 128 / kORows;   // key rows of a values stage
 
-  // for the reads that come before the wait for the kernels before this one: no stale L1
-  if (warp == 3) asm volatile("fence.acq_rel.gpu;" ::: "memory");
   if (tid == 0) {
     prefetch_tensormap(scores ? &p.tm_s : &p.tm_o);
     prefetch_tensormap(scores ? &p.tm_q : &p.tm_part);
@@ -409,23 +251,21 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     fence_mbar_init();
   }
   if (warp == 2) {
-    tmem_alloc(smem_u32(&start->tmem), 512);
+    tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
-  tc_fence_before();
-  __syncthreads();
-  const bool cut = schedule(p, start, reinterpret_cast<int*>(smem), cluster);
-  cluster_sync_all();   // both CTAs' barriers exist before either is signalled
-  tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&start->tmem);
+  grid_wait();      // the plan, qlat and the inputs are there
+  grid_trigger();   // decode_out_kernel may take SMs as they fall free
   // scores: loads 0, 1, MMA, copies, Q, softmax; values: loads 0, 1, MMA, P landed, -, rescale
   const int role = warp == 0 ? 0 : warp == (scores ? 3 : 2) ? 1 : warp == 1 ? 2 : warp < 4 ? 3 : warp >= 12 ? 4 : 5;
   Walk& k = reinterpret_cast<Walk*>(smem + kWalks)[role];
-  if (lane == 0 && (warp <= 4 || warp == 12)) k.start(*start);
-  if (cut && blockIdx.x == 0) {
-    grid_wait();
-    atomicOr(p.ws.err, kErrBadBlock);
-  }
+  bool first = true;
+  if (lane < kWalkWords && (warp <= 4 || warp == 12))
+    reinterpret_cast<uint32_t*>(&k)[lane] = __ldcg(p.ws.walks + kWalkBytes / 4 * cluster + lane);
+  tc_fence_before();
+  cluster_sync_all();   // both CTAs' barriers exist before either is signalled
+  tc_fence_after();
+  const uint32_t tmem = *const_cast<volatile uint32_t*>(tmem_slot);
 
   if (scores) {
     if ((warp == 0 || warp == 3) && lane == 0) {
@@ -441,9 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         mbar_arrive_expect_tx(bar(kSF + s), kBlk);
         return true;
       };
-      while (ok && next_range(p, k)) {
-        grid_wait();      // qlat is there, and the error word cleared
-        grid_trigger();   // decode_out_kernel may take SMs as they fall free
+      while (ok && next_of_one(p, k, first)) {
         const int qrow = k.w.q_begin * H + k.row0;
         for (int i = 0; k.head && i < kQBoxes; ++i, ++u) {
           if ((u & 1) != mine) continue;
@@ -474,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       const uint64_t sd0 = sdesc_sw128(sb + kSRing, 16, 1024);
       int g = 0, s = 0, e = 0;
       uint32_t ph = 0;
-      while (ok && next_of_warp(p, k, lane)) {
+      while (ok && next_of_warp(p, k, first, lane)) {
         if (k.head) {
           s += kQBoxes;   // the Q stages
           if (s >= kSStages) { s -= kSStages; ph ^= 1u; }
@@ -507,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       const uint32_t o_p = mapa_shared(sb + kOP, 1u), o_fac = mapa_shared(sb + kFac, 1u), o_pf = mapa_shared(bar(kPF), 1u);
       bool ok = true;
       int g = 0;
-      while (ok && next_range(p, k)) {
+      while (ok && next_of_one(p, k, first)) {
         for (int j = 0; j < k.n && ok; ++j, ++g) {
           const int b = g & 1;
           // P tile b of the values CTA is free once the PV of tile g - 2 is done
@@ -525,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
       bool ok = true;
       int e = 0, u = 0;
-      while (next_of_group(p, k, r == 0, 7, 128)) {
+      while (next_of_group(p, k, first, r == 0, 7, 128)) {
         // the MMAs that read the Q before this are done
         if (ok && e > 0) ok = await_warp(p, bar(kQE), (e - 1) & 1);
         ++e;
@@ -571,11 +409,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       bool ok = true;
       int g = 0;
       float m_used = -INFINITY, l = 0.f, lsum = 0.f;
-      while (next_of_group(p, k, tid == 128, 5, 256)) {
+      while (next_of_group(p, k, first, tid == 128, 5, 256)) {
         const int prow = k.row0 + r;
         const bool live = prow < k.rows;
         const int64_t orow = (int64_t)k.w.q_begin * H + prow;
-        if (kFp8) grid_wait();   // for the queries' scales
         const float qs = kFp8 && live ? p.ws.qscale[orow] * p.kv_scale : 1.f, sl2 = p.scale_log2 * qs;
         {
           // q_rope turned by pos - offset, as a K-major swizzled block: chunks 4 half .. of the row.  This warp has
@@ -736,10 +573,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       const int nh = warp >> 1;
       bool ok = true;
       int u = nh;
-      while (ok && next_range(p, k)) {
-        grid_wait();   // the error word is cleared
-        grid_trigger();
-        const int stages = kOPerTile * k.n, boxes = k.tail ? k.boxes() : 0;
+      while (ok && next_of_one(p, k, first)) {
+        const int stages = kOPerTile * k.n, boxes = k.tail ? boxes_of(k) : 0;
         for (int i = 0; i < stages + boxes; ++i, u += 2) {
           const int s = u % kOStages;
           const int row = i < stages ? cache_row(p, k.r, k.t0 + kORows * i, k.k_hi) : 0;
@@ -769,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       if (lane == 0)
         for (int b = 0; b < 2; ++b) mbar_arrive_expect_tx(bar(kPF + b), kTxP);
       bool head = true;
-      while (ok && next_of_warp(p, k, lane)) {
+      while (ok && next_of_warp(p, k, first, lane)) {
         if (k.head) head = true;
 #pragma unroll 1
         for (int j = 0; j < k.n && ok; ++j, ++g) {
@@ -833,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         }
         if (k.tail) {
           ++done;
-          advance(2 * k.boxes());
+          advance(2 * boxes_of(k));
         }
       }
       if (!ok && lane == 0) {
@@ -847,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       const uint32_t stf = mapa_shared(bar(kSTF), 0u);
       int g = 0;
       bool ok = true;
-      while (ok && next_range(p, k))
+      while (ok && next_of_one(p, k, first))
         for (int j = 0; j < k.n && ok; ++j, ++g) {
           ok = await(p, bar(kPF + (g & 1)), (g >> 1) & 1);
           if (ok) mbar_arrive_cluster_relaxed(stf + 8u * (g & 1));   // relaxed: a landed copy has read its source
@@ -859,7 +694,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       const volatile int* hand = reinterpret_cast<const volatile int*>(smem + kHand);
       bool ok = true;
       int g = 0, ev = 0, u = half;   // tiles, hand-overs, this half's next stage
-      while (next_of_group(p, k, tid == 128, 5, 256)) {
+      while (next_of_group(p, k, first, tid == 128, 5, 256)) {
         g += k.n;
         u += 2 * kOPerTile * k.n;
         if (!k.tail) continue;   // a piece's states leave at its end
@@ -901,7 +736,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         const int rows = k.rows - k.row0;      // live rows of the item
         const bool whole = k.slot < 0;
         const int row0 = whole ? k.w.q_begin * H + k.row0 : k.slot * kItemRows;   // first row of the states
-        const int boxes = k.boxes();
+        const int boxes = boxes_of(k);
         // A warp of 32 live rows stages 32 columns of them in its quarter of a box and stores them by TMA, four
         // boxes in turn, at its own pace; a warp with fewer writes them by its threads.  256 KB in 4.6 us: the SM's
         // stores to L2 pace it, about 30 B a cycle (contiguous 4 KB copies, loads of the next columns started
@@ -954,7 +789,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       if (lane == 0) bulk_wait0();   // every store complete before the CTA's shared memory goes
     }
   }
-  grid_wait();   // also the CTAs without work
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();   // nothing of the other CTA is under way into this one
@@ -966,7 +800,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 
 }  // namespace
 
-cudaError_t launch_decode_attn(const DecodeParams& p, bool fp8, cudaStream_t s) {
+cudaError_t decode_clusters(int* out) {
   static std::atomic<int> resident_on[64];   // per device, 0: not configured yet
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -995,6 +829,11 @@ cudaError_t launch_decode_attn(const DecodeParams& p, bool fp8, cudaStream_t s) 
     clusters = resident < 1 ? 1 : resident < kDecodeClusters ? resident : kDecodeClusters;
     resident_on[dev].store(clusters);
   }
+  *out = clusters;
+  return cudaSuccess;
+}
+
+cudaError_t launch_decode_attn(const DecodeParams& p, bool fp8, int clusters, cudaStream_t s) {
   return launch_dependent(fp8 ? decode_attn_kernel<true> : decode_attn_kernel<false>, dim3(2 * clusters), kThreads, kSmem,
                           p, s);
 }

@@ -47,6 +47,99 @@ struct QA {
 };
 constexpr uint32_t kIdescQA = idesc_bf16(128, 256, false, false);
 
+// Decode: the work units of all requests, cut evenly over the attention's
+// clusters, and each cluster's walk at its first range.  One CTA; thread t takes
+// requests [t k, (t + 1) k).  It runs beside the projections of the other CTAs:
+// in the attention kernel itself, before its first load, it took 3 us, and 8 to
+// 12 with 16 documents.
+struct PlanSpace {
+  int pre[128];                  // units before each thread's requests
+  int warp[4];
+  RequestWork work[128];         // of a thread's last request
+  Walk walk[kDecodeClusters];
+};
+__device__ void plan_decode(const DecodeQParams& p, PlanSpace& s) {
+  const DecodeBatch& b = p.batch;
+  const int B = b.rows.num_reqs, k = (B + 127) / 128;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int r0 = min(B, tid * k), r1 = min(B, r0 + k);
+  RequestWork w;
+  int sum = 0;
+  bool cut = false, mixed = false;   // a sequence longer than its table, a request that ends before it starts
+#pragma unroll 1
+  for (int r = r0; r < r1; ++r) {
+    w = request_work(b, r);
+    sum += w.units() * w.items;
+    cut |= __ldg(b.rows.seq_lens + r) > b.max_blocks * kBlock;
+    if (b.rows.cu_q != nullptr) mixed |= __ldg(b.rows.cu_q + r + 1) < __ldg(b.rows.cu_q + r);
+    s.work[tid] = w;
+  }
+  int pre = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, pre, o);
+    if (lane >= o) pre += v;
+  }
+  if (lane == 31) s.warp[warp] = pre;
+  // a cu_q that does not ascend could count rows twice and pass 31 bits: such a batch has no work
+  mixed = __syncthreads_or(mixed);
+  cut = __syncthreads_or(cut) || mixed;
+  int total = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (i < warp) pre += s.warp[i];
+    total += s.warp[i];
+  }
+  pre -= sum;
+  if (mixed) pre = total = 0;
+  s.pre[tid] = pre;
+  const int n = min(total, p.clusters);
+  if (tid == 0) {
+    *p.err = cut ? kErrBadBlock : 0u;
+    p.first[B] = total;
+    p.first[B + 1] = n;
+  }
+  __syncthreads();
+  for (int c = tid; c < p.clusters; c += 128) {
+    Walk& v = s.walk[c];
+    v.start(c, 0, 0, B, 0, s.work[0]);
+    v.more = false;
+    if (c < n) {
+      const int begin = unit_begin(c, n, total);
+      int t = 0;   // the last thread whose requests start at or before this unit
+#pragma unroll
+      for (int step = 64; step > 0; step >>= 1)
+        if (s.pre[t + step] <= begin) t += step;
+      int r = t * k, at = s.pre[t];
+      RequestWork u = s.work[t];
+      if (k > 1) {
+#pragma unroll 1
+        for (; r < B; ++r) {
+          u = request_work(b, r);
+          const int past = at + u.units() * u.items;
+          if (begin < past) break;
+          at = past;
+        }
+      }
+      v.start(c, begin, unit_begin(c + 1, n, total), r, at, u);
+      v.more = next_range(b, v);
+    }
+  }
+  // the requests' first units, for the join
+  int at = pre;
+#pragma unroll 1
+  for (int r = r0; r < r1; ++r) {
+    p.first[r] = at;
+    if (k > 1) w = request_work(b, r);
+    at += mixed ? 0 : w.units() * w.items;
+  }
+  __syncthreads();
+  for (int i = tid; i < p.clusters * kWalkWords; i += 128) {
+    const int c = i / kWalkWords, j = i - c * kWalkWords;
+    p.walks[c * (kWalkBytes / 4) + j] = reinterpret_cast<const uint32_t*>(&s.walk[c])[j];
+  }
+}
+
 template <bool kF8, class Params>
 __global__ void __launch_bounds__(128, 1) qabsorb_kernel(const __grid_constant__ Params p) {
   using L = QA<kF8>;
@@ -57,13 +150,16 @@ __global__ void __launch_bounds__(128, 1) qabsorb_kernel(const __grid_constant__
   const uint32_t bar_full = sbase + L::kBars, bar_done = bar_full + 8;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sgen + L::kBars + 16);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h = blockIdx.z;
+  const int h = (int)blockIdx.z - (kDecode ? 1 : 0);
   const int c0 = blockIdx.y * L::kCols;
   const int t0 = p.row0 + blockIdx.x * 128;   // first token of the tile (TMA coordinates)
   if constexpr (kDecode) {                    // launched dependently
     grid_wait();      // the inputs are there
-    grid_trigger();   // the attention kernel may start its own set-up
-    if (threadIdx.x == 0 && (blockIdx.x | blockIdx.y | blockIdx.z) == 0) *p.err = 0u;
+    grid_trigger();   // the attention kernel may take SMs as they fall free
+    if (h < 0) {
+      if ((blockIdx.x | blockIdx.y) == 0) plan_decode(p, *reinterpret_cast<PlanSpace*>(sgen));
+      return;
+    }
   }
 
   if (threadIdx.x == 0) {
@@ -364,7 +460,7 @@ cudaError_t launch_decode_qabsorb(const DecodeQParams& p, cudaStream_t s) {
   cudaError_t e = configure_headproj();
   if (e != cudaSuccess) return e;
   const bool f8 = p.qscale != nullptr;
-  const dim3 grid((p.tokens + 127) / 128, f8 ? 1 : kDc / 256, p.num_heads);
+  const dim3 grid((p.tokens + 127) / 128, f8 ? 1 : kDc / 256, p.num_heads + 1);   // z = 0: the plan
   return f8 ? launch_dependent(qabsorb_kernel<true, DecodeQParams>, grid, 128, QA<true>::kSmem, p, s)
             : launch_dependent(qabsorb_kernel<false, DecodeQParams>, grid, 128, QA<false>::kSmem, p, s);
 }

@@ -14,8 +14,7 @@ namespace mla {
 // waits: so what a dependent kernel reads before its own wait was there before
 // the kernel that it depends on, and one wait covers all earlier kernels.  Nothing
 // says that an SM's L1, which may hold what an earlier call found at the same
-// address, is cleared before the wait: those reads go to L2 (kL2), or come after
-// a fence of the CTA.
+// address, is cleared before the wait: reads before it go to L2 (kL2).
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
@@ -146,6 +145,107 @@ __device__ __forceinline__ int cluster_of(int x, int n, int total) { return (int
 // with those after it.
 __device__ __forceinline__ int piece_slot(int c, int x, int n, int total) {
   return 2 * c + (unit_begin(c, n, total) <= x ? 1 : 0);
+}
+
+// A cluster's run of units, walked alike by every role, as ranges of key tiles
+// with one RoPE offset: tiles j = 0 .. n - 1 of 128 keys from key t0 on, of
+// which [k_lo, k_hi) count.  The ranges of a piece (a run of one item's tiles)
+// follow one another, the first marked `head`, the last `tail`.  The query
+// absorption's launch leaves each cluster's walk at its first range; a role's
+// copy sits in shared memory, advanced by one of its threads.
+struct Walk {
+  // range
+  int64_t offset;
+  int t0, n, k_lo, k_hi;
+  bool more, head, tail;
+  // its piece
+  int r, row0, slot, rows;   // request, first row of the item, slot of its state (-1: a whole item), the request's rows
+  RequestWork w;             // of request r
+  // where the walk is
+  int cluster, at, end, first;        // next unit, one past the run's last, first unit of request r
+  int lo, hi, g, last_key, acc;   // the piece's tiles; next range, end of the keys so far, tiles so far
+  // run [begin, stop) of units, which begins in request q with its first unit f and work u
+  __device__ __forceinline__ void start(int c, int begin, int stop, int q, int f, const RequestWork& u) {
+    cluster = c;
+    at = begin;
+    end = stop;
+    r = q;
+    first = f;
+    w = u;
+    lo = hi = acc = 0;
+  }
+};
+constexpr int kWalkWords = sizeof(Walk) / 4;
+static_assert(sizeof(Walk) % 8 == 0 && sizeof(Walk) <= kWalkBytes, "a warp copies a walk in one step");
+
+// Advances a walk to its next range; false at its end.
+__device__ __forceinline__ bool next_range(const DecodeBatch& b, Walk& k) {
+  k.head = false;
+  while (k.acc >= k.hi) {   // the next piece
+    while (true) {
+      if (k.at >= k.end || k.r >= b.rows.num_reqs) return false;
+      const int u = k.w.units();
+      const int past = k.first + u * k.w.items;
+      if (k.at >= past) {   // also a request without units
+        k.first = past;
+        if (++k.r < b.rows.num_reqs) k.w = request_work(b, k.r);
+        continue;
+      }
+      const int item = k.at - k.first < u ? 0 : (k.at - k.first) / u;
+      const int base = k.first + item * u;
+      const int stop = min(base + u, k.end);
+      k.lo = max(0, k.at - base - kItemUnits);
+      k.hi = max(0, stop - base - kItemUnits);
+      k.at = stop;
+      if (k.hi <= k.lo) continue;   // only units of the item's start
+      k.row0 = item * kItemRows;
+      k.slot = (k.lo == 0 && k.hi == k.w.tiles) ? -1 : 2 * k.cluster + (k.lo == 0 ? 1 : 0);
+      break;
+    }
+    k.head = true;
+    k.rows = k.w.q_count * b.num_heads;
+    if (k.w.sg.x == k.w.sg.y) {   // no segments: one range
+      k.t0 = 128 * k.lo;
+      k.n = k.hi - k.lo;
+      k.k_lo = 0;
+      k.k_hi = k.w.len;
+      k.offset = 0;
+      k.tail = true;
+      k.acc = k.hi;
+      return true;
+    }
+    // ranges before the piece's first tile
+    int g = k.w.sg.x, last = 0, acc = 0;
+    const int len = k.w.len, lo = k.lo;
+    const int2 sg = k.w.sg;
+#pragma unroll 1
+    for (; g <= sg.y; ++g) {
+      const KeyRange kr = request_range(b, sg, g, last, len);
+      const int t = range_tiles(kr);
+      if (acc + t > lo) break;
+      acc += t;
+      last = kr.hi;
+    }
+    k.g = g;
+    k.last_key = last;
+    k.acc = acc;
+  }
+  while (true) {   // the next range with tiles: the piece's tiles say there is one
+    const KeyRange kr = request_range(b, k.w.sg, k.g, k.last_key, k.w.len);
+    const int t = range_tiles(kr), from = k.acc;
+    k.last_key = kr.hi;
+    k.acc += t;
+    ++k.g;
+    const int lo = max(from, k.lo), hi = min(k.acc, k.hi);
+    if (lo >= hi) continue;
+    k.t0 = (kr.lo & ~(kBlock - 1)) + 128 * (lo - from);
+    k.n = hi - lo;
+    k.k_lo = kr.lo;
+    k.k_hi = kr.hi;
+    k.offset = kr.offset;
+    k.tail = k.acc >= k.hi;
+    return true;
+  }
 }
 
 }  // namespace mla

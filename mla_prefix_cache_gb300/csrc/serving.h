@@ -42,6 +42,7 @@ cudaError_t launch_cache_append(AppendParams p, bool fp8, cudaStream_t s);
 constexpr int kDecodeClusters = 76;
 constexpr int kDecodeSlots = 2 * kDecodeClusters;
 constexpr int kItemRows = 128;   // (token, head) rows of a work item
+constexpr int kWalkBytes = 128;  // a walk's share of the workspace
 
 // What both kernels know of the batch's work.
 struct DecodeBatch {
@@ -53,19 +54,11 @@ struct DecodeBatch {
   int num_heads;
 };
 
-// Query absorption for decode (headproj.cu): as QAbsorbParams, but the E4M3 form
-// has also the codes of what the first ones leave, e4m3(qlat / s - qlat8) (the two
-// together hold qlat to about 2^-8 of itself), and the launch, a dependent one,
-// sets the error word to 0.
-struct DecodeQParams : QAbsorbParams {
-  CUtensorMap tm_out2;     // the second codes, as tm_out
-};
-cudaError_t launch_decode_qabsorb(const DecodeQParams& p, cudaStream_t s);
-
 // Latent attention (decode.cu).  Workspace arrays:
 struct DecodeSpace {
   uint32_t* err;
   int32_t* first;        // [num_reqs + 2]: the requests' first work units, all units, clusters in use
+  uint32_t* walks;       // [kDecodeClusters][kWalkBytes]: each cluster's walk over its work, at its first range
   uint8_t* qlat;         // bf16 [rows * H][512], or E4M3 [2][rows * H][512]
   float* qscale;         // [rows * H]: the E4M3 rows' scales
   float* lat;            // [rows * H][512]: states of rows whose keys one cluster had
@@ -73,6 +66,21 @@ struct DecodeSpace {
   float* part;           // [kDecodeSlots][128][512]: states of shared rows
   float* part_lse;       // [kDecodeSlots][128]
 };
+
+// Query absorption and plan (headproj.cu).  As QAbsorbParams, but the E4M3 form
+// has also the codes of what the first ones leave, e4m3(qlat / s - qlat8) (the two
+// together hold qlat to about 2^-8 of itself), and the launch, a dependent one,
+// sets the error word and leaves the attention's plan: `first` and `walks`.
+struct DecodeQParams : QAbsorbParams {
+  CUtensorMap tm_out2;     // the second codes, as tm_out
+  DecodeBatch batch;
+  int clusters;            // of the attention's grid
+  int32_t* first;
+  uint32_t* walks;
+};
+cudaError_t launch_decode_qabsorb(const DecodeQParams& p, cudaStream_t s);
+// The attention's clusters on the current device: as many as are resident at once.
+cudaError_t decode_clusters(int* clusters);
 
 struct DecodeParams {
   CUtensorMap tm_q;      // qlat as [rows * H][512] bf16, or [2 * rows * H][512] bytes, box 128 B x 128
@@ -90,7 +98,7 @@ struct DecodeParams {
   float scale_log2;
   uint64_t rope_frac[kDr / 2];
 };
-cudaError_t launch_decode_attn(const DecodeParams& p, bool fp8, cudaStream_t s);
+cudaError_t launch_decode_attn(const DecodeParams& p, bool fp8, int clusters, cudaStream_t s);
 
 // Joining of the pieces' states and the output projection (decode_out.cu):
 // out[t][h] = out_scale sum_pieces w o W_UV,h, lse[t][h].
