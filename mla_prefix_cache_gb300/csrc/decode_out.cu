@@ -5,10 +5,12 @@
 // A CTA takes some tokens of one head: up to 64, fewer where the grid would not
 // fill the GPU.  Its 32 warps join the fp32 states of their rows (few rows:
 // several warps a row, each some of the pieces) into one K-major swizzled
-// operand of 512 columns, each value as its bf16 (rows 0 .. 63) and the bf16 of
-// what that leaves (rows 64 .. 127), so that one chain of M = 128, N = 128 MMAs
-// multiplies o to 2^-16; W_UV,h comes by TMA in four chunks of 128 rows, two
-// buffers deep, and the two halves of the product are added at the end.
+// operand of 512 columns, each value as its bf16 and, in other rows, the bf16 of
+// what that leaves, so that one chain of M = 128, N = 128 MMAs multiplies o to
+// 2^-16; the two products are added at the end.  W_UV,h comes by TMA in chunks
+// of 128 rows, two buffers deep; where there are 16 tokens at most, their rows
+// take a quarter of the space and all four chunks are there before the states
+// (the rows of the MMA that no token has read what lies behind).
 // Latency-bound: a row is two dependent loads from L2 (weights, states), so the
 // rows are spread over many warps (8 warps took 30 us for 64 tokens of 128
 // heads).
@@ -21,16 +23,8 @@ namespace {
 
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
 constexpr uint32_t kBlk = 16384;                   // [128 rows x 128 B] swizzled block
-constexpr uint32_t kA = 0;                         // 8 blocks of 64 columns
-constexpr uint32_t kB = 8 * kBlk;                  // 2 buffers of [128 c x 128 j] in two blocks
-constexpr uint32_t kRows = kB + 4 * kBlk;
-constexpr uint32_t kBegin = kRows + 128 * 20;      // first unit of each cluster
-constexpr uint32_t kBars = (kBegin + 4 * (kDecodeClusters + 1) + 15) & ~15u;   // B landed x 2, MMAs done x 2, TMEM address
-constexpr uint32_t kSmem = kBars + 48;
-static_assert(kSmem <= 232448, "more than 227 KB of shared memory per CTA");
-constexpr uint32_t kIdesc = idesc_bf16(128, 128, false, true);
 constexpr int kMaxPieces = kDecodeClusters;        // of one item
-constexpr int kMaxShare = 8;                       // warps that share a row
+constexpr int kSmallRows = 16;
 
 struct RowOf {
   int x;           // unit of the item's first tile
@@ -41,14 +35,21 @@ struct RowOf {
 };
 static_assert(sizeof(RowOf) == 20, "row table");
 
-// Partial sums of warps that share rows (at most 4 rows then): 2 KB each in the
-// operand's rows 8 .. 63 and 72 .. 127, which nothing else uses.
-__device__ __forceinline__ uint32_t share_at(int warp) {
-  const int s = warp % 6;
-  return kA + (uint32_t)(warp / 6) * kBlk + (s < 3 ? 1024 : 9216 - 3 * 2048) + (uint32_t)s * 2048;
-}
-static_assert((kWarps + 5) / 6 <= 8, "the warps' partial sums fit beside the rows");
-
+template <bool kSmall>
+struct Lay {
+  static constexpr int kRest = kSmall ? kSmallRows : 64;           // row of a state's rest: this many below
+  static constexpr uint32_t kABlk = 2 * kRest * 128;               // 64 columns of the rows that tokens have
+  static constexpr int kChunks = kSmall ? 4 : 2;                   // buffers of [128 c x 128 j] in two blocks
+  static constexpr uint32_t kA = 0;                                // 8 blocks of 64 columns
+  static constexpr uint32_t kB = 8 * kABlk;
+  static constexpr uint32_t kShare = kB + kChunks * 2 * kBlk;      // partial sums of warps that share rows, 2 KB each
+  static constexpr uint32_t kRows = kShare + (kSmall ? kWarps * 2048 : 0);
+  static constexpr uint32_t kBegin = kRows + 64 * 20;              // first unit of each cluster
+  static constexpr uint32_t kBars = (kBegin + 4 * (kDecodeClusters + 1) + 15) & ~15u;   // B landed, MMAs done x 2, TMEM address
+  static constexpr uint32_t kSmem = kBars + 8 * (kChunks + 2) + 16;
+};
+static_assert(Lay<false>::kSmem <= 232448 && Lay<true>::kSmem <= 232448, "more than 227 KB of shared memory per CTA");
+constexpr uint32_t kIdesc = idesc_bf16(128, 128, false, true);
 __device__ __forceinline__ bool wait(uint32_t* err, uint32_t bar, uint32_t parity) {
   if (mbar_wait(bar, parity)) return true;
   atomicOr(err, kErrTimeout);
@@ -68,29 +69,32 @@ __device__ __forceinline__ int find_request(const BatchRows& b, int x) {
 }
 
 // 4 columns 4 lane + 128 k of row i into the operand: their bf16, and that of the rest.
+template <class L>
 __device__ __forceinline__ void put4(uint32_t a, int i, int lane, int k, float4 v) {
   const int c = 4 * lane + 128 * k;
-  const uint32_t addr = a + (uint32_t)(c >> 6) * kBlk + sw128_off((uint32_t)i, (uint32_t)((c & 63) >> 3)) + (c & 4) * 2;
+  const uint32_t addr = a + (uint32_t)(c >> 6) * L::kABlk + sw128_off((uint32_t)i, (uint32_t)((c & 63) >> 3)) + (c & 4) * 2;
   const uint32_t h0 = pack_bf16(v.x, v.y), h1 = pack_bf16(v.z, v.w);
   asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(h0), "r"(h1) : "memory");
-  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr + 64 * 128), "r"(pack_bf16(v.x - bf16_lo(h0), v.y - bf16_hi(h0))),
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr + L::kRest * 128), "r"(pack_bf16(v.x - bf16_lo(h0), v.y - bf16_hi(h0))),
                "r"(pack_bf16(v.z - bf16_lo(h1), v.w - bf16_hi(h1)))
                : "memory");
 }
 
+template <bool kSmall>
 __global__ void __launch_bounds__(kThreads, 1) decode_out_kernel(const __grid_constant__ DecodeOutParams p) {
+  using L = Lay<kSmall>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sb = smem_u32(smem);
-  const uint32_t bars = sb + kBars;
-  RowOf* rows = reinterpret_cast<RowOf*>(smem + kRows);
-  int* begin = reinterpret_cast<int*>(smem + kBegin);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kBars + 32);
+  const uint32_t bars = sb + L::kBars, done = bars + 8 * L::kChunks;
+  RowOf* rows = reinterpret_cast<RowOf*>(smem + L::kRows);
+  int* begin = reinterpret_cast<int*>(smem + L::kBegin);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kBars + 8 * (L::kChunks + 2));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int H = p.batch.num_heads, h = blockIdx.z, r0 = blockIdx.x * p.tile;
   const int R = min(p.tile, p.batch.rows.rows - r0);
 
   auto load_w = [&](int ch) {
-    const uint32_t b = ch & 1, dst = sb + kB + b * 2 * kBlk;
+    const uint32_t b = ch % L::kChunks, dst = sb + L::kB + b * 2 * kBlk;
     mbar_arrive_expect_tx(bars + 8 * b, 2 * kBlk);
     tma_load_2d(dst, &p.tm_w, 128 * H + 128 * h, 128 * ch, bars + 8 * b);
     tma_load_2d(dst + kBlk, &p.tm_w, 128 * H + 128 * h + 64, 128 * ch, bars + 8 * b);
@@ -98,10 +102,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_out_kernel(const __grid_co
   if (tid == 0) {
     prefetch_tensormap(&p.tm_w);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) mbar_init(bars + 8 * i, 1);
+    for (int i = 0; i < L::kChunks + 2; ++i) mbar_init(bars + 8 * i, 1);
     fence_mbar_init();
-    load_w(0);
-    load_w(1);
+    for (int ch = 0; ch < L::kChunks; ++ch) load_w(ch);
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_slot), 128);
@@ -148,7 +151,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_out_kernel(const __grid_co
   const uint32_t tmem = *tmem_slot;
 
   // ---------------------------------------------------------------- the rows' states
-  const int G = R <= 4 ? kMaxShare : 1;   // warps a row
+  int G = 1;        // warps a row
+  if (kSmall)
+    while (2 * G * R <= kWarps) G *= 2;
   const int part = warp % G;
   for (int i = warp / G; i < R; i += kWarps / G) {
     const RowOf o = rows[i];
@@ -159,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_out_kernel(const __grid_co
 #pragma unroll
         for (int k = 0; k < 4; ++k) v[k] = src[32 * k];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) put4(sb + kA, i, lane, k, v[k]);
+        for (int k = 0; k < 4; ++k) put4<L>(sb + L::kA, i, lane, k, v[k]);
       }
       continue;
     }
@@ -191,47 +196,44 @@ __global__ void __launch_bounds__(kThreads, 1) decode_out_kernel(const __grid_co
       for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
       const float inv = sum != 0.f ? 1.f / sum : 0.f;
       if (part == 0 && lane == 0) rows[i].lse = sum != 0.f ? m + __logf(sum) : -INFINITY;
-#pragma unroll
-      for (int k = 0; k < kPerLane; ++k) {
-        if (32 * k >= o.n) break;
-        const int last = min(32, o.n - 32 * k);
+      static_assert(kPerLane == 3, "the pieces of three lane groups");
 #pragma unroll 2
-        for (int l = part; l < last; l += G) {
-          const float wi = __shfl_sync(0xffffffffu, w[k], l) * inv;
-          const int row = __shfl_sync(0xffffffffu, at[k], l);
-          const float4* src = reinterpret_cast<const float4*>(p.ws.part + (int64_t)row * kDc) + lane;
-          float4 v[4];
+      for (int l = part; l < o.n; l += G) {
+        const float wi = __shfl_sync(0xffffffffu, l < 32 ? w[0] : l < 64 ? w[1] : w[2], l & 31) * inv;
+        const int row = __shfl_sync(0xffffffffu, l < 32 ? at[0] : l < 64 ? at[1] : at[2], l & 31);
+        const float4* src = reinterpret_cast<const float4*>(p.ws.part + (int64_t)row * kDc) + lane;
+        float4 v[4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) v[q] = src[32 * q];
+        for (int q = 0; q < 4; ++q) v[q] = src[32 * q];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            acc[q].x = fmaf(wi, v[q].x, acc[q].x);
-            acc[q].y = fmaf(wi, v[q].y, acc[q].y);
-            acc[q].z = fmaf(wi, v[q].z, acc[q].z);
-            acc[q].w = fmaf(wi, v[q].w, acc[q].w);
-          }
+        for (int q = 0; q < 4; ++q) {
+          acc[q].x = fmaf(wi, v[q].x, acc[q].x);
+          acc[q].y = fmaf(wi, v[q].y, acc[q].y);
+          acc[q].z = fmaf(wi, v[q].z, acc[q].z);
+          acc[q].w = fmaf(wi, v[q].w, acc[q].w);
         }
       }
     }
     if (G == 1) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) put4(sb + kA, i, lane, k, acc[k]);
+      for (int k = 0; k < 4; ++k) put4<L>(sb + L::kA, i, lane, k, acc[k]);
     } else {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) reinterpret_cast<float4*>(smem + share_at(warp))[lane + 32 * k] = acc[k];
+      for (int k = 0; k < 4; ++k) reinterpret_cast<float4*>(smem + L::kShare + 2048 * warp)[lane + 32 * k] = acc[k];
     }
   }
   if (G > 1) {
     __syncthreads();
-    if (warp < 4 * R) {   // columns 128 k .. of row i
-      const int i = warp >> 2, k = warp & 3;
-      if (rows[i].n != 1) {
+    for (int x = warp; x < 4 * R; x += kWarps) {   // columns 128 k .. of row i
+      const int i = x >> 2, k = x & 3, n = rows[i].n;
+      if (n != 1) {
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int g = 0; g < G; ++g) {
-          const float4 v = reinterpret_cast<const float4*>(smem + share_at(i * G + g))[lane + 32 * k];
+#pragma unroll 4
+        for (int g = 0; g < min(G, n); ++g) {
+          const float4 v = reinterpret_cast<const float4*>(smem + L::kShare + 2048 * (i * G + g))[lane + 32 * k];
           s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
         }
-        put4(sb + kA, i, lane, k, s);
+        put4<L>(sb + L::kA, i, lane, k, s);
       }
     }
   }
@@ -242,42 +244,43 @@ __global__ void __launch_bounds__(kThreads, 1) decode_out_kernel(const __grid_co
   bool ok = true;
   if (tid == 0) {
     for (int ch = 0; ch < 4 && ok; ++ch) {
-      const uint32_t b = ch & 1;
-      ok = wait(p.ws.err, bars + 8 * b, (ch >> 1) & 1);
+      const uint32_t b = ch % L::kChunks;
+      ok = wait(p.ws.err, bars + 8 * b, (ch / L::kChunks) & 1);
       if (!ok) break;
       tc_fence_after();
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk)
-        mma_bf16(tmem, sdesc_sw128(sb + kA + (2 * ch + (kk >> 2)) * kBlk + (kk & 3) * 32, 16, 1024),
-                 sdesc_sw128(sb + kB + b * 2 * kBlk + kk * 2048, kBlk, 1024), kIdesc, (ch | kk) ? 1u : 0u);
-      mma_commit(bars + 16 + 8 * b);
-      if (ch < 2) {
-        ok = wait(p.ws.err, bars + 16 + 8 * b, 0);
+        mma_bf16(tmem, sdesc_sw128(sb + L::kA + (2 * ch + (kk >> 2)) * L::kABlk + (kk & 3) * 32, 16, 1024),
+                 sdesc_sw128(sb + L::kB + b * 2 * kBlk + kk * 2048, kBlk, 1024), kIdesc, (ch | kk) ? 1u : 0u);
+      if (!kSmall || ch >= 2) mma_commit(done + 8 * (ch & 1));
+      if (!kSmall && ch < 2) {
+        ok = wait(p.ws.err, done + 8 * b, 0);
         if (ok) load_w(ch + 2);
       }
     }
   }
   ok = __syncthreads_and(ok);
-  if (ok) ok = wait(p.ws.err, bars + 16, 1) && wait(p.ws.err, bars + 24, 1);
+  if (ok) ok = wait(p.ws.err, done, kSmall ? 0 : 1) && wait(p.ws.err, done + 8, kSmall ? 0 : 1);
   ok = __syncthreads_and(ok);
   tc_fence_after();
   if (ok) {
-    // sixteen warps: TMEM lanes 32 (w mod 4) .., columns 32 (w / 4) ..; lanes 64 .. 127, the products of the rests,
-    // pass through shared memory (the weights' buffers)
-    const int q = warp & 3, i = 32 * (q & 1) + lane, cb = 32 * (warp >> 2);
-    float* rest = reinterpret_cast<float*>(smem + kB) + i * 132 + cb;   // 64 rows of 128, padded
-    const bool rows_here = warp < 16 && 32 * (q & 1) < R;
+    // sixteen warps: TMEM lanes 32 (w mod 4) .., columns 32 (w / 4) ..; the products of the rests, in lanes 64 ..
+    // 127 (16 tokens at most: in lanes 16 .. 31), pass through shared memory (the weights' buffers)
+    const int q = warp & 3, i = (32 * q + lane) % L::kRest, cb = 32 * (warp >> 2);
+    const bool of_rest = 32 * q + lane >= L::kRest;
+    float* rest = reinterpret_cast<float*>(smem + L::kB) + i * 132 + cb;   // rows of 128, padded
+    const bool rows_here = warp < 16 && (kSmall ? q == 0 : 32 * (q & 1) < R);
     uint32_t v[32];
     if (rows_here) {
       tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + cb, v);
-      if (q >= 2) {
+      if (of_rest) {
 #pragma unroll
         for (int k = 0; k < 8; ++k)
           reinterpret_cast<uint4*>(rest)[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
       }
     }
     __syncthreads();
-    if (rows_here && q < 2 && i < R && rows[i].n >= 0) {
+    if (rows_here && !of_rest && i < R && rows[i].n >= 0) {
       const int64_t orow = (int64_t)(r0 + i) * H + h, o = orow * kDv + cb;
       const bool empty = rows[i].lse == -INFINITY;   // no key seen: 0
 #pragma unroll
@@ -318,12 +321,15 @@ cudaError_t launch_decode_out(const DecodeOutParams& p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!configured[dev].load()) {
-    e = cudaFuncSetAttribute(decode_out_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    e = cudaFuncSetAttribute(decode_out_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Lay<false>::kSmem);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(decode_out_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Lay<true>::kSmem);
     if (e != cudaSuccess) return e;
     configured[dev].store(true);
   }
-  return launch_dependent(decode_out_kernel, dim3((p.batch.rows.rows + p.tile - 1) / p.tile, 1, p.batch.num_heads), kThreads,
-                          kSmem, p, s);
+  const dim3 grid((p.batch.rows.rows + p.tile - 1) / p.tile, 1, p.batch.num_heads);
+  return p.tile <= kSmallRows ? launch_dependent(decode_out_kernel<true>, grid, kThreads, Lay<true>::kSmem, p, s)
+                              : launch_dependent(decode_out_kernel<false>, grid, kThreads, Lay<false>::kSmem, p, s);
 }
 
 }  // namespace mla
