@@ -21,20 +21,34 @@
 // CTA's TMEM and Q [128 x 512] half of another's:
 //  - CTA 0 (scores): Q in TMEM, its rotated q_rope in shared memory; per tile
 //    S = Q [c | k_rope]^T (M = 128, N = 128) into one of two TMEM buffers, the
-//    running softmax of one row a thread, and P with the rows' rescale factors
+//    running softmax (two threads a row), and P with the rows' rescale factors
 //    staged and copied in bulk into the other CTA.
 //  - CTA 1 (values): O += P c (M = 128, N = 256 twice), rows rescaled in TMEM
-//    when their maximum rose by more than 2^8; at a piece's end O / l leaves.
-// Each CTA reads the cache's blocks in place by TMA, the scores as rows of all
-// 128 keys in blocks of 128 B, the values 32 KB at a time.
+//    when their maximum rose by more than 2^8 (FP8 2^4); at a piece's end O / l
+//    leaves.
+// Each CTA reads the cache's blocks in place by TMA, 16 KB a stage: the scores a
+// block of 128 B of all 128 keys, the values half the columns of 32 or 64 keys.
 //
 // An FP8 cache is multiplied as it is stored, on kind::f8f6f4, without a
 // conversion: what would be bf16 operands are two 8-bit terms each.  qlat is
 // q8 + q8', E4M3 codes by the row's scale and of what they leave (relative
-// error below 2^-8).  P is its value rounded to 2 mantissa bits in E5M2, whose
-// range keeps weights down to 2^-24 of the largest, and the rest in E4M3
-// (together below 2^-7, 1.3e-3 in the mean).  Two 8-bit MMAs take the time of
-// one bf16 MMA on a cache of half the bytes.
+// error below 2^-8).  P counts in units of 2^-7 of the largest weight: its
+// value rounded to f16 and then to 2 mantissa bits in E5M2, whose range keeps
+// weights down to 2^-23, and the rest in E4M3 (together below 2^-7, 1.3e-3 in
+// the mean).  Two 8-bit MMAs take the time of one bf16 MMA on a cache of half
+// the bytes.
+//
+// What bounds it.  A bf16 tile takes 2.0 us against 1.2 us of MMAs (36 of 64
+// cycles in one CTA, 16 of 128 in the other): in the scores CTA every tile moves
+// about 375 KB through shared memory (147 KB written by TMA, read by the MMAs,
+// P staged and copied), and with the cache in L2 it is 8% faster only.  An FP8
+// tile takes 1.35 to 1.5 us, the MMAs 1.2 of them (tensor pipes busy 60% of a
+// launch of 105 us, the start, the end and the handoffs the rest).  A launch
+// begins with 4.3 us from its plan to the first scores (Q through registers into
+// TMEM, then the first keys) and ends with 4 us for the last tile's chain and 6
+// us for 256 KB of fp32 states, at the 30 B a cycle that an SM stores to L2.
+// 64 requests of 2K to 32K bf16 tokens, 128 heads: 201 us with the kernels
+// before and after; 64 of 4K to 16K FP8 tokens: 139 us.
 #include <atomic>
 
 #include "serving.cuh"

@@ -5,6 +5,7 @@
 //   qabsorb_kernel<true>   qlat8[t][h][:] = e4m3(qlat / s), s = amax / 448 of the row
 //                          (for decode also e4m3(qlat / s - qlat8))
 //   absorb_proj_kernel     out[t][h][:]   = scale o[t H + h] W_UV,h             [128]
+// For decode the first launch also plans the attention (plan_decode).
 // Both are one tcgen05 MMA chain per CTA (M = 128 rows of one head), operands
 // staged in shared memory with 128-byte swizzle, the accumulator in TMEM.
 //

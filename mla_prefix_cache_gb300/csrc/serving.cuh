@@ -157,13 +157,13 @@ struct Walk {
   // range
   int64_t offset;
   int t0, n, k_lo, k_hi;
-  bool more, head, tail;
   // its piece
   int r, row0, slot, rows;   // request, first row of the item, slot of its state (-1: a whole item), the request's rows
   RequestWork w;             // of request r
   // where the walk is
   int cluster, at, end, first;        // next unit, one past the run's last, first unit of request r
   int lo, hi, g, last_key, acc;   // the piece's tiles; next range, end of the keys so far, tiles so far
+  bool more, head, tail;          // of the range (last here: they fill up a word)
   // run [begin, stop) of units, which begins in request q with its first unit f and work u
   __device__ __forceinline__ void start(int c, int begin, int stop, int q, int f, const RequestWork& u) {
     cluster = c;
