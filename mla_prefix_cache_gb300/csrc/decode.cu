@@ -38,6 +38,11 @@
 // the mean).  Two 8-bit MMAs take the time of one bf16 MMA on a cache of half
 // the bytes.
 //
+// A bf16 cache's operands are qlat, q_rope and P rounded to bf16 once each: 2.0e-3
+// of the output's norm together, where a bf16 output's own rounding is 1.7e-3.
+// Second terms of Q (whose MMAs read every block of keys again) would add 1.1 us
+// to a tile of 2.0, of P as much and 32 KB to copy.
+//
 // What bounds it.  A bf16 tile takes 2.0 us against 1.2 us of MMAs (36 of 64
 // cycles in one CTA, 16 of 128 in the other): in the scores CTA every tile moves
 // about 375 KB through shared memory (147 KB written by TMA, read by the MMAs,
