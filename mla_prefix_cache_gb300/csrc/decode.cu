@@ -108,7 +108,6 @@ constexpr uint32_t kShared = kBars + 8 * kNBars;   // TMEM address, then the han
 constexpr uint32_t kHand = kShared + 16;
 constexpr uint32_t kWalks = kHand + 16;            // the roles' walks
 constexpr int kRoles = 6;
-constexpr uint32_t kTxP = kPBytes + kFacBytes;
 
 constexpr uint32_t kIdS = idesc_bf16(128, 128, false, false);
 constexpr uint32_t kIdPV = idesc_bf16(128, 256, false, true);
@@ -365,12 +364,21 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       bool ok = true;
       int g = 0;
       while (ok && next_of_one(p, k, first)) {
+        // groups of 8 rows down to the item's last live one, in both blocks (16 of 128 rows live: a copy of all of
+        // them made the whole launch 8% longer).  What the other rows of P hold ends in rows of O that none reads.
+        const uint32_t live = min(kBlk, 1024u * (uint32_t)((k.rows - k.row0 + 7) >> 3));
         for (int j = 0; j < k.n && ok; ++j, ++g) {
           const int b = g & 1;
           // P tile b of the values CTA is free once the PV of tile g - 2 is done
           ok = await(p, bar(kPST + b), (g >> 1) & 1) && (g < 2 || await(p, bar(kPFR + b), ((g - 2) >> 1) & 1));
           if (!ok) break;
-          bulk_copy_to_peer(o_p + b * kPBytes, sb + kPS + b * kPBytes, kPBytes, o_pf + 8u * b);
+          mbar_arrive_expect_tx_cluster(o_pf + 8u * b, 2 * live + kFacBytes);
+          if (live == kBlk) {
+            bulk_copy_to_peer(o_p + b * kPBytes, sb + kPS + b * kPBytes, kPBytes, o_pf + 8u * b);
+          } else {
+            bulk_copy_to_peer(o_p + b * kPBytes, sb + kPS + b * kPBytes, live, o_pf + 8u * b);
+            bulk_copy_to_peer(o_p + b * kPBytes + kBlk, sb + kPS + b * kPBytes + kBlk, live, o_pf + 8u * b);
+          }
           bulk_copy_to_peer(o_fac + b * kFacBytes, sb + kFac + b * kFacBytes, kFacBytes, o_pf + 8u * b);
         }
       }
@@ -620,8 +628,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         s += n;
         while (s >= kOStages) { s -= kOStages; ph ^= 1u; }
       };
-      if (lane == 0)
-        for (int b = 0; b < 2; ++b) mbar_arrive_expect_tx(bar(kPF + b), kTxP);
       bool head = true;
       while (ok && next_of_warp(p, k, first, lane)) {
         if (k.head) head = true;
@@ -656,8 +662,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           }
           if ((flags & ~0xFFu) && !zero_not_finite<kFp8>(p, sb, s, ph, lane)) { ok = false; break; }
           fence_proxy_async_smem();   // P was written by the other CTA's copy, the MMA reads it as an operand
-          if (lane == 0) mbar_arrive_expect_tx_relaxed(bar(kPF + b), kTxP);
-          __syncwarp();
           tc_fence_after();
 #pragma unroll 1
           for (int i = 0; i < kOPerTile; ++i) {

@@ -48,6 +48,12 @@ __host__ __device__ constexpr uint32_t idesc_8bit(int M, int N, int a_format, in
   return idesc_e4m3(M, N) | ((uint32_t)a_format << 7) | ((uint32_t)b_format << 10) | ((b_mn ? 1u : 0u) << 16);
 }
 
+// Arrives on a barrier of the cluster and expects `bytes` on it (relaxed: the barrier only counts bytes).
+__device__ __forceinline__ void mbar_arrive_expect_tx_cluster(uint32_t cluster_bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_bar), "r"(bytes)
+               : "memory");
+}
+
 // The single-CTA forms (cta_group::1, M = 128) from one elected lane of a
 // converged warp, some consecutive K steps a statement: the lane is elected and
 // branched to once, and the operands move by constants (descriptors count 16
