@@ -439,6 +439,8 @@ DECODE = [
     ("ragged_rows", 33, [61, 190, 0, 1000, 5], [1, 9, 2, 4, 7]),
     ("long", 16, [9000], [2]),
     ("many", 3, [(37 * i) % 211 for i in range(150)], [1 + i % 2 for i in range(150)]),
+    ("wide", 128, [60 + (29 * i) % 200 for i in range(70)], [1] * 70),       # 64 tokens of a head a CTA at the end
+    ("mid", 64, [200 + i for i in range(25)], [2] * 25),                      # 32
 ]
 
 
@@ -816,6 +818,36 @@ def test_decode_after_append_equals_prefill_of_the_same_tokens(api):
                                softmax_scale=wl.softmax_scale)
     assert float((out - ref[n - 1:]).norm() / ref[n - 1:].norm()) <= 2 * REL_RMS
     assert float((lse - ref_lse[n - 1:]).abs().max()) <= 2e-2     # two 1e-2 lse bounds of 1300 unit-size logits
+
+
+@gpu
+@pytest.mark.parametrize("kv", ["bf16", "fp8_e4m3"])
+def test_decode_graphs_that_share_a_workspace(api, kv):
+    """Two captured calls of different batches on one workspace, first full of other bytes, replayed in turn: each
+    replay has its own results, bit for bit."""
+    wls = [W.make_workload("g0", 16, [900, 40, 300], [1, 2, 1], kv_dtype=kv, seed=60),
+           W.make_workload("g1", 48, [64, 2100], [3, 1], kv_dtype=kv, seed=61)]
+    devs = [Dev(api, w) for w in wls]
+    want = [d.decode() for d in devs]
+    n = max(api.decode_workspace_size(w.num_reqs, w.q.shape[0], w.num_heads) for w in wls)
+    ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+    outs = [(torch.empty_like(o), torch.empty_like(x)) for o, x in want]
+    graphs = []
+    for d, (o, x) in zip(devs, outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            d.decode(out=o, lse=x, workspace=ws)
+        graphs.append(g)
+    ws.fill_(255)
+    for i in (0, 1, 0, 0, 1, 1, 0, 1):
+        for o, x in outs:
+            o.zero_()
+            x.zero_()
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        assert api.device_error(ws) == 0
+        assert torch.equal(outs[i][0], want[i][0]) and torch.equal(outs[i][1], want[i][1])
+        assert not outs[1 - i][0].any()
 
 
 @gpu
