@@ -340,10 +340,8 @@ def block_compare(kv_cache: torch.Tensor, block_a: torch.Tensor, block_b: torch.
 
 def _at(t: torch.Tensor, name: str, device: int, dtype, shape=None) -> int:
     """Address of a contiguous tensor of `dtype` (and `shape`) on CUDA device `device`."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.get_device() != device:
-        raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
+    if not isinstance(t, torch.Tensor) or t.get_device() != device:
+        raise ValueError(f"{name} must be a tensor on cuda:{device}")
     if dtype is not None and t.dtype is not dtype:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if shape is not None and t.shape != shape:
@@ -358,7 +356,7 @@ def _current(t: torch.Tensor, name: str) -> int:
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     device = t.get_device()
-    if device != torch.cuda.current_device():
+    if device != torch._C._cuda_getDevice():
         raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
     return device
 

@@ -1799,6 +1799,17 @@ int mla_block_compare(const void* kv_cache, int kv_dtype, int num_blocks, const 
                                           reinterpret_cast<cudaStream_t>(stream)));
 }
 
+// The angles of a call that takes a few microseconds: 32 powers are 0.8 of them, so the last theta's are kept.
+static void serving_fracs(float theta, uint64_t* frac) {
+  thread_local float last = 0.f;
+  thread_local uint64_t kept[kDr / 2];
+  if (theta != last) {
+    rope_fracs((double)theta, kept);
+    last = theta;
+  }
+  std::copy(kept, kept + kDr / 2, frac);
+}
+
 // Shared validation of the serving entry points' batch description.
 static int batch_rows(const int32_t* cu_q, const int32_t* seq_lens, int num_reqs, int rows, BatchRows* b) {
   if (num_reqs < 0 || rows < 0) return MLA_ERR_INVALID_ARG;
@@ -1846,7 +1857,7 @@ int mla_cache_append(const void* kv, int64_t kv_row_stride, const int32_t* pos, 
   p.num_blocks = num_blocks;
   p.inv_scale = 1.f / kv_scale;
   p.err = dev_error;
-  rope_fracs((double)rope_theta, p.rope_frac);
+  serving_fracs(rope_theta, p.rope_frac);
   return cuda_status(launch_cache_append(p, kv_dtype == MLA_KV_FP8_E4M3, reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -1992,7 +2003,7 @@ int mla_decode(const void* q, const int32_t* q_pos, const void* kv_cache, int kv
   p.num_blocks = num_blocks;
   p.kv_scale = fp8 ? kv_scale : 1.f;
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
-  rope_fracs((double)rope_theta, p.rope_frac);
+  serving_fracs(rope_theta, p.rope_frac);
   cudaEvent_t ev_b = static_cast<cudaEvent_t>(g_ev_begin.load());
   cudaEvent_t ev_e = static_cast<cudaEvent_t>(g_ev_end.load());
   const bool timed = ev_b != nullptr && ev_e != nullptr;
