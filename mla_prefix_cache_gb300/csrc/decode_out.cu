@@ -8,9 +8,10 @@
 // operand of 512 columns, each value as its bf16 and, in other rows, the bf16 of
 // what that leaves, so that one chain of M = 128, N = 128 MMAs multiplies o to
 // 2^-16; the two products are added at the end.  W_UV,h comes by TMA in chunks
-// of 128 rows, two buffers deep; where there are 16 tokens at most, their rows
-// take a quarter of the space and all four chunks are there before the states
-// (the rows of the MMA that no token has read what lies behind).
+// of 128 rows, two buffers deep; where there are 32 tokens at most, their rows
+// leave room for all four chunks, which are there before the states (the rows of
+// the MMA that no token has read what lies behind), and with 16 also for partial
+// sums of warps that share a row.
 // Latency-bound: a row is two dependent loads from L2 (weights, states), so the
 // rows are spread over many warps (8 warps took 30 us for 64 tokens of 128
 // heads).
@@ -24,7 +25,6 @@ namespace {
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
 constexpr uint32_t kBlk = 16384;                   // [128 rows x 128 B] swizzled block
 constexpr int kMaxPieces = kDecodeClusters;        // of one item
-constexpr int kSmallRows = 16;
 
 struct RowOf {
   int x;           // unit of the item's first tile
@@ -35,20 +35,21 @@ struct RowOf {
 };
 static_assert(sizeof(RowOf) == 20, "row table");
 
-template <bool kSmall>
+template <int kTokens>   // at most, of a CTA: 16, 32 or 64
 struct Lay {
-  static constexpr int kRest = kSmall ? kSmallRows : 64;           // row of a state's rest: this many below
+  static constexpr int kRest = kTokens;                            // row of a state's rest: this many below
   static constexpr uint32_t kABlk = 2 * kRest * 128;               // 64 columns of the rows that tokens have
-  static constexpr int kChunks = kSmall ? 4 : 2;                   // buffers of [128 c x 128 j] in two blocks
+  static constexpr int kChunks = kTokens <= 32 ? 4 : 2;            // buffers of [128 c x 128 j] in two blocks
+  static constexpr bool kShared = kTokens <= 16;                   // warps may share a row
   static constexpr uint32_t kA = 0;                                // 8 blocks of 64 columns
   static constexpr uint32_t kB = 8 * kABlk;
   static constexpr uint32_t kShare = kB + kChunks * 2 * kBlk;      // partial sums of warps that share rows, 2 KB each
-  static constexpr uint32_t kRows = kShare + (kSmall ? kWarps * 2048 : 0);
-  static constexpr uint32_t kBegin = kRows + 64 * 20;              // first unit of each cluster
+  static constexpr uint32_t kRows = kShare + (kShared ? kWarps * 2048 : 0);
+  static constexpr uint32_t kBegin = kRows + kTokens * 20;         // first unit of each cluster
   static constexpr uint32_t kBars = (kBegin + 4 * (kDecodeClusters + 1) + 15) & ~15u;   // B landed, MMAs done x 2, TMEM address
   static constexpr uint32_t kSmem = kBars + 8 * (kChunks + 2) + 16;
+  static_assert(kSmem <= 232448, "more than 227 KB of shared memory per CTA");
 };
-static_assert(Lay<false>::kSmem <= 232448 && Lay<true>::kSmem <= 232448, "more than 227 KB of shared memory per CTA");
 constexpr uint32_t kIdesc = idesc_bf16(128, 128, false, true);
 __device__ __forceinline__ bool wait(uint32_t* err, uint32_t bar, uint32_t parity) {
   if (mbar_wait(bar, parity)) return true;
@@ -80,9 +81,9 @@ __device__ __forceinline__ void put4(uint32_t a, int i, int lane, int k, float4 
                : "memory");
 }
 
-template <bool kSmall>
+template <int kTokens>
 __global__ void __launch_bounds__(kThreads, 1) decode_out_kernel(const __grid_constant__ DecodeOutParams p) {
-  using L = Lay<kSmall>;
+  using L = Lay<kTokens>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sb = smem_u32(smem);
   const uint32_t bars = sb + L::kBars, done = bars + 8 * L::kChunks;
@@ -152,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_out_kernel(const __grid_co
 
   // ---------------------------------------------------------------- the rows' states
   int G = 1;        // warps a row
-  if (kSmall)
+  if (L::kShared)
     while (2 * G * R <= kWarps) G *= 2;
   const int part = warp % G;
   for (int i = warp / G; i < R; i += kWarps / G) {
@@ -252,24 +253,24 @@ __global__ void __launch_bounds__(kThreads, 1) decode_out_kernel(const __grid_co
       for (int kk = 0; kk < 8; ++kk)
         mma_bf16(tmem, sdesc_sw128(sb + L::kA + (2 * ch + (kk >> 2)) * L::kABlk + (kk & 3) * 32, 16, 1024),
                  sdesc_sw128(sb + L::kB + b * 2 * kBlk + kk * 2048, kBlk, 1024), kIdesc, (ch | kk) ? 1u : 0u);
-      if (!kSmall || ch >= 2) mma_commit(done + 8 * (ch & 1));
-      if (!kSmall && ch < 2) {
+      if (L::kChunks == 2 || ch >= 2) mma_commit(done + 8 * (ch & 1));
+      if (L::kChunks == 2 && ch < 2) {
         ok = wait(p.ws.err, done + 8 * b, 0);
         if (ok) load_w(ch + 2);
       }
     }
   }
   ok = __syncthreads_and(ok);
-  if (ok) ok = wait(p.ws.err, done, kSmall ? 0 : 1) && wait(p.ws.err, done + 8, kSmall ? 0 : 1);
+  if (ok) ok = wait(p.ws.err, done, L::kChunks == 4 ? 0 : 1) && wait(p.ws.err, done + 8, L::kChunks == 4 ? 0 : 1);
   ok = __syncthreads_and(ok);
   tc_fence_after();
   if (ok) {
-    // sixteen warps: TMEM lanes 32 (w mod 4) .., columns 32 (w / 4) ..; the products of the rests, in lanes 64 ..
-    // 127 (16 tokens at most: in lanes 16 .. 31), pass through shared memory (the weights' buffers)
+    // sixteen warps: TMEM lanes 32 (w mod 4) .., columns 32 (w / 4) ..; the products of the rests, in as many lanes
+    // behind those of the tokens, pass through shared memory (the weights' buffers)
     const int q = warp & 3, i = (32 * q + lane) % L::kRest, cb = 32 * (warp >> 2);
-    const bool of_rest = 32 * q + lane >= L::kRest;
+    const bool of_rest = 32 * q + lane >= L::kRest;   // (of lanes below 2 kRest)
     float* rest = reinterpret_cast<float*>(smem + L::kB) + i * 132 + cb;   // rows of 128, padded
-    const bool rows_here = warp < 16 && (kSmall ? q == 0 : 32 * (q & 1) < R);
+    const bool rows_here = warp < 16 && 32 * q < 2 * L::kRest && 32 * q % L::kRest < R;
     uint32_t v[32];
     if (rows_here) {
       tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + cb, v);
@@ -321,15 +322,18 @@ cudaError_t launch_decode_out(const DecodeOutParams& p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!configured[dev].load()) {
-    e = cudaFuncSetAttribute(decode_out_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Lay<false>::kSmem);
+    e = cudaFuncSetAttribute(decode_out_kernel<16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Lay<16>::kSmem);
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(decode_out_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Lay<true>::kSmem);
+      e = cudaFuncSetAttribute(decode_out_kernel<32>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Lay<32>::kSmem);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(decode_out_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Lay<64>::kSmem);
     if (e != cudaSuccess) return e;
     configured[dev].store(true);
   }
   const dim3 grid((p.batch.rows.rows + p.tile - 1) / p.tile, 1, p.batch.num_heads);
-  return p.tile <= kSmallRows ? launch_dependent(decode_out_kernel<true>, grid, kThreads, Lay<true>::kSmem, p, s)
-                              : launch_dependent(decode_out_kernel<false>, grid, kThreads, Lay<false>::kSmem, p, s);
+  if (p.tile <= 16) return launch_dependent(decode_out_kernel<16>, grid, kThreads, Lay<16>::kSmem, p, s);
+  if (p.tile <= 32) return launch_dependent(decode_out_kernel<32>, grid, kThreads, Lay<32>::kSmem, p, s);
+  return launch_dependent(decode_out_kernel<64>, grid, kThreads, Lay<64>::kSmem, p, s);
 }
 
 }  // namespace mla
