@@ -155,6 +155,12 @@ __global__ void __launch_bounds__(128, 1) qabsorb_kernel(const __grid_constant__
   const int c0 = blockIdx.y * L::kCols;
   const int t0 = p.row0 + blockIdx.x * 128;   // first token of the tile (TMA coordinates)
   if constexpr (kDecode) {                    // launched dependently
+    // the head's weights on their way to L2 while the kernel before this one runs (whose writes L2 sees in any order)
+    if (h >= 0 && threadIdx.x == 0)
+#pragma unroll
+      for (int nh = 0; nh < L::kHalves; ++nh)
+#pragma unroll
+        for (int db = 0; db < 2; ++db) tma_prefetch_l2_2d(&p.tm_w, 128 * h + 64 * db, c0 + 256 * nh);
     grid_wait();      // the inputs are there
     grid_trigger();   // the attention kernel may take SMs as they fall free
     if (h < 0) {

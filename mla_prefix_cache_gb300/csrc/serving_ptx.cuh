@@ -48,6 +48,11 @@ __host__ __device__ constexpr uint32_t idesc_8bit(int M, int N, int a_format, in
   return idesc_e4m3(M, N) | ((uint32_t)a_format << 7) | ((uint32_t)b_format << 10) | ((b_mn ? 1u : 0u) << 16);
 }
 
+// A box of a tensor map into L2.
+__device__ __forceinline__ void tma_prefetch_l2_2d(const void* map, int x, int y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(map), "r"(x), "r"(y) : "memory");
+}
+
 // Arrives on a barrier of the cluster and expects `bytes` on it (relaxed: the barrier only counts bytes).
 __device__ __forceinline__ void mbar_arrive_expect_tx_cluster(uint32_t cluster_bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_bar), "r"(bytes)
