@@ -155,7 +155,8 @@ __global__ void __launch_bounds__(128, 1) qabsorb_kernel(const __grid_constant__
   const int c0 = blockIdx.y * L::kCols;
   const int t0 = p.row0 + blockIdx.x * 128;   // first token of the tile (TMA coordinates)
   if constexpr (kDecode) {                    // launched dependently
-    // the head's weights on their way to L2 while the kernel before this one runs (whose writes L2 sees in any order)
+    // the head's weights on their way to L2 while the kernel before this one runs (what that one may still write of
+    // them, L2 will have: a prefetch reads nothing)
     if (h >= 0 && threadIdx.x == 0)
 #pragma unroll
       for (int nh = 0; nh < L::kHalves; ++nh)
