@@ -359,32 +359,34 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         }
         if (ok) mma_commit_elect(bar(kQE));
       }
-    } else if (warp == 2 && lane == 0) {
+    } else if (warp == 2) {
       // ---------------------------------------------------------- staged P and its factors into the values CTA
+      constexpr int kPieceRows = kFp8 ? 16 : 8;
+      constexpr uint32_t kPiece = 128 * kPieceRows;
       const uint32_t o_p = mapa_shared(sb + kOP, 1u), o_fac = mapa_shared(sb + kFac, 1u), o_pf = mapa_shared(bar(kPF), 1u);
       bool ok = true;
       int g = 0;
-      while (ok && next_of_one(p, k, first)) {
-        // groups of 8 rows down to the item's last live one, in both blocks (16 of 128 rows live: a copy of all of
-        // them made the whole launch 8% longer).  What the other rows of P hold ends in rows of O that none reads.
-        const uint32_t live = min(kBlk, 1024u * (uint32_t)((k.rows - k.row0 + 7) >> 3));
+      while (ok && next_of_warp(p, k, first, lane)) {
+        // Pieces of a block down to the item's last live rows (16 of 128 live: a copy of all of them made the whole
+        // launch 8% longer; what the other rows of P hold ends in rows of O that none reads), one a lane.  In pieces
+        // the copy passes between this CTA's loads: with one of 32 KB, 64 bf16 requests took 200 us, with 2 KB 192.5,
+        // with 1 KB 189.5 (FP8, whose loads are fewer: 139, 137.5, 140).
+        const uint32_t live = (uint32_t)(min(128, k.rows - k.row0) + kPieceRows - 1) / kPieceRows;   // pieces of a block
+        const uint32_t mine = lane % (128 / kPieceRows), at = lane / (128 / kPieceRows) * kBlk + mine * kPiece;
         for (int j = 0; j < k.n && ok; ++j, ++g) {
           const int b = g & 1;
           // P tile b of the values CTA is free once the PV of tile g - 2 is done
-          ok = await(p, bar(kPST + b), (g >> 1) & 1) && (g < 2 || await(p, bar(kPFR + b), ((g - 2) >> 1) & 1));
+          ok = await_warp(p, bar(kPST + b), (g >> 1) & 1) && (g < 2 || await_warp(p, bar(kPFR + b), ((g - 2) >> 1) & 1));
           if (!ok) break;
-          mbar_arrive_expect_tx_cluster(o_pf + 8u * b, 2 * live + kFacBytes);
-          if (live == kBlk) {
-            bulk_copy_to_peer(o_p + b * kPBytes, sb + kPS + b * kPBytes, kPBytes, o_pf + 8u * b);
-          } else {
-            bulk_copy_to_peer(o_p + b * kPBytes, sb + kPS + b * kPBytes, live, o_pf + 8u * b);
-            bulk_copy_to_peer(o_p + b * kPBytes + kBlk, sb + kPS + b * kPBytes + kBlk, live, o_pf + 8u * b);
+          if (lane == 0) {
+            mbar_arrive_expect_tx_cluster(o_pf + 8u * b, 2 * live * kPiece + kFacBytes);
+            bulk_copy_to_peer(o_fac + b * kFacBytes, sb + kFac + b * kFacBytes, kFacBytes, o_pf + 8u * b);
           }
-          bulk_copy_to_peer(o_fac + b * kFacBytes, sb + kFac + b * kFacBytes, kFacBytes, o_pf + 8u * b);
+          if (lane < 256 / kPieceRows && mine < live) bulk_copy_to_peer(o_p + b * kPBytes + at, sb + kPS + b * kPBytes + at, kPiece, o_pf + 8u * b);
         }
       }
       // the last two PV commits land before this CTA exits
-      for (int v = max(0, g - 2); v < g && ok; ++v) ok = await(p, bar(kPFR + (v & 1)), (v >> 1) & 1);
+      for (int v = max(0, g - 2); v < g && ok; ++v) ok = await_warp(p, bar(kPFR + (v & 1)), (v >> 1) & 1);
     } else if (warp >= 12) {
       // ---------------------------------------------------------- Q: qlat from its stages into TMEM
       const int r = tid - 384;
