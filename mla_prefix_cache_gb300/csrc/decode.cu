@@ -166,9 +166,9 @@ __device__ __forceinline__ bool next_of_group(const DecodeParams& p, Walk& k, bo
   if (!first) {
     named_bar_sync(id, count);
     if (leader) k.more = next(p, k);
-    named_bar_sync(id, count);
   }
   first = false;
+  named_bar_sync(id, count);
   return *const_cast<volatile bool*>(&k.more);
 }
 
@@ -273,6 +273,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
+  tc_fence_before();
+  cluster_sync_all();   // both CTAs' barriers exist before either is signalled
+  tc_fence_after();
+  const uint32_t tmem = *const_cast<volatile uint32_t*>(tmem_slot);
   grid_wait();      // the plan, qlat and the inputs are there
   grid_trigger();   // decode_out_kernel may take SMs as they fall free
   // scores: loads 0, 1, MMA, copies, Q, softmax; values: loads 0, 1, MMA, P landed, -, rescale
@@ -281,10 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   bool first = true;
   if (lane < kWalkWords && (warp <= 4 || warp == 12))
     reinterpret_cast<uint32_t*>(&k)[lane] = __ldcg(p.ws.walks + kWalkBytes / 4 * cluster + lane);
-  tc_fence_before();
-  cluster_sync_all();   // both CTAs' barriers exist before either is signalled
-  tc_fence_after();
-  const uint32_t tmem = *const_cast<volatile uint32_t*>(tmem_slot);
+  __syncwarp();
 
   if (scores) {
     if ((warp == 0 || warp == 3) && lane == 0) {
