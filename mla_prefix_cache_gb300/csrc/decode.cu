@@ -122,17 +122,6 @@ constexpr uint32_t kIdPV8r = idesc_8bit(128, 256, 0, 0, true);    // E4M3 rest o
 constexpr float kRescaleBf16 = 8.f, kRescaleFp8 = 4.f;
 constexpr float kPBiasFp8 = 7.f;
 
-// The larger of two bf16 values (16 bits each), as float bits.
-__device__ __forceinline__ uint32_t max_bf16(uint32_t a, uint32_t b) {
-  return __float_as_uint(fmaxf(__uint_as_float(a << 16), __uint_as_float(b << 16)));
-}
-// A float's bf16 not below it, as 16 bits.
-__device__ __forceinline__ uint32_t bf16_up(float x) {
-  const uint32_t u = __float_as_uint(x);
-  return ((int32_t)u >= 0 ? u + 0xFFFFu : u) >> 16;
-}
-
-
 // Stages of each half of the columns that a piece's states leave through, if it has 32 live rows (fewer are written by
 // their threads).
 constexpr int kBoxes = 4;
@@ -510,15 +499,20 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             }
             mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
           }
-          // the row's maximum over both halves, rounded up to bf16 by both threads alike (any common reference
-          // near the maximum will do).  The two warps exchange in their 128 bytes of the sums' place beside this
-          // P tile; two tiles on, both are past the next tile's barrier, so these reads are done.
-          uint8_t* fac = smem + kFac + b * kFacBytes;
-          volatile uint16_t* mx16 = reinterpret_cast<volatile uint16_t*>(fac + kFacSum + 128 * (warp & 3));
-          volatile float* l32 = reinterpret_cast<volatile float*>(fac + kFacSum + 128 * (warp & 3));
-          mx16[32 * half + lane] = (uint16_t)bf16_up(mx);
+          // The row's maximum over both halves, in fp32: a reference some bits above it would lose P where the scores
+          // are large.  The two threads exchange in the staging buffer, each in a chunk that the other writes its
+          // P to, which reads it after the barrier and before that.
+          const uint32_t stg = sb + kPS + b * kPBytes;
+          // chunk c of a half of the row.  bf16: 64 keys are the half's own block; 8-bit: 4 chunks of each term's block
+          auto chunk = [&](int hh, int c) {
+            return kFp8 ? stg + (c >> 2) * kBlk + sw128_off((uint32_t)r, (uint32_t)(4 * hh + (c & 3)))
+                        : stg + hh * kBlk + sw128_off((uint32_t)r, (uint32_t)c);
+          };
+          const uint32_t word = 4 * ((lane >> 3) & 3);   // the 32 rows in 32 banks
+          sts32(chunk(half ^ 1, 0) + word, __float_as_uint(mx));
           named_bar_sync(pair, 64);
-          const float m_tile = __uint_as_float(max_bf16(mx16[lane], mx16[32 + lane])) * sl2;
+          const float m_tile = fmaxf(mx, __uint_as_float(lds32(chunk(half, 0) + word))) * sl2;
+          uint8_t* fac = smem + kFac + b * kFacBytes;
           float alpha = 1.f;
           if (m_tile > m_used + (kFp8 ? kRescaleFp8 : kRescaleBf16)) {
             alpha = ex2(m_used - m_tile);   // 0 when m_used = -inf
@@ -559,22 +553,15 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           f2unpack(s2[1], s4[2], s4[3]);
           l = l * alpha + ((s4[0] + s4[2]) + (s4[1] + s4[3]));
           if (tail && j == n - 1) {   // the piece's last tile: the row's sum over both halves
-            named_bar_sync(pair, 64);   // the maxima have been read
-            if (half) l32[lane] = l;
+            if (half) sts32(chunk(0, 1) + word, __float_as_uint(l));
             named_bar_sync(pair, 64);
             if (half == 0) {
-              lsum = l + l32[lane];
-              l32[lane] = lsum;
+              lsum = l + __uint_as_float(lds32(chunk(0, 1) + word));
+              reinterpret_cast<float*>(fac + kFacSum)[r] = lsum;
             }
           }
-          const uint32_t stg = sb + kPS + b * kPBytes;
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            // bf16: 64 keys are the half's own block; 8-bit: 4 chunks of each term's block
-            const uint32_t at = kFp8 ? stg + (c >> 2) * kBlk + sw128_off((uint32_t)r, (uint32_t)(4 * half + (c & 3)))
-                                     : stg + half * kBlk + sw128_off((uint32_t)r, (uint32_t)c);
-            sts128(at, pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
-          }
+          for (int c = 0; c < 8; ++c) sts128(chunk(half, c), pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
           // P = 0 does not hide a key that is not finite from O: a query before it would have NaN
           const uint32_t any_odd = __any_sync(0xffffffffu, odd != 0.f) ? 0x100u : 0u;
           uint16_t* flag = reinterpret_cast<uint16_t*>(fac + kFacFlags + 4 * (warp & 3)) + half;

@@ -1,5 +1,5 @@
 // PTX of the serving kernels beside what ptx.cuh has: conversions of 8-bit
-// terms, and single-CTA MMAs several a statement.
+// terms, words of shared memory, and single-CTA MMAs several a statement.
 #pragma once
 
 #include "ptx.cuh"
@@ -46,6 +46,16 @@ __device__ __forceinline__ float2 e4m3x2_floats(uint32_t pair) {
 // be alike, and B MN-major.
 __host__ __device__ constexpr uint32_t idesc_8bit(int M, int N, int a_format, int b_format, bool b_mn) {
   return idesc_e4m3(M, N) | ((uint32_t)a_format << 7) | ((uint32_t)b_format << 10) | ((b_mn ? 1u : 0u) << 16);
+}
+
+// A word of shared memory.
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
 // A box of a tensor map into L2.

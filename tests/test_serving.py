@@ -922,3 +922,46 @@ def test_decode_allocates_on_the_stream_that_it_runs_on(api):
     torch.cuda.synchronize()
     for o, x in got:
         assert torch.equal(o, want[0]) and torch.equal(x, want[1])
+
+
+# ------------------------------------------------------------------ values at the range's ends
+
+def rope_scores(wl, logits, heads):
+    """Makes the score of key t of the batch's only request, for head h, logits[t] * heads[h]: no latent query, one
+    q_rope at position 0, keys along it (each with its bf16 roundings, as decode_ref has them)."""
+    rng = np.random.Generator(np.random.PCG64(70))
+    n = int(wl.seq_lens[0])
+    qr = rng.standard_normal(64)
+    wl.q[...] = 0
+    wl.q_pos[...] = 0
+    wl.q[..., 128:] = W.f32_to_bf16_bits((np.asarray(heads)[None, :, None] * qr).astype(np.float32))
+    t = np.arange(n)
+    k = W.f32_to_bf16_bits((np.asarray(logits)[:, None] / wl.softmax_scale * qr / (qr @ qr)).astype(np.float32))
+    wl.kv_cache[wl.block_table[0][t // 64], t % 64, 512:] = k if wl.kv_dtype == "bf16" else k.view(np.uint8)
+
+
+def set_latents(wl, c):
+    """Latents of the batch's only request."""
+    t = np.arange(c.shape[0])
+    if wl.kv_dtype == "bf16":
+        x = W.f32_to_bf16_bits(c.astype(np.float32))
+    else:
+        x = torch.from_numpy((c / wl.kv_scale).clip(-448, 448).astype(np.float32)).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+    wl.kv_cache[wl.block_table[0][t // 64], t % 64, :512] = x
+
+
+@gpu
+@pytest.mark.parametrize("kv", ["bf16", "fp8_e4m3"])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("logit", [1e2, 1e3, 1e4, 1e5])
+def test_decode_large_logits(api, kv, sign, logit):
+    """The largest logits are logit (1 + h / 16) for head h, of either sign, shared by five equal keys in both halves
+    of several tiles; every other key lies at least an eighth of that below, e^-12 and less.  The output is the five
+    keys' mean, whatever the error that a score of this size has (2^-9 of it, alike for equal keys)."""
+    n, H = 900, 16
+    wl = W.make_workload("ll", H, [n - 1], [1], kv_dtype=kv, seed=62)
+    rng = np.random.Generator(np.random.PCG64(63))
+    x = rng.uniform(-1, 0.875, n) if sign > 0 else rng.uniform(-2, -1.125, n)
+    x[[3, 77, 300, 777, 895]] = sign
+    rope_scores(wl, logit * x, 1 + np.arange(H) / 16)
+    check_decode(api, wl)
