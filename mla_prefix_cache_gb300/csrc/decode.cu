@@ -32,11 +32,16 @@
 // An FP8 cache is multiplied as it is stored, on kind::f8f6f4, without a
 // conversion: what would be bf16 operands are two 8-bit terms each.  qlat is
 // q8 + q8', E4M3 codes by the row's scale and of what they leave (relative
-// error below 2^-8).  P counts in units of 2^-7 of the largest weight: its
-// value rounded to f16 and then to 2 mantissa bits in E5M2, whose range keeps
-// weights down to 2^-23, and the rest in E4M3 (together below 2^-7, 1.3e-3 in
-// the mean).  Two 8-bit MMAs take the time of one bf16 MMA on a cache of half
-// the bytes.
+// error below 2^-8).  P is p + p', both E5M2, in units of 2^-11 of the largest
+// weight: its value rounded to f16 and then to 2 mantissa bits, and what that
+// leaves, together within 2^-7 of a weight (2.5e-3 rms) down to 2^-21 of the
+// largest and 2^-28 of the largest below.  (An E4M3 p' halves that error, but its
+// least step of 2^-9 leaves weights below 2^-10 of the largest with p alone, off
+// by 5% rms: rows whose output is many small weights beside one of a small value
+// were off by as much.)  O is divided by the sum of the weights as they are
+// multiplied, so that an error that equal weights share does not stay; lse is
+// made of their sum in fp32.  Two 8-bit MMAs take the time of one bf16 MMA on a
+// cache of half the bytes.
 //
 // A bf16 cache's operands are qlat, q_rope and P rounded to bf16 once each: 2.0e-3
 // of the output's norm together, where a bf16 output's own rounding is 1.7e-3.
@@ -113,14 +118,12 @@ constexpr int kRoles = 6;
 constexpr uint32_t kIdS = idesc_bf16(128, 128, false, false);
 constexpr uint32_t kIdPV = idesc_bf16(128, 256, false, true);
 constexpr uint32_t kIdS8 = idesc_8bit(128, 128, 0, 0, false);
-constexpr uint32_t kIdPV8 = idesc_8bit(128, 256, 1, 0, true);     // E5M2 P
-constexpr uint32_t kIdPV8r = idesc_8bit(128, 256, 0, 0, true);    // E4M3 rest of P
+constexpr uint32_t kIdPV8 = idesc_8bit(128, 256, 1, 0, true);     // E5M2 terms of P
 // Rows are rescaled when their maximum rises by more than this (log2 units).
-// 8-bit terms of P: P counts in units of 2^-7, so that it spans 2^11 down to
-// what E5M2 holds, and what the first term leaves of it stays between E4M3's
-// 448 and its least normal 2^-6 for weights down to 2^-10 of the largest.
+// 8-bit terms of P: P counts in units of 2^-11, so that it spans 2^15, below
+// E5M2's and f16's largest, down to E5M2's least step 2^-16.
 constexpr float kRescaleBf16 = 8.f, kRescaleFp8 = 4.f;
-constexpr float kPBiasFp8 = 7.f;
+constexpr float kPBiasFp8 = 11.f;
 
 // Stages of each half of the columns that a piece's states leave through, if it has 32 live rows (fewer are written by
 // their threads).
@@ -428,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       // are met
       bool ok = true;
       int g = 0;
-      float m_used = -INFINITY, l = 0.f, lsum = 0.f;
+      float m_used = -INFINITY, l = 0.f, lt = 0.f, lsum = 0.f;   // lt: of P as its terms hold it
       while (next_of_group(p, k, first, tid == 128, 5, 256)) {
         const int prow = k.row0 + r;
         const bool live = prow < k.rows;
@@ -465,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         const bool tail = k.tail;
         if (k.head) {
           m_used = -INFINITY;
-          l = lsum = 0.f;
+          l = lt = lsum = 0.f;
         }
 #pragma unroll 1
         for (int j = 0; j < n; ++j, ++g) {
@@ -521,8 +524,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           const float mref = ((m_used == -INFINITY) ? 0.f : m_used) - (kFp8 ? kPBiasFp8 : 0.f);
           const uint64_t sc2 = f2pack(sl2, sl2), nm2 = f2pack(-mref, -mref);
           // P in registers while the previous tile's copy is still in flight: bf16 pairs, or per four keys a
-          // word of E5M2 and a word of E4M3 codes
+          // word of each term's codes
           uint64_t s2[2] = {0ull, 0ull};
+          float t0 = 0.f, t1 = 0.f;   // 8-bit: the sums of the two terms
           uint32_t pk[32];
           {
 #pragma unroll
@@ -532,10 +536,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
               const float a = ex2(x0), bb = ex2(x1);
               s2[c & 1] = fadd2(s2[c & 1], f2pack(a, bb));
               if constexpr (kFp8) {
-                // f16 (2^-11), its nearest E5M2, and the rest of it, which f16 holds exactly, in E4M3
+                // f16 (2^-11), its nearest E5M2, the rest of it, which f16 holds exactly, and that in E5M2 too
                 const uint32_t h16 = pack_f16(a, bb);
-                const uint32_t h2 = e5m2x2_of_f16x2(h16);
-                const uint32_t r2 = e4m3x2_of_f16x2(sub_f16x2(h16, __byte_perm(h2, 0u, 0x1404)));
+                const uint32_t h2 = e5m2x2_of_f16x2(h16), hw = __byte_perm(h2, 0u, 0x1404);   // (E5M2: f16's high byte)
+                const uint32_t r2 = e5m2x2_of_f16x2(sub_f16x2(h16, hw));
+                add_f16x2(t0, t1, fadd_f16x2(hw, __byte_perm(r2, 0u, 0x1404)));               // their sum: exact in f16
                 if (c & 1) {
                   pk[c >> 1] = __byte_perm(pk[c >> 1], h2, 0x5410);
                   pk[16 + (c >> 1)] = __byte_perm(pk[16 + (c >> 1)], r2, 0x5410);
@@ -552,12 +557,16 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           f2unpack(s2[0], s4[0], s4[1]);
           f2unpack(s2[1], s4[2], s4[3]);
           l = l * alpha + ((s4[0] + s4[2]) + (s4[1] + s4[3]));
-          if (tail && j == n - 1) {   // the piece's last tile: the row's sum over both halves
-            if (half) sts32(chunk(0, 1) + word, __float_as_uint(l));
+          if (kFp8) lt = lt * alpha + (t0 + t1);
+          if (tail && j == n - 1) {   // the piece's last tile: the row's sums over both halves
+            if (half) {
+              sts32(chunk(0, 1) + word, __float_as_uint(l));
+              if (kFp8) sts32(chunk(0, 2) + word, __float_as_uint(lt));
+            }
             named_bar_sync(pair, 64);
             if (half == 0) {
               lsum = l + __uint_as_float(lds32(chunk(0, 1) + word));
-              reinterpret_cast<float*>(fac + kFacSum)[r] = lsum;
+              reinterpret_cast<float*>(fac + kFacSum)[r] = kFp8 ? lt + __uint_as_float(lds32(chunk(0, 2) + word)) : lsum;
             }
           }
 #pragma unroll
@@ -669,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
               // k-steps 2 i, 2 i + 1 of the tile: 16 keys (bf16) or 32 (FP8) each
               const uint32_t acc = (head && i == 0) ? 0u : 1u;
               const uint64_t pd = sdesc_add(pd0, b * kPBytes + (kFp8 ? i * 64 : (i >> 1) * kBlk + (i & 1) * 64));
-              if (kFp8) mma_ss2x2_mn_8bit_elect(tmem + 256 * nh, pd, cd, kIdPV8, acc, kIdPV8r);
+              if (kFp8) mma_ss2x2_mn_8bit_elect(tmem + 256 * nh, pd, cd, kIdPV8, acc);
               else mma_ss2_mn_elect(tmem + 256 * nh, pd, cd, kIdPV, acc);
               mma_commit_elect(bar(kCE + s));
               advance(1);

@@ -6,8 +6,9 @@
 
 namespace mla {
 
-// f16 pairs (the low half holds the first): from floats, their difference, and
-// their E5M2 and E4M3 codes (two bytes), all rounded to nearest even.
+// f16 pairs (the low half holds the first): from floats, their difference and
+// sum, their E5M2 codes (two bytes), all rounded to nearest even, and each added
+// to a float.
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -18,14 +19,18 @@ __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
+__device__ __forceinline__ uint32_t fadd_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ void add_f16x2(float& lo, float& hi, uint32_t a) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tadd.rn.f32.f16 %0, l, %0;\n\tadd.rn.f32.f16 %1, h, %1;\n\t}"
+      : "+f"(lo), "+f"(hi) : "r"(a));
+}
 __device__ __forceinline__ uint32_t e5m2x2_of_f16x2(uint32_t a) {
   uint16_t r;
   asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(a));
-  return r;
-}
-__device__ __forceinline__ uint32_t e4m3x2_of_f16x2(uint32_t a) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(a));
   return r;
 }
 
@@ -116,13 +121,13 @@ __device__ __forceinline__ void mma_ss2_mn_elect(uint32_t d_tmem, uint64_t a_des
                "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
                : "memory");
 }
-// Two K steps of two 8-bit terms of A, the second 16 KB on and of another
-// format, with B MN-major (4096 bytes a step of 32 rows).
+// Two K steps of two 8-bit terms of A, the second 16 KB on, with B MN-major
+// (4096 bytes a step of 32 rows).
 __device__ __forceinline__ void mma_ss2x2_mn_8bit_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                                        uint32_t accumulate, uint32_t idesc2) {
-  asm volatile(MLA_ELECT(MLA_SS("f8f6f4", "0", "0", "%3", "p") MLA_SS("f8f6f4", "1024", "0", "%5", "q")
-                             MLA_SS("f8f6f4", "2", "256", "%3", "q") MLA_SS("f8f6f4", "1026", "256", "%5", "q"))::"r"(d_tmem),
-               "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(idesc2)
+                                                        uint32_t accumulate) {
+  asm volatile(MLA_ELECT(MLA_SS("f8f6f4", "0", "0", "%3", "p") MLA_SS("f8f6f4", "1024", "0", "%3", "q")
+                             MLA_SS("f8f6f4", "2", "256", "%3", "q") MLA_SS("f8f6f4", "1026", "256", "%3", "q"))::"r"(d_tmem),
+               "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
                : "memory");
 }
 #undef MLA_ELECT

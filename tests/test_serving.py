@@ -965,3 +965,32 @@ def test_decode_large_logits(api, kv, sign, logit):
     x[[3, 77, 300, 777, 895]] = sign
     rope_scores(wl, logit * x, 1 + np.arange(H) / 16)
     check_decode(api, wl)
+
+
+@gpu
+@pytest.mark.parametrize("kv", ["bf16", "fp8_e4m3"])
+@pytest.mark.parametrize("tail", ["equal", "spread"])
+@pytest.mark.parametrize("nats", [5, 7, 9, 11, 12, 14])
+def test_decode_small_weights_beside_a_sink(api, kv, tail, nats):
+    """One key whose latent is 0 lies nats .. nats + 1 above 4095 others, whose latents have no common part: the
+    output is made of their weights alone, each e^-nats of the largest.  A weight may be off by 2^-7 of it (the sum
+    of two 8-bit terms of three bits each), of standard deviation 2^-7 / sqrt(3) at most, beside the four other
+    roundings; the sink's score by nats u / sqrt(3) times sqrt(3 / 64) for 64 products of a normal q_rope with
+    itself: sqrt(4 (u / sqrt(3))^2 + (2^-7 / sqrt(3))^2 + (14 u / 8)^2) = 9.4e-3 of the output, below REL_RMS."""
+    n, H, B = 4096, 16, 80
+    wl = W.make_workload("sw", H, [n - 1], [1], kv_dtype=kv, seed=64)
+    rng = np.random.Generator(np.random.PCG64(65))
+    x = np.zeros(n) if tail == "equal" else 0.5 * rng.standard_normal(n)
+    x[50] = nats
+    rope_scores(wl, x, 1 + np.arange(H) / (16 * nats))
+    c = rng.standard_normal((n, 512))
+    c[50] = 0
+    set_latents(wl, c)
+    ref = decode_ref(wl)
+    # 80 requests over the same rows: each cluster has a whole one's tiles, so that the others stand beside the sink
+    d = Dev(api, wl)
+    d.q, d.q_pos, d.seq_lens = d.q.repeat(B, 1, 1), d.q_pos.repeat(B), d.seq_lens.repeat(B)
+    d.block_table = d.block_table.repeat(B, 1)
+    out, lse = d.decode(cu_q=None)
+    assert api.device_error(api.decode.last_workspace) == 0
+    assert_decode(out, lse, tuple(np.repeat(x, B, 0) for x in ref))
