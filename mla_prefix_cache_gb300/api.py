@@ -52,9 +52,11 @@ def launch_count() -> int:
 
 
 def kv_dtype_code(kv_cache: torch.Tensor) -> int:
-    if kv_cache.dtype == torch.bfloat16 and kv_cache.shape[-1] == 576:
+    # a pool of other blocks is refused: the kernels find row 64 id + slot of a block id
+    block = kv_cache.shape[1:]
+    if kv_cache.dtype == torch.bfloat16 and block == (64, 576):
         return KV_BF16
-    if kv_cache.dtype == torch.uint8 and kv_cache.shape[-1] == 640:
+    if kv_cache.dtype == torch.uint8 and block == (64, 640):
         return KV_FP8_E4M3
     raise ValueError("kv_cache must be bf16 [NB,64,576] or uint8 [NB,64,640]")
 

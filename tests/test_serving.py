@@ -994,3 +994,41 @@ def test_decode_small_weights_beside_a_sink(api, kv, tail, nats):
     out, lse = d.decode(cu_q=None)
     assert api.device_error(api.decode.last_workspace) == 0
     assert_decode(out, lse, tuple(np.repeat(x, B, 0) for x in ref))
+
+
+# ------------------------------------------------------------------ caches of another shape
+
+def other_pools(device):
+    """Caches of another block size, of flat rows and of another row, of 40 blocks' rows each."""
+    shapes = [(160, 16), (20, 128), (2560,), (1, 40, 64), (40, 64, 1)]
+    rows = [(torch.bfloat16, 576), (torch.uint8, 640)]
+    pools = [torch.zeros(s + (n,), dtype=t, device=device) for s in shapes for t, n in rows]
+    return pools + [torch.zeros((40, 64, n), dtype=t, device=device) for t, n in ((torch.bfloat16, 640), (torch.uint8, 576), (torch.float16, 576))]
+
+
+def test_cache_shapes_are_checked():
+    from mla_prefix_cache_gb300 import api as A
+    assert A.kv_dtype_code(torch.zeros((3, 64, 576), dtype=torch.bfloat16)) == _lib.KV_BF16
+    assert A.kv_dtype_code(torch.zeros((3, 64, 640), dtype=torch.uint8)) == _lib.KV_FP8_E4M3
+    for pool in other_pools("cpu"):
+        with pytest.raises(ValueError):
+            A.kv_dtype_code(pool)
+
+
+@gpu
+def test_calls_refuse_caches_of_another_shape(api):
+    wl = W.make_workload("sh", 16, [70, 90], [1, 1], seed=69)
+    d = Dev(api, wl)
+    kv, ids = torch.ones((2, 576), dtype=torch.bfloat16, device="cuda"), torch.zeros(2, dtype=torch.int32, device="cuda")
+    for pool in other_pools("cuda"):
+        d.kv_cache = pool
+        for call in (lambda: d.decode(),
+                     lambda: api.cache_append(kv, d.q_pos, pool, d.block_table, d.seq_lens),
+                     lambda: api.gather_latent(pool, d.block_table[0], 0, 1),
+                     lambda: api.block_hash(pool, ids),
+                     lambda: api.block_compare(pool, ids, ids),
+                     lambda: api.prefill(d.q, d.q_pos, pool, d.block_table, wl.seq_lens, wl.cu_q, d.kv_b_proj, chunk=128,
+                                         softmax_scale=wl.softmax_scale)):
+            with pytest.raises(ValueError):
+                call()
+        assert not pool.view(torch.uint8).any()
