@@ -480,7 +480,7 @@ int mla_block_compare(const void* kv_cache, int kv_dtype, int num_blocks, const 
  *                before cu_q[0] and behind cu_q[num_reqs] are left out.
  *  seq_lens      device int32 [num_reqs]: the requests' tokens with the new
  *                rows.  A row whose token index is negative (a padded request
- *                of length 0) is left out.
+ *                of length 0, or of any negative one) is left out.
  *  dev_error     device uint32, optional: bit 0 is set for a row whose block
  *                id lies outside [0, num_blocks) or whose token lies behind
  *                the block table (the row is not written).

@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm) cache_append_kernel
       past = row + 1;                       // no request's row: before the first one, or behind the last
       if (r >= 0) {
         past = request_rows(p.batch, r).y;
-        len = __ldg(p.batch.seq_lens + r);
+        len = max(__ldg(p.batch.seq_lens + r), 0);   // (so that no token index below leaves 32 bits)
       }
     }
     int stop = min(past, end);

@@ -1032,3 +1032,13 @@ def test_calls_refuse_caches_of_another_shape(api):
             with pytest.raises(ValueError):
                 call()
         assert not pool.view(torch.uint8).any()
+
+
+@gpu
+@pytest.mark.parametrize("n", [0, -1, -5, -2 ** 31 + 5, -2 ** 31 + 1, -2 ** 31])
+def test_append_leaves_requests_of_negative_length_out(api, n):
+    c = append_case([70, 66, 80], [3, 5, 4], "bf16", seed=10)
+    c["lens"][1] = n
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    check_append(c, run_append(api, c, dev_error=err))
+    assert int(err.item()) == 0
