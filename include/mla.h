@@ -532,8 +532,9 @@ int mla_cache_append(const void* kv, int64_t kv_row_stride, const int32_t* pos, 
  *  softmax_scale positive.
  *  num_heads     H in [1, 128].
  * What a query does not see may hold anything, also where another query of the
- * request sees it.  A query that sees a value that is not finite has NaN where
- * the score is NaN or infinite, and nothing of that key where it is -infinite.
+ * request sees it.  A query that sees a key whose latent part is not finite has
+ * NaN in out.  A score that is NaN or infinite makes out and lse NaN too; one of
+ * -infinite by the key's k_rope part leaves nothing of that key.
  * A cu_q that does not ascend sets the error word as a bad block id does, and
  * no row is attended.  A block id outside [0, num_blocks) reads as zero
  * rows and sets the error word, as does a sequence longer than its block

@@ -203,27 +203,54 @@ __device__ __noinline__ void zero_rows(uint32_t stage, int lo, int hi, int lane)
   __syncwarp();
 }
 
-// Zeroes the 16-byte pieces of a tile's values stages (from stage s on, of parity ph) that hold a value that is not
-// finite, as above.  The ring holds a whole tile.
+// The last key token that live row i of a request's rows sees.
+__device__ __forceinline__ int last_key(const Walk& k, int i, int H) { return k.w.len - (k.rows - 1 - i) / H - 1; }
+
+// Tile j of a range, whose P is in buffer b and whose values stages begin at s, of parity ph, may hold a key that is not
+// finite and that some rows do not see: the 16-byte pieces of its latents that are not finite are zeroed, and bf16 rows
+// that see such a key have NaN as its weight (an infinity with a score of -infinite has weight 0 so far; E4M3 has NaN
+// only, which is in the score).  The ring holds a whole tile.
 template <bool kFp8>
-__device__ __noinline__ bool zero_not_finite(const DecodeParams& p, uint32_t sb, int s, uint32_t ph, int lane) {
+__device__ __noinline__ bool zero_not_finite(const DecodeParams& p, const Walk& k, int j, int b, uint32_t sb, int s,
+                                             uint32_t ph, int lane) {
   constexpr uint32_t kOnes = kFp8 ? 0x7F7F7F7Fu : 0x7F807F80u;   // E4M3's NaN, bf16's exponent
-  constexpr int kStages = 128 * 1024 / (kFp8 ? 2 : 1) / kOStage;
+  constexpr int kStages = 128 * 1024 / (kFp8 ? 2 : 1) / kOStage, kRows = kFp8 ? 64 : 32;
   static_assert(kStages <= kOStages, "a tile's stages");
   bool ok = true;
 #pragma unroll 1
-  for (int i = 0; i < kStages && ok; ++i) {
-    ok = await_warp(p, sb + kBars + 8 * (kCF + s), ph);
-    const uint32_t stage = sb + kORing + s * kOStage;
+  for (int i = 0; i < kStages && ok; i += 2) {   // both halves of the columns of the same keys
+    uint32_t bad = 0;                            // of the keys, 32 of them (bf16)
 #pragma unroll 1
-    for (uint32_t at = stage + 16 * lane; ok && at < stage + kOStage; at += 512) {
-      uint32_t w[4], any = 0;
-      lds128(at, w);
+    for (int nh = 0; nh < 2 && ok; ++nh) {
+      ok = await_warp(p, sb + kBars + 8 * (kCF + s), ph);
+      const uint32_t stage = sb + kORing + s * kOStage;
+#pragma unroll 1
+      for (uint32_t at = 16 * lane; ok && at < kOStage; at += 512) {
+        uint32_t w[4], any = 0;
+        lds128(stage + at, w);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) any |= kFp8 ? __vcmpeq4(w[k] & kOnes, kOnes) : __vcmpeq2(w[k] & kOnes, kOnes);
-      if (any) sts128(at, 0u, 0u, 0u, 0u);
+        for (int q = 0; q < 4; ++q) any |= kFp8 ? __vcmpeq4(w[q] & kOnes, kOnes) : __vcmpeq2(w[q] & kOnes, kOnes);
+        if (any) {
+          sts128(stage + at, 0u, 0u, 0u, 0u);
+          bad |= 1u << ((at >> 7) % kRows & 31);
+        }
+      }
+      if (++s == kOStages) { s = 0; ph ^= 1u; }
     }
-    if (++s == kOStages) { s = 0; ph ^= 1u; }
+    if (!kFp8) {
+      bad = __reduce_or_sync(0xffffffffu, bad);
+#pragma unroll 1
+      for (; ok && bad; bad &= bad - 1) {
+        const int key = (i >> 1) * kRows + __ffs(bad) - 1, kt = k.t0 + 128 * j + key;   // in the tile, its token
+#pragma unroll 1
+        for (int r = lane; kt >= k.k_lo && kt < k.k_hi && r < min(kItemRows, k.rows - k.row0); r += 32)
+          if (kt <= last_key(k, k.row0 + r, p.batch.num_heads))
+            asm volatile("st.shared.b16 [%0], %1;" ::"r"(sb + kOP + b * kPBytes + (key >> 6) * kBlk +
+                                                         sw128_off((uint32_t)r, (uint32_t)(key & 63) >> 3) + 2 * (key & 7)),
+                         "h"((uint16_t)0x7FC0)
+                         : "memory");
+      }
+    }
   }
   fence_proxy_async_smem();
   __syncwarp();
@@ -463,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           __syncwarp();
           if (lane == 0 && ok) mbar_arrive(bar(kQRd));
         }
-        const int qk = live ? k.w.len - (k.rows - 1 - prow) / H - 1 : -1;   // the last key token the row sees
+        const int qk = live ? last_key(k, prow, H) : -1;
         const int n = k.n, t0 = k.t0, k_lo = k.k_lo, k_hi = k.k_hi, slot = k.slot;
         const bool tail = k.tail;
         if (k.head) {
@@ -660,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             }
             if (!await_warp(p, bar(kCD), events++ & 1)) { ok = false; break; }
           }
-          if ((flags & ~0xFFu) && !zero_not_finite<kFp8>(p, sb, s, ph, lane)) { ok = false; break; }
+          if ((flags & ~0xFFu) && !zero_not_finite<kFp8>(p, k, j, b, sb, s, ph, lane)) { ok = false; break; }
           fence_proxy_async_smem();   // P was written by the other CTA's copy, the MMA reads it as an operand
           tc_fence_after();
 #pragma unroll 1

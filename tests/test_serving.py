@@ -1042,3 +1042,37 @@ def test_append_leaves_requests_of_negative_length_out(api, n):
     err = torch.zeros(1, dtype=torch.int32, device="cuda")
     check_append(c, run_append(api, c, dev_error=err))
     assert int(err.item()) == 0
+
+
+@gpu
+@pytest.mark.parametrize("kv, where", [("bf16", 3), ("bf16", 515), ("fp8_e4m3", 515)])    # a latent value, a RoPE value
+@pytest.mark.parametrize("token", [5, 200, 515, 598])    # in an inner tile, in the last one, a new one but the last
+@pytest.mark.parametrize("H", [16, 64])                  # 64 rows of an item of 128, two whole items
+def test_decode_infinite_key(api, kv, where, token, H):
+    """An infinite latent makes a query that sees it NaN whatever its score's sign, an infinite k_rope where the
+    score is +infinite; at -infinite it leaves nothing of the key.  The tile's place changes nothing."""
+    wl = W.make_workload("inf", H, [596], [4], kv_dtype=kv, seed=68)
+    rot = turn(bf16_values(wl.q)[..., 128:], angles(wl.q_pos.astype(np.int64))[:, None])
+    lat = np.einsum("ihd,chd->ihc", bf16_values(wl.q)[..., :128], bf16_values(wl.kv_b_proj)[:, :H * 128].reshape(512, H, 128))
+    tol = decode_ref(wl)[2]
+    row = wl.kv_cache[wl.block_table[0][token // 64], token % 64]
+    if kv == "bf16":
+        row[where] = 0x7F80                                                      # +inf
+    else:
+        row[512:].view(np.uint16)[where - 512] = 0x7F80
+    out, lse = Dev(api, wl).decode()
+    assert api.device_error(api.decode.last_workspace) == 0
+    with np.errstate(all="ignore"):
+        ref = decode_ref(wl)
+    up = (lat[..., where] if where < 512 else rot[..., where - 512]) > 0     # the score's sign
+    sees = token <= 596 + np.arange(4)
+    nan = sees[:, None] & (up | (where < 512))
+    got = out.double().cpu().numpy()
+    assert np.array_equal(np.isnan(got).all(-1), nan) and np.array_equal(np.isnan(got).any(-1), nan)
+    assert up[sees].any() and not up[sees].all()
+    down = sees[:, None] & ~up                                                   # lse without the key
+    x = lse.double().cpu().numpy()
+    assert np.isnan(x[sees[:, None] & up]).all()
+    assert (np.abs(x[down] - ref[1][down]) <= tol[down]).all()
+    keep = ~nan
+    assert np.linalg.norm(got[keep] - ref[0][keep]) <= REL_RMS * np.linalg.norm(ref[0][keep])
