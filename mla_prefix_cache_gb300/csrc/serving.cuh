@@ -90,9 +90,10 @@ __device__ __forceinline__ KeyRange request_range(const DecodeBatch& b, int2 sg,
   const int64_t s = __ldg(b.segments + 3 * (int64_t)i), n = __ldg(b.segments + 3 * (int64_t)i + 1);
   k.offset = __ldg(b.segments + 3 * (int64_t)i + 2);
   const int64_t lo = s < end ? (int64_t)end : s;
-  const int64_t e = n <= 0 ? lo : (n > (int64_t)len - s ? (int64_t)len : s + n);   // no overflow for any n
+  // neither sum leaves 64 bits: s >= 0 in the first, s < 0 < n or s + n <= len in the second
+  const int64_t e = n <= 0 ? lo : (s >= 0 && n > (int64_t)len - s) ? (int64_t)len : s + n;
   k.lo = (int)(lo < len ? lo : len);
-  k.hi = (int)(e < k.lo ? k.lo : e);
+  k.hi = (int)(e < k.lo ? k.lo : e < len ? e : len);
   return k;
 }
 // 128-key tiles of a range: they start at the cache block that holds its first key.

@@ -1076,3 +1076,13 @@ def test_decode_infinite_key(api, kv, where, token, H):
     assert (np.abs(x[down] - ref[1][down]) <= tol[down]).all()
     keep = ~nan
     assert np.linalg.norm(got[keep] - ref[0][keep]) <= REL_RMS * np.linalg.norm(ref[0][keep])
+
+
+@gpu
+@pytest.mark.parametrize("kv", ["bf16", "fp8_e4m3"])
+def test_decode_segments_at_the_ends_of_64_bits(api, kv):
+    lo, hi = -2 ** 63, 2 ** 63 - 1
+    wl = W.make_workload("s64", 16, [300, 300, 300, 300, 300], [1, 1, 2, 1, 1], kv_dtype=kv, seed=66)
+    segs = [[(lo, 1, 0), (10, 20, 5)], [(lo, hi, 0), (0, 7, 0)], [(-5, 10, 3), (hi, 1, 0)], [(hi, hi, 0)],
+            [(lo + 1, hi, 0), (2, hi, 9)]]
+    check_decode(api, wl, segs)
