@@ -528,7 +528,8 @@ int mla_cache_append(const void* kv, int64_t kv_row_stride, const int32_t* pos, 
  *  workspace     device, 256-B aligned, at least mla_decode_workspace_size(...)
  *                bytes; holds the device error word read by
  *                mla_get_device_error().  Calls that may overlap on the GPU
- *                must not share it.
+ *                must not share it.  With total_q = 0 nothing is launched and
+ *                the word stays as it is.
  *  softmax_scale positive.
  *  num_heads     H in [1, 128].
  * What a query does not see may hold anything, also where another query of the

@@ -439,6 +439,8 @@ def _decode_tensors(device, B, T_q, H, out, out_dtype, lse, return_lse, workspac
         lse = torch.empty((T_q, H), dtype=torch.float32, device=device)
     if workspace is None:
         workspace = torch.empty(decode_workspace_size(B, T_q, H), dtype=torch.uint8, device=device)
+        if T_q == 0:      # nothing will be launched that sets the error word
+            workspace[:4] = 0
     return out, lse, workspace
 
 

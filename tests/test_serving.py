@@ -1086,3 +1086,13 @@ def test_decode_segments_at_the_ends_of_64_bits(api, kv):
     segs = [[(lo, 1, 0), (10, 20, 5)], [(lo, hi, 0), (0, 7, 0)], [(-5, 10, 3), (hi, 1, 0)], [(hi, hi, 0)],
             [(lo + 1, hi, 0), (2, hi, 9)]]
     check_decode(api, wl, segs)
+
+
+@gpu
+def test_decode_of_no_rows_reports_no_error(api):
+    wl = W.make_workload("nr", 16, [70, 90], [1, 1], seed=67)
+    d = Dev(api, wl)
+    junk = torch.full((api.decode_workspace_size(2, 0, 16),), 255, dtype=torch.uint8, device="cuda")
+    del junk                 # the allocator hands its memory to the call
+    api.decode(d.q[:0], d.q_pos[:0], d.kv_cache, d.block_table, d.seq_lens, d.kv_b_proj, softmax_scale=0.07)
+    assert api.device_error(api.decode.last_workspace) == 0
