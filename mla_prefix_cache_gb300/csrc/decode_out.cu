@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_out_kernel(const __grid_co
       for (int k = 0; k < kPerLane; ++k) {
         const int c = o.c0 + lane + 32 * k;
         const bool have = lane + 32 * k < o.n;
-        at[k] = have ? (2 * c + (begin[c] <= o.x ? 1 : 0)) * kItemRows + o.ridx : 0;
+        at[k] = have ? piece_slot(c, begin[c] <= o.x) * kItemRows + o.ridx : 0;
         w[k] = have ? p.ws.part_lse[at[k]] : -INFINITY;
         m = fmaxf(m, w[k]);
       }

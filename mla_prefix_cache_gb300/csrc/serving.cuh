@@ -141,12 +141,10 @@ __device__ __forceinline__ int unit_begin(int c, int n, int total) {   // floor(
   return c * q + c * (total - q * n) / n;
 }
 __device__ __forceinline__ int cluster_of(int x, int n, int total) { return (int)(((uint64_t)(x + 1) * (uint32_t)n - 1) / (uint32_t)total); }
-// The slot of the state that cluster c has of an item whose first tile is unit
-// x: each cluster shares one item with the clusters before it at most, and one
-// with those after it.
-__device__ __forceinline__ int piece_slot(int c, int x, int n, int total) {
-  return 2 * c + (unit_begin(c, n, total) <= x ? 1 : 0);
-}
+// The slot of the state that cluster c has of a shared item, by whether it has
+// the item's first tile: each cluster shares one item with the clusters before it
+// at most, and one with those after it.
+__device__ __forceinline__ int piece_slot(int c, bool first_tile) { return 2 * c + (first_tile ? 1 : 0); }
 
 // A cluster's run of units, walked alike by every role, as ranges of key tiles
 // with one RoPE offset: tiles j = 0 .. n - 1 of 128 keys from key t0 on, of
@@ -200,7 +198,7 @@ __device__ __forceinline__ bool next_range(const DecodeBatch& b, Walk& k) {
       k.at = stop;
       if (k.hi <= k.lo) continue;   // only units of the item's start
       k.row0 = item * kItemRows;
-      k.slot = (k.lo == 0 && k.hi == k.w.tiles) ? -1 : 2 * k.cluster + (k.lo == 0 ? 1 : 0);
+      k.slot = (k.lo == 0 && k.hi == k.w.tiles) ? -1 : piece_slot(k.cluster, k.lo == 0);
       break;
     }
     k.head = true;
