@@ -148,6 +148,12 @@ static int env_int(const char* name, int dflt) {
   return (v && *v) ? std::atoi(v) : dflt;
 }
 
+// Every wait of a kernel gives up after 2 s (the error word then reads
+// MLA_ERR_TIMEOUT).  Tests shorten it (MLA_WAIT_LIMIT_US, at least 1 ms).
+static uint64_t wait_limit_ns() {
+  return (uint64_t)std::max(1000, std::min(2000000, env_int("MLA_WAIT_LIMIT_US", 2000000))) * 1000ull;
+}
+
 struct FusedPlan {
   std::vector<uint8_t> skip;      // the plan's skipped requests
   std::vector<Piece> pieces;      // LPT order, group_begin unset
@@ -658,11 +664,9 @@ static int prefill_fused(const void* q, const int32_t* q_pos, const void* kv_cac
   // once), and fewer than the ring lanes: a producer waits for the lane's
   // previous job, whose consumers must precede it in the queue.
   p.prod_ahead = std::max(1, std::min(producer_lookahead(), fw.ring_lanes - 1));
-  // Every wait of the kernel gives up after 2 s (the error word then reads
-  // MLA_ERR_TIMEOUT).  Tests shorten it (MLA_WAIT_LIMIT_US, at least 1 ms) and
-  // withhold the producers of one job (MLA_TEST_WITHHOLD_JOB) to make a wait
-  // run out on purpose.
-  p.wait_limit_ns = (uint64_t)std::max(1000, std::min(2000000, env_int("MLA_WAIT_LIMIT_US", 2000000))) * 1000ull;
+  // Tests withhold the producers of one job (MLA_TEST_WITHHOLD_JOB) to make a
+  // wait run out on purpose.
+  p.wait_limit_ns = wait_limit_ns();
   p.withhold_job = env_int("MLA_TEST_WITHHOLD_JOB", -1);
   p.l2_hints = env_int("MLA_L2_HINTS", 1) != 0 ? 1 : 0;
   // error word + role queue (keep_err: a caller running several sub-calls keeps the error word)
@@ -2003,6 +2007,8 @@ int mla_decode(const void* q, const int32_t* q_pos, const void* kv_cache, int kv
   p.num_blocks = num_blocks;
   p.kv_scale = fp8 ? kv_scale : 1.f;
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
+  p.wait_limit_ns = wait_limit_ns();
+  p.withhold = env_int("MLA_TEST_WITHHOLD_CLUSTER", -1);
   serving_fracs(rope_theta, p.rope_frac);
   cudaEvent_t ev_b = static_cast<cudaEvent_t>(g_ev_begin.load());
   cudaEvent_t ev_e = static_cast<cudaEvent_t>(g_ev_end.load());

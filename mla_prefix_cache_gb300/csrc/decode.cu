@@ -165,13 +165,13 @@ __device__ __forceinline__ bool next_of_group(const DecodeParams& p, Walk& k, bo
 }
 
 // Waits for a barrier's phase; false, and the error word, when it gives up.
-__device__ __noinline__ bool await_long(uint32_t* err, uint32_t bar, uint32_t parity) {
-  if (mbar_wait(bar, parity)) return true;
-  atomicOr(err, kErrTimeout);
+__device__ __noinline__ bool await_long(const DecodeParams& p, uint32_t bar, uint32_t parity) {
+  if (mbar_wait(bar, parity, p.wait_limit_ns)) return true;
+  atomicOr(p.ws.err, kErrTimeout);
   return false;
 }
 __device__ __forceinline__ bool await(const DecodeParams& p, uint32_t bar, uint32_t parity) {
-  return mbar_try_wait(bar, parity) || await_long(p.ws.err, bar, parity);
+  return mbar_try_wait(bar, parity) || await_long(p, bar, parity);
 }
 __device__ __forceinline__ bool await_warp(const DecodeParams& p, uint32_t bar, uint32_t parity) {
   return __all_sync(0xffffffffu, await(p, bar, parity));
@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         mbar_arrive_expect_tx(bar(kSF + s), kBlk);
         return true;
       };
-      while (ok && next_of_one(p, k, first)) {
+      while (ok && cluster != p.withhold && next_of_one(p, k, first)) {
         const int qrow = k.w.q_begin * H + k.row0;
         for (int i = 0; k.head && i < kQBoxes; ++i, ++u) {
           if ((u & 1) != mine) continue;
@@ -344,6 +344,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       }
       // the last reads are signalled before this CTA exits
       for (int v = max(0, u - kSStages); v < u && ok; ++v) ok = await(p, bar(kSE + v % kSStages), (v / kSStages) & 1);
+      // a wait gave up: the loads in flight land first
+      for (int v = max(0, u - kSStages); v < u && !ok; ++v)
+        if ((v & 1) == mine) await(p, bar(kSF + v % kSStages), (v / kSStages) & 1);
     } else if (warp == 1) {
       // ---------------------------------------------------------- S = Q [c | k_rope]^T
       bool ok = true;
@@ -407,6 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       }
       // the last two PV commits land before this CTA exits
       for (int v = max(0, g - 2); v < g && ok; ++v) ok = await_warp(p, bar(kPFR + (v & 1)), (v >> 1) & 1);
+      for (int v = max(0, g - 2); v < g && !ok; ++v) await_warp(p, bar(kSTF + (v & 1)), (v >> 1) & 1);   // as above, the copies
     } else if (warp >= 12) {
       // ---------------------------------------------------------- Q: qlat from its stages into TMEM
       const int r = tid - 384;
@@ -641,7 +645,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           }
         }
       }
-      for (int v = u - kOStages < nh ? nh : u - kOStages; v < u && ok; v += 2) ok = await(p, bar(kCE + v % kOStages), (v / kOStages) & 1);
+      const int last = u - kOStages < nh ? nh : u - kOStages;
+      for (int v = last; v < u && ok; v += 2) ok = await(p, bar(kCE + v % kOStages), (v / kOStages) & 1);
+      for (int v = last; v < u && !ok; v += 2) await(p, bar(kCF + v % kOStages), (v / kOStages) & 1);   // as above
     } else if (warp == 1) {
       // ---------------------------------------------------------- P landed, rows rescaled, O += P c
       volatile int* hand = reinterpret_cast<volatile int*>(smem + kHand);

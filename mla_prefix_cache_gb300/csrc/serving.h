@@ -96,6 +96,8 @@ struct DecodeParams {
   int num_blocks;
   float kv_scale;                // 1 for bf16 rows
   float scale_log2;
+  uint64_t wait_limit_ns;        // bound of every wait (a timeout sets kErrTimeout)
+  int withhold;                  // test hook: this cluster's loads of Q and scores' keys are not made, so the waits for them run out (-1: none)
   uint64_t rope_frac[kDr / 2];
 };
 cudaError_t launch_decode_attn(const DecodeParams& p, bool fp8, int clusters, cudaStream_t s);

@@ -1096,3 +1096,35 @@ def test_decode_of_no_rows_reports_no_error(api):
     del junk                 # the allocator hands its memory to the call
     api.decode(d.q[:0], d.q_pos[:0], d.kv_cache, d.block_table, d.seq_lens, d.kv_b_proj, softmax_scale=0.07)
     assert api.device_error(api.decode.last_workspace) == 0
+
+
+@gpu
+@pytest.mark.parametrize("kv", ["bf16", "fp8_e4m3"])
+@pytest.mark.parametrize("lens, rows, cluster", [
+    ([300], 1, 2),                    # 3 tiles and 2 units before them, a cluster each: the first tile's
+    ([700] * 40, 2, 0),               # 320 units: the first cluster has an item's first two tiles
+    ([0, 5000, 60, 1500], 9, 20),     # 124 units: units 32 and 33, inside the second request
+], ids=["one", "pieces", "mixed"])
+def test_decode_wait_runs_out_and_reports_timeout(api, monkeypatch, kv, lens, rows, cluster):
+    """Failure detection without a fault: one cluster's loads of Q and of the scores' keys are withheld (a test hook of
+    the library), so that the waits for them and for all that comes of them run out after the shortened limit.  The
+    kernel records MLA_ERR_TIMEOUT, frees its tensor memory and returns, the other clusters' rows are right, and so is
+    the next call on the same workspace."""
+    wl = W.make_workload("to", 16, lens, [rows] * len(lens), kv_dtype=kv, seed=71)
+    d = Dev(api, wl)
+    ws = torch.empty(api.decode_workspace_size(len(lens), rows * len(lens), 16), dtype=torch.uint8, device="cuda")
+    monkeypatch.setenv("MLA_WAIT_LIMIT_US", "2000")
+    monkeypatch.setenv("MLA_TEST_WITHHOLD_CLUSTER", str(cluster))
+    out, lse = d.decode(workspace=ws)
+    torch.cuda.synchronize()
+    assert api.device_error(ws) == 6                 # MLA_ERR_TIMEOUT
+    assert api.device_error(ws) == 0                 # cleared by the read
+    monkeypatch.delenv("MLA_TEST_WITHHOLD_CLUSTER")
+    monkeypatch.delenv("MLA_WAIT_LIMIT_US")
+    ref = decode_ref(wl)
+    if len(lens) > 1:                                # the cluster has none of the last request's keys
+        last = slice(-rows, None)
+        assert_decode(out[last], lse[last], tuple(x[last] for x in ref))
+    out, lse = d.decode(workspace=ws)
+    assert api.device_error(ws) == 0
+    assert_decode(out, lse, ref)
