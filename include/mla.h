@@ -521,9 +521,10 @@ int mla_cache_append(const void* kv, int64_t kv_row_stride, const int32_t* pos, 
  *                Rows of out and lse before cu_q[0] and behind
  *                cu_q[num_reqs] are not written.
  *  out           device [total_q, H, 128], fp32 or bf16 per out_dtype.  A row
- *                that sees no key is 0.
+ *                that sees no key is 0, and so is one whose scores are all
+ *                -infinite.
  *  lse           device fp32 [total_q, H], optional (NULL): natural log, -inf
- *                for a row that sees no key.
+ *                for those rows.
  *  kv_scale      FP8 caches: 2^-32 .. 2^32.
  *  workspace     device, 256-B aligned, at least mla_decode_workspace_size(...)
  *                bytes; holds the device error word read by
@@ -536,6 +537,8 @@ int mla_cache_append(const void* kv, int64_t kv_row_stride, const int32_t* pos, 
  * request sees it.  A query that sees a key whose latent part is not finite has
  * NaN in out.  A score that is NaN or infinite makes out and lse NaN too; one of
  * -infinite by the key's k_rope part leaves nothing of that key.
+ * FP8 caches: a softmax weight is held within 2^-7 of itself, or within 2^-28 of
+ * the row's largest where that is more (2^-8 of itself for bf16 caches).
  * A cu_q that does not ascend sets the error word as a bad block id does, and
  * no row is attended.  A block id outside [0, num_blocks) reads as zero
  * rows and sets the error word, as does a sequence longer than its block

@@ -52,14 +52,14 @@
 // 64 cycles in one CTA, 16 of 128 in the other): in the scores CTA every tile
 // moves about 375 KB through shared memory (147 KB written by TMA, read by the
 // MMAs, P staged and copied), 76 clusters draw 5.4 TB/s of rows, and with the
-// cache in L2 a tile is 8% faster only.  An FP8 tile takes 1.35 to 1.5 us, the
-// MMAs 1.2 of them (tensor pipes busy 60% of a launch of 105 us, the start, the
+// cache in L2 a tile is 8% faster only.  An FP8 tile takes 1.4 to 1.55 us, the
+// MMAs 1.2 of them (tensor pipes busy 60% of a launch of 104 us, the start, the
 // end and the handoffs the rest).  A launch begins with 4.3 us from its plan to
 // the first scores (Q through registers into TMEM, then the first keys) and ends
 // with 4 us for the last tile's chain and 6 us for 256 KB of fp32 states, at the
 // 30 B a cycle that an SM stores to L2.  64 requests of 2K to 32K bf16 tokens, 128
 // heads: 189 us with the kernels before and after; 64 of 4K to 16K FP8 tokens:
-// 137 us.
+// 139 us.
 #include <atomic>
 
 #include "serving.cuh"

@@ -18,6 +18,8 @@ latent state before W_UV and the output to bf16 (or to something finer).
    at most (scores, through their unit-size logits; weights; state; output; and
    the query's through the keys' common direction): 5.1e-3 of the output's norm
    together, held to twice that.
+   (The weights of an FP8 cache are sums of two E5M2 terms, within 2^-7: 2^-7 /
+   sqrt(3) in the place of one u / sqrt(3), 6.4e-3 together, under the same bound.)
 """
 import ctypes
 import math
