@@ -534,8 +534,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
           }
           // The row's maximum over both halves, in fp32: a reference some bits above it would lose P where the scores
-          // are large.  The two threads exchange in the staging buffer, each in a chunk that the other writes its
-          // P to, which reads it after the barrier and before that.
+          // are large.  Each thread leaves its own in the staging buffer, in a chunk that the other one reads behind
+          // the barrier and only then writes its P to.
           const uint32_t stg = sb + kPS + b * kPBytes;
           // chunk c of a half of the row.  bf16: 64 keys are the half's own block; 8-bit: 4 chunks of each term's block
           auto chunk = [&](int hh, int c) {

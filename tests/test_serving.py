@@ -1130,3 +1130,14 @@ def test_decode_wait_runs_out_and_reports_timeout(api, monkeypatch, kv, lens, ro
     out, lse = d.decode(workspace=ws)
     assert api.device_error(ws) == 0
     assert_decode(out, lse, ref)
+
+
+@gpu
+@pytest.mark.parametrize("kv", ["bf16", "fp8_e4m3"])
+def test_decode_long_context(api, kv):
+    # 131072 tokens, two queries: 2048 blocks, each of 64 distinct ones 32 times in the table
+    wl = W.make_workload("lc", 8, [4094], [2], kv_dtype=kv, seed=72)
+    wl.block_table = np.tile(wl.block_table[:, :64], (1, 32))
+    wl.ctx_lens = wl.ctx_lens + np.int32(31 * 4096)
+    wl.q_pos = wl.q_pos + np.int32(31 * 4096)
+    check_decode(api, wl)
