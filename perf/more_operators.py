@@ -1,8 +1,7 @@
 """The operators of a sparse decoding step, as they are measured: block tables
 and slot maps from the requests' lengths, the mean row of every block that new
-rows fill, a cheap score of every block for every query, the choice of the
-blocks that a query attends, and the attention over blocks that are scored and
-chosen on the way.
+rows fill, a cheap score of every block for every query, and the choice of the
+blocks that a query attends.
 
 ``run`` computes each in its plain form, elementary torch operations in 32 bits
 rounded once at the end, or, where ``own`` is true, through the framework's
@@ -19,12 +18,10 @@ own = False
 D_C, D_R, D_NOPE, D_V, BLOCK = 512, 64, 128, 128, 64
 ROW = D_C + D_R
 THETA = 10000.0
-#: Most rows of a step, (query, head, block) products, (query, block) pairs, cached tokens and chosen blocks of a case.
+#: Most rows of a step, (query, head, block) products and (query, block) pairs of a case.
 MOST_ROWS = 65536
 MOST_PRODUCTS = 32 * 2048 * 128
 MOST_PAIRS = 128 * 16384
-MOST_KEYS = 16 * 131074
-MOST_CHOSEN = 64 * 32
 
 
 def listed():
@@ -32,7 +29,6 @@ def listed():
     m = lambda name, **k: dict({"name": name, "op": "means", "kv": "bf16", "spread": 1}, **k)  # noqa: E731
     s = lambda name, **k: dict({"name": name, "op": "scores", "heads": 128, "q": 1, "spread": 1}, **k)  # noqa: E731
     c = lambda name, **k: dict({"name": name, "op": "select", "scores": "fp32", "q": 1, "sinks": 1, "recent": 2, "spread": 1}, **k)  # noqa: E731
-    d = lambda name, **k: dict({"name": name, "op": "sparse", "heads": 128, "q": 1, "kv": "bf16", "sinks": 1, "recent": 2, "spread": 1}, **k)  # noqa: E731
     return [
         # a decoding step with four drafted tokens each, and the cut back to the accepted ones
         t("tables_64_drafts", kind="drafts", reqs=64, lo=2048, hi=32768, new=5),
@@ -40,12 +36,16 @@ def listed():
         t("tables_32_prompts", kind="prompts", reqs=32, lo=512, hi=4096, new=4096),
         # a large continuous batch: sequences end, others begin, behind a shared prefix of 16 blocks
         t("tables_512_mixed", kind="mixed", reqs=512, lo=1024, hi=32768, new=128, shared=16),
-        # a decoding step with three drafted tokens each, FP8 cache: one request in 16 fills a block
-        m("means_64_step_fp8", reqs=64, lo=2048, hi=32768, new_lo=4, new_hi=4, kv="fp8"),
+        # a decoding step with three drafted tokens each: one request in 16 fills a block
+        m("means_64_step", reqs=64, lo=2048, hi=32768, new_lo=4, new_hi=4),
+        # a prefill batch of ragged new extents, FP8 cache
+        m("means_8_prefill_fp8", reqs=8, lo=512, hi=8192, new_lo=512, new_hi=4096, kv="fp8"),
         # a long prefill
         m("means_4x16k", reqs=4, lo=16384, hi=16384, new_lo=15000, new_hi=16384),
         # one user's next token over a 32K prompt
         s("scores_1x32k", reqs=1, lo=32769, hi=32769),
+        # a shard of 32 heads with three drafted tokens per request
+        s("scores_24_heads32_draft", reqs=24, lo=1000, hi=12000, heads=32, q=4),
         # a full serving batch with ragged contexts
         s("scores_64_mixed", reqs=64, lo=2048, hi=32768),
         # long prompts
@@ -54,17 +54,13 @@ def listed():
         c("select_64_mixed", reqs=64, lo=2048, hi=32768, keep=32),
         # a million tokens each
         c("select_128x1m", reqs=128, lo=1 << 20, hi=1 << 20, keep=64),
-        # the whole of it in a full serving batch: 2048 tokens attended of up to 32768
-        d("sparse_64_mixed", reqs=64, lo=2048, hi=32768, keep=32),
-        # long prompts in an FP8 cache, one drafted token verified with the next one, 4096 tokens attended
-        d("sparse_16x128k_fp8_draft", reqs=16, lo=131074, hi=131074, q=2, keep=64, kv="fp8"),
     ]
 
 
 def draw(rng):
     log = lambda lo, hi: int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))  # noqa: E731
     spread = rng.randrange(1 << 20)
-    op = rng.choice(["tables", "means", "scores", "scores", "select", "sparse", "sparse"])
+    op = rng.choice(["tables", "means", "scores", "scores", "select"])
     if op == "tables":
         kind = rng.choice(["drafts", "prompts", "mixed"])
         reqs = log(1, 512)
@@ -85,15 +81,9 @@ def draw(rng):
         reqs = log(1, 128)
         hi = log(512, max(513, min(1 << 19, BLOCK * MOST_PRODUCTS // (128 * reqs * q))))
         return {"op": op, "heads": heads, "q": q, "reqs": reqs, "lo": log(max(256, hi / 16), hi), "hi": hi, "spread": spread}
-    sinks, recent = rng.randrange(0, 4), rng.randrange(1, 4)
-    if op == "sparse":
-        reqs = log(1, 128)
-        keep = max(sinks + recent + 1, log(1, max(1, min(128, MOST_CHOSEN // (reqs * q)))))
-        hi = log(512, max(513, min(1 << 18, MOST_KEYS // reqs, BLOCK * MOST_PRODUCTS // (128 * reqs * q))))
-        return {"op": op, "heads": rng.choice([128, 128, 64, 32, 16, rng.randrange(8, 129)]), "q": q, "kv": rng.choice(["bf16", "fp8"]), "reqs": reqs,
-                "lo": log(max(256, hi / 16), hi), "hi": hi, "keep": keep, "sinks": sinks, "recent": recent, "spread": spread}
     reqs = log(1, 256)
     hi = log(64, max(64, min(1 << 20, BLOCK * MOST_PAIRS // (reqs * q))))
+    sinks, recent = rng.randrange(0, 4), rng.randrange(1, 4)
     return {"op": op, "scores": rng.choice(["fp32", "bf16"]), "q": q, "reqs": reqs, "lo": log(max(q, hi / 16), hi), "hi": hi,
             "keep": max(sinks + recent, log(1, 256)), "sinks": sinks, "recent": recent, "spread": spread}
 
@@ -218,55 +208,13 @@ def prepare(case, seed):
         s["table"], s["lens"] = torch.empty((rows, case["keep"]), dtype=torch.int32, device=dev), torch.empty(rows, dtype=torch.int32, device=dev)
         return s
     H = case["heads"]
-    s["q_pos"] = (s["seq_lens"][:, None] - q + torch.arange(q, device=dev)[None, :]).to(torch.int32).reshape(-1).contiguous()
-    s["softmax_scale"] = (D_NOPE + D_R) ** -0.5
-    if case["op"] == "sparse":
-        return _topics(s, lens, pool, g)
     # means of a block's rows keep what its tokens share: less than unit variance, and queries that tell blocks apart
     s["means"] = (0.4 * torch.randn((pool, ROW), generator=g, device=dev)).to(torch.bfloat16)
     s["q"] = (2.5 * torch.randn((rows, H, D_NOPE + D_R), generator=g, device=dev)).to(torch.bfloat16)
     s["kv_b_proj"] = (torch.randn((D_C, H * (D_NOPE + D_V)), generator=g, device=dev) / math.sqrt(D_C)).to(torch.bfloat16)
+    s["q_pos"] = (s["seq_lens"][:, None] - q + torch.arange(q, device=dev)[None, :]).to(torch.int32).reshape(-1).contiguous()
     s["out"] = torch.empty((rows, width), dtype=torch.bfloat16, device=dev)
-    return s
-
-
-def _topics(s, lens, pool, g):
-    """The rest of a sparse case's state: each request asks for a topic that some of its blocks are about, as many as can be chosen, and the others are not."""
-    case, dev = s["case"], s["seq_lens"].device
-    H, q, B = case["heads"], case["q"], len(lens)
-    rows, want = B * q, case["keep"] - case["sinks"] - case["recent"]
-    w = torch.randn((D_C, H * (D_NOPE + D_V)), generator=g, device=dev) / math.sqrt(D_C)
-    s["kv_b_proj"] = w.to(torch.bfloat16)
-    topic = torch.randn((B, D_C), generator=g, device=dev)
-    ask = torch.einsum("bc,chd->bhd", topic, w[:, :H * D_NOPE].reshape(D_C, H, D_NOPE))
-    s["q"] = torch.randn((rows, H, D_NOPE + D_R), generator=g, device=dev)
-    s["q"][..., :D_NOPE] += 0.5 * ask.repeat_interleave(q, 0)
-    s["q"] = s["q"].to(torch.bfloat16)
-    # the blocks between the first and the recent ones of every query of the request, where there is a choice
-    own = torch.tensor([[(n - q) // BLOCK, (n - 1) // BLOCK] for n in lens], device=dev)
-    end = torch.where(own[:, 0] + 1 > case["keep"], own[:, 0], own[:, 1]) + 1 - case["recent"]
-    j = torch.arange(s["block_table"].shape[1], device=dev)
-    free = (j >= case["sinks"]) & (j < end[:, None])
-    rank = torch.rand(free.shape, generator=g, device=dev).masked_fill_(~free, 2.0).argsort(1).argsort(1)
-    about = torch.zeros(pool, dtype=torch.int64, device=dev)     # 0: no topic, else 1 + the request
-    hit = free & (rank < want)
-    about[s["block_table"][hit].long()] = 1 + hit.nonzero()[:, 0]
-    topics = torch.cat((torch.zeros((1, D_C), device=dev), topic))
-    fp8 = case["kv"] == "fp8"
-    s["kv_scale"] = 5.5 / 448.0 if fp8 else 1.0
-    s["kv_cache"] = torch.empty((pool, BLOCK, D_C + 2 * D_R), dtype=torch.uint8, device=dev) if fp8 else torch.empty((pool, BLOCK, ROW), dtype=torch.bfloat16, device=dev)
-    s["means"] = torch.empty((pool, ROW), dtype=torch.bfloat16, device=dev)
-    for a in range(0, pool, 4096):
-        part = s["kv_cache"][a:a + 4096]
-        x = torch.randn(part.shape[:2] + (ROW,), generator=g, device=dev)
-        x[..., :D_C] += topics[about[a:a + 4096]][:, None]
-        if fp8:
-            part[..., :D_C] = (x[..., :D_C] / s["kv_scale"]).clamp_(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
-            part[..., D_C:] = x[..., D_C:].to(torch.bfloat16).view(torch.uint8)
-        else:
-            part.copy_(x)
-        s["means"][a:a + 4096] = _values(case, part, s["kv_scale"]).mean(1)
-    s["out"] = torch.empty((rows, H, D_V), dtype=torch.bfloat16, device=dev)
+    s["softmax_scale"] = (D_NOPE + D_R) ** -0.5
     return s
 
 
@@ -330,10 +278,11 @@ def _plain_tables(s, lens, cu, slots):
     return _tables_outputs(s, slots)
 
 
-def _values(case, rows, scale):
-    if case["kv"] == "bf16":
-        return rows.float()
-    return torch.cat((rows[..., :D_C].view(torch.float8_e4m3fn).float() * scale, rows[..., D_C:].view(torch.bfloat16).float()), -1)
+def _rows(s, blocks):
+    c = s["kv_cache"][blocks]
+    if s["case"]["kv"] == "bf16":
+        return c.float()
+    return torch.cat((c[..., :D_C].view(torch.float8_e4m3fn).float() * s["kv_scale"], c[..., D_C:].view(torch.bfloat16).float()), -1)
 
 
 def _filled(s):
@@ -352,38 +301,32 @@ def _filled(s):
 
 def _plain_means(s):
     blocks, n = _filled(s), s["means"].shape[0]
-    mean = _values(s["case"], s["kv_cache"][blocks.clamp_max(n - 1)], s["kv_scale"]).sum(1) / BLOCK
+    mean = _rows(s, blocks.clamp_max(n - 1)).sum(1) / BLOCK
     more = torch.cat((s["means"], s["means"][:1]))     # one place more for what is not written
     more[blocks] = mean.to(torch.bfloat16)
     s["means"].copy_(more[:n])
     return {"means": s["means"]}
 
 
-def _latent_queries(s):
-    """[request][query and head][576]: the queries as the cached rows meet them."""
+def _plain_scores(s):
     H, q, B = s["case"]["heads"], s["case"]["q"], s["seq_lens"].shape[0]
+    m = s["means"][s["block_table"].long().clamp_min(0)].float()
     x = s["q"].float().reshape(B, q, H, -1)
     w = s["kv_b_proj"][:, :H * D_NOPE].float().reshape(D_C, H, D_NOPE)
     lat = torch.einsum("bqhd,chd->bqhc", x[..., :D_NOPE], w)
     rot = _turn(x[..., D_NOPE:], _angles(s["q_pos"].reshape(B, q, 1)))
-    return torch.cat((lat, rot), -1).reshape(B, q * H, ROW)
-
-
-def _plain_scores(s, x):
-    H, rows = s["case"]["heads"], s["q"].shape[0]
-    m = s["means"][s["block_table"].long().clamp_min(0)].float()
-    score = (x @ m.transpose(1, 2) * s["softmax_scale"]).reshape(rows, H, -1)
+    score = (torch.cat((lat, rot), -1).reshape(B, q * H, ROW) @ m.transpose(1, 2) * s["softmax_scale"]).reshape(B * q, H, -1)
     seen = _seen(s)
     score = score.masked_fill(~seen[:, None], float("-inf"))
     top = score.amax(-1, keepdim=True)
     p = torch.exp(score - torch.where(top == float("-inf"), torch.zeros_like(top), top))
     share = (p / p.sum(-1, keepdim=True).clamp_min(1e-30)).sum(1) / H
-    return share.masked_fill(~seen, float("-inf"))
+    s["out"].copy_(share.masked_fill(~seen, float("-inf")))
+    return {"scores": s["out"]}
 
 
-def _plain_select(s, scores):
-    """(block table, length) of the chosen blocks of every query."""
-    case = s["case"]
+def _plain_select(s):
+    case, scores = s["case"], s["scores"].float()
     mine, width = _own_block(s), s["block_table"].shape[1]
     j = torch.arange(width, device=scores.device)
     always = (j < case["sinks"]) | (j > mine[:, None] - case["recent"])
@@ -396,34 +339,9 @@ def _plain_select(s, scores):
     req = torch.arange(scores.shape[0], device=scores.device) // case["q"]
     table = s["block_table"][req[:, None], blocks.clamp_max(width - 1)]
     t = s["seq_lens"].long()[req] - case["q"] + torch.arange(scores.shape[0], device=scores.device) % case["q"]
-    return torch.where(i < n[:, None], table, -1), torch.where(n > 0, (n - 1) * BLOCK + t % BLOCK + 1, 0)
-
-
-def _plain_sparse(s):
-    case, rows = s["case"], s["q"].shape[0]
-    H = case["heads"]
-    x = _latent_queries(s)
-    table, lens = _plain_select(s, _plain_scores(s, x))
-    kv = _values(case, s["kv_cache"][table.long().clamp_min(0)], s["kv_scale"]).reshape(rows, -1, ROW)
-    live = torch.arange(kv.shape[1], device=kv.device) < lens[:, None]
-    kv = torch.where(live[..., None], kv, torch.zeros((), device=kv.device))
-    score = (x.reshape(rows, H, ROW) @ kv.transpose(1, 2) * s["softmax_scale"]).masked_fill(~live[:, None], float("-inf"))
-    p = torch.exp(score - score.amax(-1, keepdim=True))
-    o = (p @ kv[..., :D_C]) / p.sum(-1, keepdim=True)
-    s["out"].copy_(torch.einsum("xhc,chd->xhd", o, s["kv_b_proj"][:, H * D_NOPE:].float().reshape(D_C, H, D_V)))
-    return {"out": s["out"]}
-
-
-def _plain(s):
-    op = s["case"]["op"]
-    if op == "means":
-        return _plain_means(s)
-    if op == "scores":
-        return {"scores": s["out"].copy_(_plain_scores(s, _latent_queries(s)))}
-    if op == "sparse":
-        return _plain_sparse(s)
-    table, lens = _plain_select(s, s["scores"].float())
-    return {"table": s["table"].copy_(table), "lens": s["lens"].copy_(lens)}
+    s["table"].copy_(torch.where(i < n[:, None], table, -1))
+    s["lens"].copy_(torch.where(n > 0, (n - 1) * BLOCK + t % BLOCK + 1, 0))
+    return {"table": s["table"], "lens": s["lens"]}
 
 
 def run(state):
@@ -432,7 +350,7 @@ def run(state):
         lens, cu, slots = s["steps"][s["turn"]]
         s["turn"] ^= 1
     if not own:
-        return _plain_tables(s, lens, cu, slots) if op == "tables" else _plain(s)
+        return _plain_tables(s, lens, cu, slots) if op == "tables" else {"means": _plain_means, "scores": _plain_scores, "select": _plain_select}[op](s)
     from mla_prefix_cache_gb300 import api
     if op == "tables":
         api.assign_blocks(s["block_table"], s["held"], lens, s["free_blocks"], s["free_count"], shared=s["shared"], cu_q=cu, slots=slots)
@@ -446,13 +364,6 @@ def run(state):
         return {"scores": api.block_scores(s["q"], s["q_pos"], s["means"], s["block_table"], s["seq_lens"], s["kv_b_proj"], softmax_scale=s["softmax_scale"],
                                            rope_theta=THETA, out=s["out"], workspace=s["workspace"])}
     case = s["case"]
-    if op == "sparse":
-        if "workspace" not in s:
-            n = api.decode_sparse_workspace_size(s["seq_lens"].shape[0], s["q"].shape[0], s["q"].shape[1], s["block_table"].shape[1], case["keep"])
-            s["workspace"] = torch.empty(n, dtype=torch.uint8, device=s["q"].device)
-        return {"out": api.decode_sparse(s["q"], s["q_pos"], s["kv_cache"], s["means"], s["block_table"], s["seq_lens"], s["kv_b_proj"], keep=case["keep"],
-                                         sinks=case["sinks"], recent=case["recent"], softmax_scale=s["softmax_scale"], rope_theta=THETA,
-                                         kv_scale=s["kv_scale"], out=s["out"], workspace=s["workspace"])}
     table, lens = api.select_blocks(s["scores"], s["block_table"], s["seq_lens"], keep=case["keep"], sinks=case["sinks"], recent=case["recent"],
                                     table=s["table"], lens=s["lens"])
     return {"table": table, "lens": lens}
@@ -475,13 +386,6 @@ def work(case):
         kept = sum(min(case["keep"], x + 1) for r in seen for x in r)
         return {"bytes": pairs * (4 if case["scores"] == "fp32" else 2) + 4 * rows * (case["keep"] + 1) + 4 * kept, "flops": 0}
     H = case["heads"]
-    if case["op"] == "sparse":
-        attended = sum(min(case["keep"] * BLOCK - BLOCK + (n - q + i) % BLOCK + 1, n - q + i + 1) for n in lens for i in range(q))
-        # of the chosen blocks, those of one query count: its neighbours' may be the same
-        keys = sum(min(case["keep"] * BLOCK, n) for n in lens)
-        return {"bytes": sum(max(r) for r in seen) * (2 * ROW + 4) + keys * (2 * ROW if case["kv"] == "bf16" else D_C + 2 * D_R) +
-                2 * D_C * H * (D_NOPE + D_V) + rows * 2 * H * (D_NOPE + D_R + D_V),
-                "flops": 2 * ROW * H * pairs + 2 * (ROW + D_C) * H * attended + 2 * D_C * (D_NOPE + D_V) * H * rows}
     return {"bytes": sum(max(r) for r in seen) * (2 * ROW + 4) + 2 * D_C * H * D_NOPE + rows * (2 * H * (D_NOPE + D_R) + 2 * width),
             "flops": 2 * ROW * H * pairs + 2 * D_C * D_NOPE * H * rows}
 
@@ -503,32 +407,18 @@ def exact(case, seed):
                     mean[b] = x.to(f).mean(0)
         return {"means": mean}
     H, q = case["heads"], case["q"]
-    w = s["kv_b_proj"].to(f).reshape(D_C, 2, H, D_NOPE)
-    shares = torch.full((len(lens) * q, s["block_table"].shape[1]), float("-inf"), dtype=f, device=w.device)
-    out = []
+    w = s["kv_b_proj"][:, :H * D_NOPE].to(f).reshape(D_C, H, D_NOPE)
+    out = torch.full((len(lens) * q, s["block_table"].shape[1]), float("-inf"), dtype=f, device=w.device)
     k = torch.arange(D_R // 2, device=w.device, dtype=f)
     for r, n in enumerate(lens):
         for i in range(q):
-            b, x, pos = (n - q + i) // BLOCK, s["q"][r * q + i].to(f), int(s["q_pos"][r * q + i])
+            b = (n - q + i) // BLOCK
+            if b < 1:
+                continue
             m = s["means"][s["block_table"][r, :b].long()].to(f)
+            x, pos = s["q"][r * q + i].to(f), int(s["q_pos"][r * q + i])
             z = torch.polar(torch.ones((), dtype=f, device=w.device), pos * torch.exp(-2 * k / D_R * math.log(THETA)))
             rot = torch.view_as_real(torch.view_as_complex(x[:, D_NOPE:].reshape(H, -1, 2).contiguous()) * z).flatten(1)
-            lat = torch.einsum("hd,chd->hc", x[:, :D_NOPE], w[:, 0])
-            share = torch.softmax(s["softmax_scale"] * (lat @ m[:, :D_C].T + rot @ m[:, D_C:].T), 1).mean(0)
-            shares[r * q + i, :b] = share
-            if case["op"] == "scores":
-                continue
-            blocks = list(range(b + 1))
-            if b + 1 > case["keep"]:
-                rest = blocks[case["sinks"]:b + 1 - case["recent"]]
-                value = share.tolist()
-                best = sorted(rest, key=lambda j: (-value[j], j))[:case["keep"] - case["sinks"] - case["recent"]]
-                blocks = blocks[:case["sinks"]] + sorted(best) + blocks[b + 1 - case["recent"]:]
-            c = s["kv_cache"][s["block_table"][r, torch.tensor(blocks, device=w.device)].long()].flatten(0, 1)[:len(blocks) * BLOCK - BLOCK + (n - q + i) % BLOCK + 1]
-            if case["kv"] == "bf16":
-                c, kr = c[:, :D_C].to(f), c[:, D_C:].to(f)
-            else:
-                c, kr = c[:, :D_C].view(torch.float8_e4m3fn).to(f) * s["kv_scale"], c[:, D_C:].view(torch.bfloat16).to(f)
-            a = torch.softmax(s["softmax_scale"] * (lat @ c.T + rot @ kr.T), 1)
-            out.append(torch.einsum("hc,chd->hd", a @ c, w[:, 1]))
-    return {"out": torch.stack(out)} if case["op"] == "sparse" else {"scores": shares}
+            lat = torch.einsum("hd,chd->hc", x[:, :D_NOPE], w)
+            out[r * q + i, :b] = torch.softmax(s["softmax_scale"] * (lat @ m[:, :D_C].T + rot @ m[:, D_C:].T), 1).mean(0)
+    return {"scores": out}
