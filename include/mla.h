@@ -582,6 +582,10 @@ int mla_decode(const void* q, const int32_t* q_pos, const void* kv_cache, int kv
  *  - Then entries [held[r], need) are popped from the stack, in the order of
  *    requests and entries.  A request is served if the entries asked for by
  *    the requests up to and with it are there; the others keep what they hold.
+ *    One that is served while it holds less than its shared blocks (it was cut
+ *    back below its prefix) has its own blocks from held[r] on: shared[r] becomes
+ *    held[r], as it was before the call.  To put it behind a prefix again, write
+ *    the prefix's entries, held[r] and shared[r].
  *  - held and free_count are updated.  Stack places that a call does not push
  *    to are not written.
  *  - slots[row], for row i of the n_r rows of request r: 64 block + t % 64 of
@@ -590,7 +594,7 @@ int mla_decode(const void* q, const int32_t* q_pos, const void* kv_cache, int kv
  *  block_table   device int32 [num_reqs][max_blocks_per_req].
  *  held          device int32 [num_reqs].
  *  seq_lens      device int32 [num_reqs]; negative counts as 0.
- *  shared        device int32 [num_reqs], or NULL (0).
+ *  shared        device int32 [num_reqs], or NULL (0); lowered as above.
  *  free_blocks   device int32 [capacity];  free_count  device int32 [1].
  *  cu_q          as mla_cache_append (rows = 0: not read).
  *  slots         device int64 [rows]; rows = 0: none wanted.
@@ -599,12 +603,12 @@ int mla_decode(const void* q, const int32_t* q_pos, const void* kv_cache, int kv
  *                free_count out of range (cut to it) and a stack that would
  *                outgrow its capacity (what lies behind it is lost), bit 2 for a
  *                request that is not served.
- * Table, held, stack and count must not overlap; calls that share any of them
+ * Table, held, shared, stack and count must not overlap; calls that share any of them
  * must be ordered (one stream, or events).  Errors: MLA_ERR_INVALID_ARG,
  * MLA_ERR_UNSUPPORTED (more than 8192 requests, tables and stack of 2^31 entries
  * or more), MLA_ERR_CUDA. */
 int mla_assign_blocks(int32_t* block_table, int max_blocks_per_req, int32_t* held, const int32_t* seq_lens,
-                      const int32_t* shared, int num_reqs, int32_t* free_blocks, int capacity, int32_t* free_count,
+                      int32_t* shared, int num_reqs, int32_t* free_blocks, int capacity, int32_t* free_count,
                       const int32_t* cu_q, int rows, int64_t* slots, uint32_t* dev_error, mla_stream_t stream);
 
 /* mla_block_means -- means[b] = the mean of the 64 rows [c_kv | k_rope] of

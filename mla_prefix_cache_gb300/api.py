@@ -511,7 +511,8 @@ def assign_blocks(block_table: torch.Tensor, held: torch.Tensor, seq_lens: torch
     block_table int32 [B, max_blocks]; held int32 [B], the blocks of each table
     row in use; seq_lens int32 [B], the tokens to hold; free_blocks int32
     [capacity] with free_count int32 [1], a stack; shared int32 [B], leading
-    blocks that are not given back.  slots int64 [rows]: filled with the cache
+    blocks that are not given back (lowered to held where a request grows from
+    fewer, as those it gets are its own).  slots int64 [rows]: filled with the cache
     slot of every new row (cu_q int32 [B+1] as for cache_append).  Returns
     slots."""
     device, i32 = _current(block_table, "block_table"), torch.int32

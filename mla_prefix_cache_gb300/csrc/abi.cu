@@ -2111,7 +2111,7 @@ int mla_decode(const void* q, const int32_t* q_pos, const void* kv_cache, int kv
 // ------------------------------------------------------------ a sparse decoding step
 
 int mla_assign_blocks(int32_t* block_table, int max_blocks_per_req, int32_t* held, const int32_t* seq_lens,
-                      const int32_t* shared, int num_reqs, int32_t* free_blocks, int capacity, int32_t* free_count,
+                      int32_t* shared, int num_reqs, int32_t* free_blocks, int capacity, int32_t* free_count,
                       const int32_t* cu_q, int rows, int64_t* slots, uint32_t* dev_error, mla_stream_t stream) {
   if (num_reqs < 0 || rows < 0 || capacity < 0) return MLA_ERR_INVALID_ARG;
   if (num_reqs == 0 && rows == 0) return MLA_OK;

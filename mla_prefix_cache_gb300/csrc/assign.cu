@@ -2,6 +2,7 @@
 // 64) and held blocks so far, request r
 //   gives back  j in [max(need, shared), held)   (shared ones only leave the table)
 //   asks for    j in [held, need)
+// (where held < shared, what it gets below shared is its own: shared becomes held)
 // and both, over all requests in (r, j) order, are one run on the stack of free
 // blocks of height n: entry e of the R given back goes to place n + R - 1 - e,
 // then entry e of those taken comes from place n + R - 1 - e.  So what is given
@@ -53,12 +54,15 @@ __global__ void __launch_bounds__(kThreads, 1) assign_blocks_kernel(const __grid
   auto need = [&](const Req& q) { return q.len > p.max_blocks * kBlock ? p.max_blocks : (q.len + kBlock - 1) / kBlock; };
   int back = 0, more = 0;
   bool bad = false;
+  uint32_t below = 0;    // bit r - r0: it holds less than its shared blocks
+  static_assert(kMaxAssignReqs <= 32 * kThreads, "a bit a request of a thread");
   for (int r = r0; r < r1; ++r) {
-    const int h = __ldcg(p.held + r), sh = p.shared == nullptr ? 0 : __ldg(p.shared + r);
+    const int h = __ldcg(p.held + r), sh = p.shared == nullptr ? 0 : __ldcg(p.shared + r);      // (an earlier call may have written both)
     Req q;
     q.len = max(__ldg(p.batch.seq_lens + r), 0);
     q.held = min(max(h, 0), p.max_blocks);
     q.from = max(need(q), min(sh, q.held));
+    below |= sh > q.held ? 1u << (r - r0) : 0u;
     q.back = back;
     q.more = more;
     bad |= q.len > p.max_blocks * kBlock || h != q.held;
@@ -152,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, 1) assign_blocks_kernel(const __grid
       const Req q = req[k];
       for (int j = need(q) + lane; j < min(q.from, q.held); j += 32) p.table[(int64_t)k * p.max_blocks + j] = -1;
     }
-  cluster_sync_all();      // pushed before it is popped; everyone has read held and free_count
+  cluster_sync_all();      // pushed before it is popped; everyone has read held, shared and free_count
 
   // ---- blocks taken
   auto popped = [&](int k) { return __ldcg(p.free_blocks + top - 1 - k); };      // k < served <= top
@@ -161,6 +165,9 @@ __global__ void __launch_bounds__(kThreads, 1) assign_blocks_kernel(const __grid
   });
   auto kept = [&](const Req& q) { return need(q) <= q.held || q.more + (need(q) - q.held) <= top ? need(q) : q.held; };
   for (int k = first; k < B; k += step) p.held[k] = kept(req[k]);
+  if (below != 0 && rank == 0)      // blocks popped below the shared ones are given back like the others
+    for (int r = r0; r < r1; ++r)
+      if ((below >> (r - r0) & 1) && kept(req[r]) > req[r].held) p.shared[r] = req[r].held;
   if (first == 0) *p.free_count = top - served;
 
   // ---- slots of the new rows

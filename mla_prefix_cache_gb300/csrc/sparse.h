@@ -15,7 +15,7 @@ struct AssignParams {
   int32_t* table;            // [num_reqs][max_blocks]
   int max_blocks;
   int32_t* held;             // [num_reqs]
-  const int32_t* shared;     // optional [num_reqs]
+  int32_t* shared;           // optional [num_reqs]
   int32_t* free_blocks;      // [capacity]
   int capacity;
   int32_t* free_count;

@@ -350,6 +350,84 @@ def test_assign_reports_bad_state(api):
     assert torch.equal(d.stack, guard) and d.held.tolist() == [4, 0]
 
 
+class Prefixed:
+    """Requests behind a common prefix of `sh` blocks, of which a pool of others is to be whole at any time.  The mirror of shared[] follows the rule
+    that a request which grows from fewer blocks than its shared ones owns what it gets."""
+
+    def __init__(self, B, sh, width, pool, seed=0):
+        rng = np.random.Generator(np.random.PCG64(seed))
+        self.B, self.sh, self.width, self.pool = B, sh, width, pool
+        table = np.full((B, width), -1, dtype=np.int32)
+        table[:, :sh] = pool + np.arange(sh)
+        self.table, self.held, self.shared = i32(table), i32([sh] * B), i32([sh] * B)
+        self.stack, self.count, self.lens = i32(rng.permutation(pool)), i32([pool]), i32([64 * sh] * B)
+        self.err, self.slots = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.full((2 * B,), -9, dtype=torch.int64, device="cuda")
+        self.mirror = np.full(B, sh)
+
+    def call(self, api):
+        api.assign_blocks(self.table, self.held, self.lens, self.stack, self.count, shared=self.shared, slots=self.slots, dev_error=self.err)
+
+    def step(self, lens, call):
+        before = self.held.cpu().numpy()
+        self.lens.copy_(i32(lens))
+        torch.cuda.synchronize()
+        call()
+        torch.cuda.synchronize()
+        table, held, count, slots = self.table.cpu().numpy(), self.held.cpu().numpy(), int(self.count.item()), self.slots.cpu().numpy()
+        stack = self.stack.cpu().numpy()[:count]
+        mine = table[(table >= 0) & (table < self.pool)]
+        assert np.array_equal(np.sort(np.concatenate([stack, mine])), np.arange(self.pool)), "a block is lost or there twice"
+        self.mirror = np.where((held > before) & (self.mirror > before), before, self.mirror)
+        assert np.array_equal(self.shared.cpu().numpy(), self.mirror)
+        for r in range(self.B):
+            assert (table[r, :held[r]] >= 0).all() and (table[r, held[r]:] == -1).all()
+            for i in range(2):
+                t = lens[r] - 2 + i
+                assert slots[2 * r + i] == (table[r, t // 64] * 64 + t % 64 if 0 <= t < 64 * held[r] else -1)
+        served = [min(-(-n // 64), self.width) == h for n, h in zip(lens, held)]
+        assert int(self.err.item()) == (0 if all(served) else 4)
+        self.err.zero_()
+
+
+@gpu
+def test_assign_below_a_shared_prefix_loses_no_block(api):
+    """Cut below the prefix, grown again and retired, with shared[] left alone: what was popped below the prefix comes back."""
+    t = Prefixed(3, 4, 9, 20)
+    for lens in ([6 * 64, 5 * 64 - 3, 300], [2 * 64, 0, 4 * 64], [7 * 64, 3 * 64, 1], [0, 0, 0], [64, 512, 9 * 64], [0, 0, 0]):
+        t.step(lens, lambda: t.call(api))
+    assert t.count.item() == 20 and t.shared.tolist() == [0, 0, 0]
+
+
+@gpu
+@pytest.mark.parametrize("B, pool", [(5, 200), (5, 24), (40, 150), (1500, 9000)])
+def test_assign_below_a_shared_prefix_in_a_replayed_graph(api, B, pool):
+    """The same over random lengths, one captured call replayed, with requests put behind the prefix again and a pool that runs out."""
+    t = Prefixed(B, 3, 12, pool, seed=B)
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        t.call(api)                    # nothing changes hands
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            t.call(api)
+
+    def replay():
+        with torch.cuda.stream(stream):
+            graph.replay()
+    rng = np.random.Generator(np.random.PCG64(pool))
+    for k in range(25):
+        t.step([int(n) for n in np.where(rng.random(B) < 0.3, 0, rng.integers(0, 64 * 12 + 1, B))], replay)
+        if k % 5 == 4:                 # everyone ends, half of them begin again behind the prefix
+            t.step([0] * B, replay)
+            t.table[::2, :3] = i32(pool + np.arange(3))
+            t.held[::2] = 3
+            t.shared[::2] = 3
+            t.mirror[::2] = 3
+    t.step([0] * B, replay)
+    assert t.count.item() == pool
+
+
 @gpu
 def test_assign_refusals(api):
     t = Tables(2, 4, 6)
