@@ -622,7 +622,8 @@ int mla_assign_blocks(int32_t* block_table, int max_blocks_per_req, int32_t* hel
  *  means         device bf16 [num_blocks][576], 16-byte aligned.
  *  rows          all new rows; cu_q, seq_lens as mla_cache_append.
  *  dev_error     device uint32, optional: bit 0 is set for a block id outside
- *                [0, num_blocks) or a block behind the table (no mean is made).
+ *                [0, num_blocks) or a block behind the table (no mean is made),
+ *                bit 1 for a wait inside the kernel that ran out.
  * Errors: MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED, MLA_ERR_CUDA. */
 int mla_block_means(const void* kv_cache, int kv_dtype, float kv_scale, int num_blocks, const int32_t* block_table,
                     int max_blocks_per_req, const int32_t* seq_lens, const int32_t* cu_q, int num_reqs, int rows,

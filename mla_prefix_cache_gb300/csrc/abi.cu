@@ -2158,6 +2158,8 @@ int mla_block_means(const void* kv_cache, int kv_dtype, float kv_scale, int num_
   p.max_blocks = max_blocks_per_req;
   p.means = static_cast<uint16_t*>(means);
   p.err = dev_error;
+  p.wait_limit_ns = wait_limit_ns();
+  p.withhold = env_int("MLA_TEST_WITHHOLD_MEANS", -1);
   return cuda_status(launch_block_means(p, kv_dtype == MLA_KV_FP8_E4M3, reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(RingShape<kFp8>::kAdders + 32, 1) block_means_
   }
   __syncthreads();
   auto await = [&](uint32_t bar, uint32_t parity) {
-    if (mbar_wait(bar, parity)) return true;
+    if (mbar_wait(bar, parity, p.wait_limit_ns)) return true;
     if (p.err != nullptr) atomicOr(p.err, kErrTimeout);
     return false;
   };
@@ -221,8 +221,8 @@ __global__ void __launch_bounds__(RingShape<kFp8>::kAdders + 32, 1) block_means_
       if (id == -2 && p.err != nullptr) atomicOr(p.err, kErrBadBlock);
       for (uint32_t rest = __ballot_sync(0xffffffffu, id >= 0); ok && rest; rest &= rest - 1, ++g) {
         const int next = __shfl_sync(0xffffffffu, id, __ffs(rest) - 1), s = g % M::kStages;
-        if (g >= M::kStages) ok = __all_sync(0xffffffffu, await(empty(s), (g / M::kStages - 1) & 1));
-        if (ok && lane == 0) {
+        if (g >= M::kStages && !(ok = __all_sync(0xffffffffu, await(empty(s), (g / M::kStages - 1) & 1)))) break;
+        if (lane == 0) {
           ids[s] = next;
           mbar_arrive_expect_tx(full(s), M::kBytes);
           bulk_load(sb + s * M::kBytes, p.cache + (int64_t)next * M::kBytes, M::kBytes, full(s));
@@ -231,17 +231,22 @@ __global__ void __launch_bounds__(RingShape<kFp8>::kAdders + 32, 1) block_means_
     }
     // the end: an id of -1 (on a wait that gave up the adders give up too)
     const int s = g % M::kStages;
-    if (ok && g >= M::kStages) ok = __all_sync(0xffffffffu, await(empty(s), (g / M::kStages - 1) & 1));
+    int v = max(0, g - M::kStages);      // loads before this one have landed
+    if (ok && g >= M::kStages) {
+      ok = __all_sync(0xffffffffu, await(empty(s), (g / M::kStages - 1) & 1));
+      v += ok;                           // its stage's barrier goes on to the end's phase
+    }
     if (ok && lane == 0) {
       ids[s] = -1;
       mbar_arrive(full(s));
     }
+    for (; v < g; ++v) await(full(v % M::kStages), (v / M::kStages) & 1);   // no copy is in flight when the CTA ends
   } else {
     // ---- adders
     grid_wait();
     grid_trigger();
     const int col = tid % M::kCols, group = tid / M::kCols;
-    for (int g = 0;; ++g) {
+    for (int g = 0; (int)blockIdx.x != p.withhold; ++g) {
       const int s = g % M::kStages;
       if (named_bar_or(1, M::kAdders, !await(full(s), (g / M::kStages) & 1))) break;      // (the sums of the block before have been read too)
       const int id = ids[s];

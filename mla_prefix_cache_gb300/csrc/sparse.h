@@ -34,6 +34,8 @@ struct MeansParams {
   int max_blocks;
   uint16_t* means;               // [num_blocks][576] bf16
   uint32_t* err;                 // optional
+  uint64_t wait_limit_ns;        // bound of every wait (a timeout sets kErrTimeout)
+  int withhold;                  // test hook: this CTA of the ring kernel adds nothing up, so its loads' wait for room runs out (-1: none)
 };
 cudaError_t launch_block_means(const MeansParams& p, bool fp8, cudaStream_t s);
 

@@ -564,6 +564,29 @@ def test_means_keep_what_is_not_finite_to_itself(api, value):
 
 
 @gpu
+@pytest.mark.parametrize("kv, blocks", [("bf16", 7), ("bf16", 3), ("bf16", 2), ("fp8_e4m3", 9)])
+@pytest.mark.parametrize("cta", [0, 151])
+def test_means_wait_runs_out_and_reports_timeout(api, monkeypatch, kv, blocks, cta):
+    """Failure detection without a fault: one CTA takes no block out of its ring (a test hook of the library), so that its loads' wait for room runs
+    out after the shortened limit.  It records the timeout, waits for the copies in flight and returns; the others' means are right, and so is
+    the next call.  (A ring with room left behind all its blocks waits for none, and reports nothing.)"""
+    n = 152 * blocks                                  # CTA c has the blocks c, c + 152, ...
+    c = means_case([64 * n], [64 * n], kv)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    monkeypatch.setenv("MLA_WAIT_LIMIT_US", "2000")
+    monkeypatch.setenv("MLA_TEST_WITHHOLD_MEANS", str(cta))
+    got = run_means(api, c, dev_error=err)
+    torch.cuda.synchronize()
+    assert err.item() == (2 if blocks >= (3 if kv == "bf16" else 5) else 0)
+    monkeypatch.delenv("MLA_TEST_WITHHOLD_MEANS")
+    monkeypatch.delenv("MLA_WAIT_LIMIT_US")
+    check_means(c, got, left={(0, j) for j in range(cta, n, 152)})
+    err.zero_()
+    check_means(c, run_means(api, c, dev_error=err))
+    assert err.item() == 0
+
+
+@gpu
 def test_means_refusals(api):
     cache = torch.zeros((4, 64, 576), dtype=torch.bfloat16, device="cuda")
     means = torch.zeros((4, 576), dtype=torch.bfloat16, device="cuda")
