@@ -685,6 +685,7 @@ int mla_select_blocks(const void* scores, int scores_dtype, const int32_t* block
  *                (without segments).  Rows of out and lse that no request has
  *                are not written.
  *  means         as mla_block_scores;  keep, sinks, recent  as mla_select_blocks.
+ *                A keep of more than max_blocks_per_req is the same as that many.
  *  workspace     device, 256-B aligned, mla_decode_sparse_workspace_size(...)
  *                bytes; holds the error word read by mla_get_device_error(),
  *                set as by mla_decode.  Calls that may overlap on the GPU must

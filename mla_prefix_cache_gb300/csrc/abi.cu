@@ -2303,6 +2303,7 @@ struct SparseLayout {
 };
 static bool sparse_layout(int total_q, int num_heads, int max_blocks, int keep, SparseLayout* d) {
   if (keep < 1 || keep > INT32_MAX / kBlock) return false;
+  keep = std::min(keep, max_blocks);
   if (!scores_layout(total_q, num_heads, max_blocks, &d->scores) || !decode_layout(total_q, total_q, num_heads, &d->decode)) return false;
   d->shares = d->scores.total;
   d->table = up256(d->shares + (size_t)total_q * max_blocks * 4);
@@ -2336,8 +2337,11 @@ int mla_decode_sparse(const void* q, const int32_t* q_pos, const void* kv_cache,
   if (means == nullptr || !aligned(means, 16)) return MLA_ERR_INVALID_ARG;
   SparseLayout d;
   if (!decode_cache_taken(kv_dtype, kv_scale, num_blocks) || !sparse_layout(total_q, num_heads, max_blocks_per_req, keep, &d) ||
-      !scores_work_taken(total_q, num_reqs, max_blocks_per_req) || !decode_work_taken(total_q, num_heads, total_q, keep, 0))
+      !scores_work_taken(total_q, num_reqs, max_blocks_per_req))
     return MLA_ERR_UNSUPPORTED;
+  // a query has no more blocks than its table: with keep at that, all are chosen, whatever sinks and recent are
+  keep = std::min(keep, max_blocks_per_req);
+  if (!decode_work_taken(total_q, num_heads, total_q, keep, 0)) return MLA_ERR_UNSUPPORTED;
   if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < d.total) return MLA_ERR_WORKSPACE;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);

@@ -265,6 +265,20 @@ def test_sparse_validates_without_gpu(lib):
     assert call(T=0, q=None) == _lib.MLA_OK
 
 
+def test_sparse_keep_beyond_the_table_without_gpu(lib):
+    """More kept blocks than a table has ask for no more room and refuse no more work than as many as it has."""
+    size = lib.mla_decode_sparse_workspace_size
+    most = (2 ** 31 - 1) // 64
+    for T, H, mb in ((5, 8, 300), (300, 128, 1), (4000, 16, 2000)):
+        assert size(2, T, H, mb, most) == size(2, T, H, mb, mb + 1) == size(2, T, H, mb, mb) > 0
+    d = ctypes.c_void_p(4096)
+
+    def call(T, keep, wb):      # sizes are taken up to the workspace's
+        return lib.mla_decode_sparse(d, d, d, 0, 1.0, 8, d, d, 300, d, d, 2, T, 128, keep, 1, 2, d, 0.07, 1e4, d, 0, None, d, wb, None)
+    for keep in (300, 301, most):
+        assert call(4000, keep, size(2, 4000, 128, 300, 300) - 1) == _lib.MLA_ERR_WORKSPACE
+
+
 def test_reference_tables_undo_themselves():
     t = Tables(3, 6, 12)
     t.assign([65, 0, 200])
@@ -1040,6 +1054,22 @@ def test_sparse_is_its_parts(api, kv):
     every = d["block_table"].repeat_interleave(2, 0).contiguous()
     want = api.decode(d["q"], d["q_pos"], d["kv_cache"], every, (d["q_pos"] + 1).contiguous(), d["kv_b_proj"], **a)
     assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+@gpu
+@pytest.mark.parametrize("kv", ["bf16", "fp8_e4m3"])
+@pytest.mark.parametrize("q", [1, 3])
+def test_sparse_keeps_every_block_of_a_narrow_table(api, kv, q):
+    """A keep above the table's width, with first and recent blocks above it too: bit for bit what the width gives."""
+    t = Topics(api, [3000, 64 * 40 + 1, 500, 64], q, 32, kv, 9, 1, 2)
+    d = t.dev()
+    width = d["block_table"].shape[1]
+    ws = torch.empty(api.decode_sparse_workspace_size(4, 4 * q, 32, width, width), dtype=torch.uint8, device="cuda")
+    want = [x.clone() for x in t.run(d, keep=width, workspace=ws)]
+    for kw in (dict(keep=width + 1), dict(keep=50 * width, sinks=2 * width, recent=3 * width), dict(keep=(2 ** 31 - 1) // 64)):
+        out, lse = t.run(d, workspace=ws, **kw)
+        assert api.device_error(ws) == 0
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
 
 
 @gpu
