@@ -605,8 +605,8 @@ int mla_decode(const void* q, const int32_t* q_pos, const void* kv_cache, int kv
  *                request that is not served.
  * Table, held, shared, stack and count must not overlap; calls that share any of them
  * must be ordered (one stream, or events).  Errors: MLA_ERR_INVALID_ARG,
- * MLA_ERR_UNSUPPORTED (more than 8192 requests, tables and stack of 2^31 entries
- * or more), MLA_ERR_CUDA. */
+ * MLA_ERR_UNSUPPORTED (more than 8192 requests; num_reqs * max_blocks_per_req +
+ * capacity, or rows, of 2^31 - 2^20 or more), MLA_ERR_CUDA. */
 int mla_assign_blocks(int32_t* block_table, int max_blocks_per_req, int32_t* held, const int32_t* seq_lens,
                       int32_t* shared, int num_reqs, int32_t* free_blocks, int capacity, int32_t* free_count,
                       const int32_t* cu_q, int rows, int64_t* slots, uint32_t* dev_error, mla_stream_t stream);
@@ -648,7 +648,7 @@ int mla_block_means(const void* kv_cache, int kv_dtype, float kv_scale, int num_
  *                mla_decode (a cu_q that does not ascend: every column is -inf).
  *                Calls that may overlap on the GPU must not share it.
  * Errors: MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED (H > 128, total_q > 65535,
- * total_q * H of 2^30 or more, 2^31 or more pairs of a query and 128 blocks),
+ * (total_q + num_reqs) * ceil(max_blocks_per_req / 64) of 2^31 or more),
  * MLA_ERR_WORKSPACE, MLA_ERR_CUDA. */
 size_t mla_block_scores_workspace_size(int total_q, int num_heads, int max_blocks_per_req);
 
@@ -673,7 +673,8 @@ int mla_block_scores(const void* q, const int32_t* q_pos, const void* means, int
  *  keep          at least sinks + recent; sinks >= 0, recent >= 1.
  *  dev_error     device uint32, optional: bit 0 is set for a sequence longer
  *                than its table (cut off there).
- * Errors: MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED, MLA_ERR_CUDA. */
+ * Errors: MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED (keep of 2^25 or more),
+ * MLA_ERR_CUDA. */
 int mla_select_blocks(const void* scores, int scores_dtype, const int32_t* block_table, int max_blocks_per_req,
                       const int32_t* seq_lens, const int32_t* cu_q, int num_reqs, int total_q, int keep, int sinks,
                       int recent, int32_t* table, int32_t* lens, uint32_t* dev_error, mla_stream_t stream);
@@ -690,7 +691,10 @@ int mla_select_blocks(const void* scores, int scores_dtype, const int32_t* block
  *                bytes; holds the error word read by mla_get_device_error(),
  *                set as by mla_decode.  Calls that may overlap on the GPU must
  *                not share it.
- * Errors: those of the three. */
+ * Errors: MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED (as mla_block_scores; keep of
+ * 2^25 or more; a kv_scale outside the range of mla_decode, a cache of 2^31 tokens
+ * or more; with k = min(keep, max_blocks_per_req), total_q * (H / 128 + 1) *
+ * (k / 2 + 5) of 2^31 or more), MLA_ERR_WORKSPACE, MLA_ERR_CUDA. */
 size_t mla_decode_sparse_workspace_size(int num_reqs, int total_q, int num_heads, int max_blocks_per_req, int keep);
 
 int mla_decode_sparse(const void* q, const int32_t* q_pos, const void* kv_cache, int kv_dtype, float kv_scale,

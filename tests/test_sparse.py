@@ -279,6 +279,32 @@ def test_sparse_keep_beyond_the_table_without_gpu(lib):
         assert call(4000, keep, size(2, 4000, 128, 300, 300) - 1) == _lib.MLA_ERR_WORKSPACE
 
 
+def test_documented_limits_without_gpu(lib):
+    """The sizes that mla.h names as the first that a call refuses, and the last before them (which then miss a workspace)."""
+    d, most = ctypes.c_void_p(4096), 2 ** 25 - 1
+    taken, refused = _lib.MLA_ERR_WORKSPACE, _lib.MLA_ERR_UNSUPPORTED
+
+    def scores(T, B, mb):
+        return lib.mla_block_scores(d, d, d, 8, d, mb, d, d, B, T, 8, d, 0.07, 1e4, d, 0, None, 0, None)
+    assert scores(2048, 2047, most) == taken and scores(2048, 2048, most) == refused          # 2^12 rows and requests, 2^19 tiles
+    assert scores(65535, 2 ** 25 - 65536, 64 * 64) == taken and scores(65535, 2 ** 25 - 65535, 64 * 64) == refused
+    assert scores(65535, 1, 64) == taken and scores(65536, 1, 64) == refused
+
+    def sparse(T, keep, mb, H=128, nb=8):
+        return lib.mla_decode_sparse(d, d, d, 0, 1.0, nb, d, d, mb, d, d, 1, T, H, keep, 1, 2, d, 0.07, 1e4, d, 0, None, None, 0, None)
+    # 2 * 2048 * (k / 2 + 5) reaches 2^31 at k = 2^20 - 10
+    assert sparse(2048, 2 ** 20 - 11, 2 ** 21) == taken and sparse(2048, 2 ** 20 - 10, 2 ** 21) == refused
+    assert sparse(2048, most, 2 ** 20 - 11) == taken and sparse(2048, most, 2 ** 20 - 10) == refused
+    assert sparse(1, most, 64) == taken and sparse(1, most + 1, 64) == refused
+    assert sparse(1, 4, 64, nb=most) == taken and sparse(1, 4, 64, nb=most + 1) == refused
+    assert lib.mla_select_blocks(d, 0, d, 64, d, d, 1, 1, most + 1, 1, 2, d, d, None, None) == refused
+
+    def assign(B, mb, cap, rows=0):
+        return lib.mla_assign_blocks(d, mb, d, d, None, B, d, cap, d, d, rows, d, None, None)
+    assert assign(8193, 1, 1) == refused and assign(64, most, 64) == refused
+    assert assign(32, 2 ** 25 - 1, 2 ** 30 - 2 ** 20 + 32) == refused and assign(1, 1, 1, rows=2 ** 31 - 2 ** 20) == refused
+
+
 def test_reference_tables_undo_themselves():
     t = Tables(3, 6, 12)
     t.assign([65, 0, 200])
