@@ -636,7 +636,9 @@ int mla_block_means(const void* kv_cache, int kv_dtype, float kv_scale, int num_
  * for row i of request r, token t = seq_lens[r] - n_r + i, and -inf for the other
  * columns, up to max_blocks_per_req.  Keys are taken at offset 0: a cache with
  * relocated documents is not scored.  Operands are bf16 (q_nope W_UK,h^T and
- * the rotated q_rope rounded once each), sums fp32.  What is not finite in a block
+ * the rotated q_rope rounded once each), products, maxima and sums fp32.  Until
+ * a head's maximum is known s_hj is held in fp16, less the largest of the 32
+ * blocks around it: within 2^-11 of that difference.  What is not finite in a block
  * that a query does not see does not reach its scores; in one that it sees, or in q,
  * it leaves NaN.
  *  q, q_pos, kv_b_proj, seq_lens, cu_q, block_table   as mla_decode.
