@@ -730,6 +730,59 @@ def test_scores_peaked(api, logits):
         s.check(out)
 
 
+def share_bounds(s, x):
+    """(least, largest) share of each block of query x, whatever the scores' size.  s_hj is off by at most e_hj: the operands' roundings as in the file's
+    head, 576 fp32 additions of 2^-23 of the terms' magnitude, the f16's 2^-11 of the distance to a maximum, and 2^-15 of that distance (or of 1) for
+    the rotation and the exponentials.  A share is largest with its own score up by e and the others' down, least the other way round."""
+    r = int(np.searchsorted(s.cu, x, side="right")) - 1
+    b = (int(s.lens[r]) - (int(s.cu[r + 1]) - x)) // 64
+    q, w, m = bf16_values(s.q)[x], bf16_values(s.w)[:, :s.H * 128].reshape(512, s.H, 128), bf16_values(s.means)[s.table[r, :b]]
+    v = np.concatenate([np.einsum("hd,chd->hc", q[:, :128], w), turn(q[:, 128:], angles(int(s.pos[x]), s.theta))], 1)
+    z = s.scale * (v @ m.T)
+    far = z.max(1, keepdims=True) - z
+    e = s.scale * (6 * U_BF16 / math.sqrt(3) * np.sqrt((v ** 2) @ (m ** 2).T) + 576 * 2.0 ** -23 * (np.abs(v) @ np.abs(m).T))
+    e = e + 2.0 ** -11 * (far + e + e.max(1, keepdims=True)) + 2.0 ** -15 * np.maximum(1, far)
+
+    def share(mine, others):
+        d = others[:, None, :] - mine[:, :, None]
+        i = np.arange(b)
+        d[:, i, i] = 0.0
+        with np.errstate(over="ignore"):      # (infinitely less)
+            return (1 / np.exp(d).sum(2)).mean(0)
+    return share(z - e, z + e), share(z + e, z - e)
+
+
+def peaked(logits):
+    return Scores([6000, 9000, 64 * 70 + 1], 1, 16, spread=2.5 * logits / 10, seed=logits)
+
+
+@pytest.mark.parametrize("logits", [300, 3000])
+def test_share_bounds_tell_blocks_apart(logits):
+    """The bounds hold for the reference itself, and not for its shares moved to the next block."""
+    s = peaked(logits)
+    want = s.ref()[0]
+    for x in range(3):
+        lo, hi = share_bounds(s, x)
+        p = want[x, :len(lo)]
+        assert (lo <= p * (1 + 1e-9)).all() and (p <= hi * (1 + 1e-9) + 1e-300).all()
+        moved = np.roll(p, 1)
+        assert (moved < lo).any() and (moved > hi).any()
+        assert lo.sum() > 0.6                 # most heads' largest block is certain
+
+
+@gpu
+@pytest.mark.parametrize("logits", [20, 300, 3000])
+def test_scores_peaked_blocks(api, logits):
+    """Which blocks have the heads' attention, where scores are far apart and most of what leaves the score kernel is -infinite."""
+    s = peaked(logits)
+    out = s.run(api).double().cpu().numpy()
+    for x in range(3):
+        lo, hi = share_bounds(s, x)
+        p = out[x, :len(lo)]
+        # (the heads' sum and its last rounding: 32 of fp32)
+        assert (p >= lo * (1 - 32 * U_FP32) - 2.0 ** -126).all() and (p <= hi * (1 + 32 * U_FP32) + 2.0 ** -126).all()
+
+
 @gpu
 @pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
 @pytest.mark.parametrize("where", [0, 511, 575])
@@ -1041,6 +1094,47 @@ def test_scores_wait_runs_out_and_reports_timeout(api, monkeypatch, lens, cta):
     out = s.run(api, workspace=ws)
     assert api.device_error(ws) == 0
     s.check(out)
+
+
+@gpu
+@pytest.mark.parametrize("lens, cta, spoiled", [([3000, 700], 1, 1), ([64 * 140, 700], 0, 0), ([64 * 140, 700], 1, 0), ([64 * 140, 700], 2, 0), ([64 * 140, 700], 3, 1)])
+def test_scores_wait_runs_out_in_any_cta(api, monkeypatch, lens, cta, spoiled):
+    """As above, with the first, a middle and the last tile of a request withheld: the other request's scores are right."""
+    s = Scores(lens, 1, 16, seed=cta)
+    ws = torch.empty(api.block_scores_workspace_size(2, 16, s.table.shape[1]), dtype=torch.uint8, device="cuda")
+    want, tol = s.ref()
+    part = want.copy()
+    part[spoiled] = np.nan
+    monkeypatch.setenv("MLA_WAIT_LIMIT_US", "2000")
+    monkeypatch.setenv("MLA_TEST_WITHHOLD_SCORES", str(cta))
+    out = s.run(api, workspace=ws)
+    torch.cuda.synchronize()
+    assert api.device_error(ws) == _lib.MLA_ERR_TIMEOUT
+    monkeypatch.delenv("MLA_TEST_WITHHOLD_SCORES")
+    monkeypatch.delenv("MLA_WAIT_LIMIT_US")
+    s.check(out, (part, tol))
+    s.check(s.run(api, workspace=ws), (want, tol))
+    assert api.device_error(ws) == 0
+
+
+@gpu
+@pytest.mark.parametrize("kv", ["bf16", "fp8_e4m3"])
+def test_sparse_wait_runs_out_and_reports_timeout(api, monkeypatch, kv):
+    """The whole call with one CTA's mean rows withheld: it reports, ends, and the next one on the same workspace is right."""
+    t = Topics(api, [3000, 700], 1, 16, kv, 8, 1, 2)
+    d = t.dev()
+    ws = torch.empty(api.decode_sparse_workspace_size(2, 2, 16, t.table.shape[1], 8), dtype=torch.uint8, device="cuda")
+    want = [x.clone() for x in t.run(d, workspace=ws)]
+    for cta in (0, 1):
+        monkeypatch.setenv("MLA_WAIT_LIMIT_US", "2000")
+        monkeypatch.setenv("MLA_TEST_WITHHOLD_SCORES", str(cta))
+        t.run(d, workspace=ws)
+        torch.cuda.synchronize()
+        assert api.device_error(ws) == _lib.MLA_ERR_TIMEOUT
+        monkeypatch.delenv("MLA_TEST_WITHHOLD_SCORES")
+        monkeypatch.delenv("MLA_WAIT_LIMIT_US")
+        out, lse = t.run(d, workspace=ws)
+        assert api.device_error(ws) == 0 and torch.equal(out, want[0]) and torch.equal(lse, want[1])
 
 
 @gpu
