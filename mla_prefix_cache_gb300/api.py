@@ -500,6 +500,11 @@ def decode(q: torch.Tensor, q_pos: torch.Tensor, kv_cache: torch.Tensor, block_t
 
 # ------------------------------------------------------- a sparse decoding step
 
+def _not_32_bits(x: int) -> bool:
+    """Whether the C entries' ints would cut a number to another one; of several joined by | (beside a negative one, which they refuse, it may say no)."""
+    return x >> 31 not in (0, -1)
+
+
 def assign_blocks(block_table: torch.Tensor, held: torch.Tensor, seq_lens: torch.Tensor, free_blocks: torch.Tensor,
                   free_count: torch.Tensor, *, shared: Optional[torch.Tensor] = None,
                   cu_q: Optional[torch.Tensor] = None, slots: Optional[torch.Tensor] = None,
@@ -538,6 +543,8 @@ def block_means(kv_cache: torch.Tensor, block_table: torch.Tensor, seq_lens: tor
     block_table, seq_lens and cu_q.
 
     means bf16 [NB, 576], written at those blocks only.  Returns means."""
+    if _not_32_bits(rows):
+        raise MLAError("mla_block_means", _lib.MLA_ERR_UNSUPPORTED)
     device = _current(kv_cache, "kv_cache")
     B, bt, max_blocks, sl, cq = _batch_args(block_table, seq_lens, cu_q, rows, device)
     st = _lib.load().mla_block_means(
@@ -611,6 +618,8 @@ def select_blocks(scores: torch.Tensor, block_table: torch.Tensor, seq_lens: tor
     seq_lens, cu_q as for decode.  Returns (table int32 [T_q, keep], lens int32
     [T_q]): block_table and seq_lens of decode(q, q_pos, kv_cache, table, lens,
     kv_b_proj, ...), which attends them."""
+    if _not_32_bits(keep | sinks | recent):
+        raise MLAError("mla_select_blocks", _lib.MLA_ERR_UNSUPPORTED)
     device = _current(scores, "scores")
     if scores.dim() != 2 or block_table.dim() != 2 or scores.shape[1] != block_table.shape[1]:
         raise ValueError("scores must be [T_q, max_blocks]")
@@ -633,6 +642,8 @@ def select_blocks(scores: torch.Tensor, block_table: torch.Tensor, seq_lens: tor
 
 
 def decode_sparse_workspace_size(num_reqs: int, total_q: int, num_heads: int, max_blocks: int, keep: int) -> int:
+    if _not_32_bits(keep):
+        raise MLAError("mla_decode_sparse_workspace_size", _lib.MLA_ERR_INVALID_ARG)
     n = _lib.load().mla_decode_sparse_workspace_size(int(num_reqs), int(total_q), int(num_heads), int(max_blocks), int(keep))
     if n == 0:
         raise MLAError("mla_decode_sparse_workspace_size", _lib.MLA_ERR_INVALID_ARG)
@@ -661,8 +672,11 @@ def decode_sparse(q: torch.Tensor, q_pos: torch.Tensor, kv_cache: torch.Tensor, 
     and select_blocks choose (mla_decode_sparse), in one call.
 
     q, q_pos, kv_cache, block_table, seq_lens, cu_q, kv_b_proj, out, lse as for
-    decode; means bf16 [NB, 576] (see block_means).  Returns out [T_q, H, 128],
+    decode; means bf16 [NB, 576] (see block_means).  A keep above max_blocks
+    is the same as max_blocks.  Returns out [T_q, H, 128],
     and lse fp32 [T_q, H] with it when return_lse is set or lse is given."""
+    if _not_32_bits(keep | sinks | recent):
+        raise MLAError("mla_decode_sparse", _lib.MLA_ERR_UNSUPPORTED)
     device = _current(q, "q")
     if q.dim() != 3 or q.shape[2] != 192:
         raise ValueError("q must be [T_q, H, 192]")

@@ -305,6 +305,25 @@ def test_documented_limits_without_gpu(lib):
     assert assign(32, 2 ** 25 - 1, 2 ** 30 - 2 ** 20 + 32) == refused and assign(1, 1, 1, rows=2 ** 31 - 2 ** 20) == refused
 
 
+WIDE = [2 ** 32 + 5, 2 ** 31, -2 ** 31 - 1, 5 - 2 ** 32]      # that the library's ints would cut to 5, and to the other sign
+
+
+@pytest.mark.parametrize("n", WIDE)
+def test_numbers_beyond_32_bits_are_refused_without_gpu(lib, n):
+    """A count that does not fit the library's ints is an error, not another count.  (It is looked at before the tensors, which are not there.)"""
+    from mla_prefix_cache_gb300 import api
+    some = dict(block_table=None, seq_lens=None)
+    for kw in (dict(keep=n), dict(keep=8, sinks=n), dict(keep=8, recent=n)):
+        with pytest.raises(_lib.MLAError):
+            api.select_blocks(None, **some, **kw)
+        with pytest.raises(_lib.MLAError):
+            api.decode_sparse(None, None, None, None, **some, kv_b_proj=None, softmax_scale=0.07, **kw)
+    with pytest.raises(_lib.MLAError):
+        api.block_means(None, **some, means=None, rows=n)
+    with pytest.raises(_lib.MLAError):
+        api.decode_sparse_workspace_size(1, 1, 16, 4, n)
+
+
 def test_reference_tables_undo_themselves():
     t = Tables(3, 6, 12)
     t.assign([65, 0, 200])
