@@ -5,8 +5,9 @@
 // (FP8) read and 1152 written a block.
 //
 // The host does not know how many blocks fill up: request r has the candidates
-// [cu_r / 64 + r, cu_{r+1} / 64 + r + 1), one more than its new rows can fill at
-// least, and those that are none are passed over.  The launch before may be the one
+// [cu_r / 64 + r, cu_{r+1} / 64 + r + 1), at least the ceil(n / 64) blocks that n
+// new rows can fill (floor((c + n) / 64) - floor(c / 64) + 1 is no less for any first
+// row c), and those that are none are passed over.  The launch before may be the one
 // that wrote the block table: what is looked up ahead of the wait for it is looked at
 // again behind it (64 requests, a few blocks filled: 2.9 us, all looked up
 // behind it 3.3).
@@ -15,7 +16,7 @@
 //  - Many: a CTA an SM, whose producer warp looks up 32 candidates at a time and
 //    has blocks copied whole into a ring (three of 72 KB, or five of 40), so that
 //    an SM always has that much in flight; the other warps add up from shared
-//    memory.  65536 rows (960 blocks, 74 MB, 10.8 us at the copy rate): 14.2 us;
+//    memory.  62,818 rows (984 blocks, 74 MB, 10.8 us at the copy rate): 14.2 us;
 //    with a CTA each 17.6, 2.4 waves whose look-ups and sums have nothing in flight.
 #include <atomic>
 
