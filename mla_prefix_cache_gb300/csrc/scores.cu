@@ -18,8 +18,10 @@
 // rows do not depend on the query absorption, so their loads start before it ends.
 //
 // S leaves in f16, less the largest of its 32 blocks, which is kept in fp32 with the
-// sum of 2^(s - maximum): that moves s by 2^-11 of the difference at most,
-// about what the bf16 operands do, and half the bytes go to L2 and back.
+// sum of 2^(s - maximum): that moves s by 2^-11 of the difference at most, and half
+// the bytes go to L2 and back.  Of the fp32 shares' error against 64 bits (32 queries
+// of 2048 blocks, 2.44e-4 of their norm) the bf16 operands alone make 2.43e-4, the
+// f16 alone 2.5e-5.
 #include <atomic>
 
 #include "scores.cuh"
